@@ -271,6 +271,100 @@ ret_status retention_recurrent_step(const void* q, const void* k, const void* v,
                                     float* state, void* y, int B, int H, int dk, int dv, ret_dtype dt,
                                     void* stream);
 
+/*
+ * ---- Around retention in a block: gated recurrence, gated norm, residual norm ----
+ *
+ * The entry points below take their sequence tensors with strides, so that a
+ * tensor may be token-major ([B,T,H,d]) or a slice of a fused projection.
+ * ret_strides holds the distances, in elements, between rows that follow each
+ * other along b, h and t; the elements of a row are contiguous.  A strides
+ * argument is a HOST array with one entry per tensor, in the order its comment
+ * names, read during the call only; NULL means every tensor is contiguous in
+ * the order of its shape.  Strides are >= 0 and
+ * span at most 2^46 elements; rows of a written tensor must not
+ * overlap each other (RET_ERR_INVALID_ARG).  A written tensor may interleave
+ * with other tensors (slices of one buffer) but must share no element with
+ * them.  Any alignment of sequence tensors that is a multiple of their element
+ * is accepted; rows whose pointers, strides and length are multiples of 16
+ * bytes are moved fastest.  fp32 tensors (states, checkpoints, parameters and
+ * their gradients) are contiguous and 16-byte aligned.
+ */
+typedef struct {
+  long long b, h, t;
+} ret_strides;
+
+/*
+ * Gated linear recurrence: retention's recurrence with a decay that depends on
+ * the token and the channel, over a vector state.  Per batch, head and channel
+ *   a_t = sigmoid(f_t)^rate_h,   h_t = a_t h_(t-1) + u_t,   y_t = h_t,
+ *   u_t = x_t (normalize = 0)  or  u_t = (1 - a_t) x_t (normalize = 1),
+ * h_(-1) = state_in.  rate_h > 0 plays the part of retention's per-head decay:
+ * a small one gives its head a long memory.  f_t = -inf gives a_t = 0 (the
+ * token starts a new packed sequence), f_t = +inf gives a_t = 1; e^-|f| below
+ * 2^-126 (|f| > 87.3) counts as 0.  After a NaN, or an infinity in x or in the
+ * state, the later values of that channel are not finite; others are untouched.
+ *   x, f        : [B,H,T,d] in dt.
+ *   rate        : HOST array of H floats, finite and > 0.
+ *   state_in    : nullable (zeros); fp32 [B,H,d].
+ *   state_out   : nullable; receives h_(T-1), fp32 [B,H,d]; may be state_in exactly.
+ *   y           : written, [B,H,T,d] in dt.
+ *   checkpoints : nullable; receives the state before every block of tokens,
+ *                 retention_gated_scan_checkpoint_bytes() bytes, for the backward.
+ *   strides     : x, f, y.
+ *   workspace   : retention_gated_scan_workspace_bytes() bytes (may be NULL
+ *                 when that is 0), 16-byte aligned, owned by the caller,
+ *                 overlapping no other argument; contents ignored on entry.
+ *                 Calls that overlap in time need workspaces of their own.
+ * T = 0 copies state_in (or zeros) to state_out.  Arithmetic, states and
+ * checkpoints are fp32; y is rounded to dt.  Limits: T <= 2^30, every tensor's
+ * element count below 2^31.  Results do not depend on timing: the same call
+ * gives the same bits.
+ */
+ret_status retention_gated_scan_fwd(const void* x, const void* f, const float* rate, const float* state_in,
+                                    float* state_out, void* y, float* checkpoints, const ret_strides* strides,
+                                    int B, int H, int T, int d, int normalize, ret_dtype dt, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Sizes for the call above, pure functions of the sizes ((size_t)-1 for
+ * arguments it would reject). */
+size_t retention_gated_scan_workspace_bytes(int B, int H, int T, int d, ret_dtype dt);
+size_t retention_gated_scan_checkpoint_bytes(int B, int H, int T, int d);
+
+/*
+ * Gradients of retention_gated_scan_fwd for L = sum <grad_y, y> +
+ * <grad_state_out, state_out>.  With g_t = dL/dh_t = grad_y_t + a_(t+1) g_(t+1)
+ * (g_(T-1) also receives grad_state_out):
+ *   grad_x_t = g_t  (normalize: (1 - a_t) g_t),
+ *   grad_f_t = g_t h_(t-1) a_t rate sigmoid(-f_t)  (normalize: h_(t-1) - x_t for h_(t-1)),
+ *   grad_state_in = a_0 g_0  (grad_state_out, or zeros, when T = 0).
+ * rate is a fixed hyperparameter and has no gradient.  grad_f is 0 where f is
+ * infinite and everything else there is finite.
+ *   checkpoints    : nullable; what the forward call of the same x, f, rate,
+ *                    state_in, normalize and sizes wrote.  NULL: the forward
+ *                    recurrence runs again, into the workspace.
+ *   grad_y         : [B,H,T,d] in dt.     grad_state_out : nullable; fp32 [B,H,d].
+ *   grad_x, grad_f : written, [B,H,T,d] in dt.
+ *   grad_state_in  : nullable; written, fp32 [B,H,d]; may be grad_state_out exactly.
+ *   strides        : x, f, grad_y, grad_x, grad_f.
+ *   workspace      : retention_gated_scan_bwd_workspace_bytes() bytes, as above.
+ */
+ret_status retention_gated_scan_bwd(const void* x, const void* f, const float* rate, const float* state_in,
+                                    const float* checkpoints, const void* grad_y, const float* grad_state_out,
+                                    void* grad_x, void* grad_f, float* grad_state_in, const ret_strides* strides,
+                                    int B, int H, int T, int d, int normalize, ret_dtype dt, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+size_t retention_gated_scan_bwd_workspace_bytes(int B, int H, int T, int d, ret_dtype dt, int have_checkpoints);
+
+/*
+ * One decode step of the gated recurrence, in place on the state:
+ * state <- a state + u, y = state.
+ *   x, f : [B,H,d] in dt.   state : in/out, fp32 [B,H,d].   y : written, [B,H,d] in dt.
+ *   strides : x, f, y (t unused).
+ */
+ret_status retention_gated_scan_step(const void* x, const void* f, const float* rate, float* state, void* y,
+                                     const ret_strides* strides, int B, int H, int d, int normalize, ret_dtype dt,
+                                     void* stream);
+
 /* Text of the last error on this host thread ("" after a successful call).
  * Valid until the next libretention call on the same thread. */
 const char* retention_last_error(void);

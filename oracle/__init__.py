@@ -8,3 +8,4 @@ from .retention_oracle import (chunk_state_contribution, chunkwise, group_norm, 
 
 __all__ = ["recurrent", "recurrent_step", "parallel", "chunkwise", "chunk_state_contribution",
            "recurrent_backward", "group_norm"]
+from .block_oracle import gated_scan, gated_scan_backward  # noqa: F401

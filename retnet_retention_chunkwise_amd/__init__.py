@@ -16,8 +16,22 @@ The compute lives in hand-written HIP kernels behind a C ABI
     fused_group_norm_failed(workspace, B, H, T, dk, dv, C, dtype) -> bool
         (whether a wait of that fused call gave up; its error word)
 
+Around retention in a block (strided tensors: any layout with contiguous rows):
+
+    gated_scan_fwd(x, f, rate, state_in=None, state_out=True, normalize=False, checkpoints=None)
+        -> (y, state_out[, checkpoints])   (h_t = sigmoid(f_t)^rate h_(t-1) + u_t)
+    gated_scan_bwd(x, f, rate, grad_y, state_in=None, grad_state_out=None, checkpoints=None, normalize=False)
+        -> (grad_x, grad_f, grad_state_in)
+    gated_scan_step(x, f, rate, state, normalize=False) -> y      (state updated in place)
+
 Build the library with ``python -m retnet_retention_chunkwise_amd.build``.
 """
+from ._block import (  # noqa: F401
+    gated_scan_bwd,
+    gated_scan_checkpoint_shape,
+    gated_scan_fwd,
+    gated_scan_step,
+)
 from ._lib import (  # noqa: F401
     LIB_PATH,
     MAX_CHUNK,

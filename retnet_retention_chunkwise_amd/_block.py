@@ -1,0 +1,198 @@
+"""ctypes binding of the operators around retention in a block: the gated scan
+(and, with it, the checks of strided tensors).
+
+As in _lib, this is argument marshalling only: tensors are checked for device,
+dtype and shape, and their pointers, strides and the current stream of their
+device go through the C ABI.  Sequence tensors may have any strides as long as
+the elements of a row are contiguous (token-major tensors, slices of a fused
+projection).
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple, Union
+
+import torch
+
+from ._lib import RET_BF16, RET_F32, RetentionError, _gamma_array, last_error, load
+
+_DT = {torch.float32: RET_F32, torch.bfloat16: RET_BF16}
+_BAD = ctypes.c_size_t(-1).value
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _dtype(t: torch.Tensor) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
+    return dt
+
+
+def _rows(t: torch.Tensor, shape, like: torch.Tensor, name: str) -> torch.Tensor:
+    """A sequence tensor: shape, dtype and device, and contiguous rows."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device (cuda/HIP) tensor")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the rows (last dimension) of {name} must be contiguous")
+    return t
+
+
+def _f32(t: Optional[torch.Tensor], shape, like: torch.Tensor, name: str) -> Optional[torch.Tensor]:
+    """A state or parameter: contiguous fp32 on the same device."""
+    if t is not None and (t.dtype != torch.float32 or t.shape != shape or t.device != like.device or
+                          not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous float32 {tuple(shape)} on {like.device}")
+    return t
+
+
+def _new_f32(t: Union[torch.Tensor, bool, None], shape, like: torch.Tensor, name: str) -> Optional[torch.Tensor]:
+    """An fp32 output: a tensor to fill, True for a new one, False or None for none."""
+    if t is True:
+        return torch.empty(shape, dtype=torch.float32, device=like.device)
+    if t is None or t is False:
+        return None
+    return _f32(t, torch.Size(shape), like, name)
+
+
+def _strides(*tensors):
+    """ret_strides of [n0,n1,n2,row] tensors in the order of their shape, or NULL when all are contiguous."""
+    if all(t.is_contiguous() for t in tensors):
+        return None
+    return (ctypes.c_longlong * (3 * len(tensors)))(*(s for t in tensors for s in t.stride()[:3]))
+
+
+def _strides_bh(*tensors):
+    """The same for one-token tensors [B,H,row]."""
+    if all(t.is_contiguous() for t in tensors):
+        return None
+    return (ctypes.c_longlong * (3 * len(tensors)))(*(s for t in tensors for s in (t.stride(0), t.stride(1), 0)))
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(t: Optional[torch.Tensor], need: int, like: torch.Tensor):
+    """(tensor, pointer, bytes) of a call's scratch; allocated on the current stream when none is given."""
+    if need == _BAD:
+        raise RetentionError(1, last_error())
+    if t is None:
+        if need == 0:
+            return None, None, 0
+        t = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {like.device}")
+    return t, t.data_ptr(), t.numel() * t.element_size()
+
+
+def _call(fn, device: torch.device, *args) -> None:
+    """fn(*args, stream) with the tensors' device current and on its current stream."""
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        st = fn(*args, _raw_stream(index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
+    if st != 0:
+        raise RetentionError(st, last_error())
+
+
+def _out(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tensor:
+    return torch.empty_like(like) if t is None else _rows(t, like.shape, like, name)
+
+
+def _scan_inputs(x: torch.Tensor, f: torch.Tensor, dims: int):
+    if x.dim() != dims:
+        raise ValueError("expected x and f [B,H,T,d]" if dims == 4 else "expected x and f [B,H,d]")
+    dt = _dtype(x)
+    _rows(x, x.shape, x, "x")
+    _rows(f, x.shape, x, "f")
+    return dt
+
+
+def gated_scan_checkpoint_shape(B: int, H: int, T: int, d: int) -> Tuple[int, int, int, int]:
+    """Shape of the fp32 checkpoints of a [B,H,T,d] call: the state before every block of tokens."""
+    n = int(load().retention_gated_scan_checkpoint_bytes(B, H, T, d))
+    if n == _BAD:
+        raise RetentionError(1, last_error())
+    return B, H, n // (4 * B * H * d), d
+
+
+def gated_scan_fwd(x: torch.Tensor, f: torch.Tensor, rate, state_in: Optional[torch.Tensor] = None,
+                   state_out: Union[torch.Tensor, bool, None] = True, normalize: bool = False,
+                   y: Optional[torch.Tensor] = None, checkpoints: Union[torch.Tensor, bool, None] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Gated linear recurrence on the GPU (retention_gated_scan_fwd):
+    h_t = a_t h_(t-1) + u_t, a_t = sigmoid(f_t)^rate_h, u_t = x_t or (normalize) (1 - a_t) x_t, y_t = h_t.
+
+    x, f [B,H,T,d] (float32 or bfloat16; rows contiguous, any other strides); rate: H exponents > 0 on the
+    host.  state_in: optional fp32 [B,H,d]; state_out: a tensor to fill (may be state_in), True to allocate
+    one, False/None for none.  Returns (y, state_out), and with checkpoints (True, or a tensor of
+    gated_scan_checkpoint_shape) (y, state_out, checkpoints) for gated_scan_bwd.
+    """
+    lib = load()
+    dt = _scan_inputs(x, f, 4)
+    B, H, T, d = x.shape
+    state_in = _f32(state_in, torch.Size((B, H, d)), x, "state_in")
+    state_out = _new_f32(state_out, (B, H, d), x, "state_out")
+    y = _out(y, x, "y")
+    want = checkpoints is not None and checkpoints is not False
+    if want:
+        checkpoints = _new_f32(checkpoints, gated_scan_checkpoint_shape(B, H, T, d), x, "checkpoints")
+    else:
+        checkpoints = None
+    ws, wp, wn = _workspace(workspace, lib.retention_gated_scan_workspace_bytes(B, H, T, d, dt), x)
+    _call(lib.retention_gated_scan_fwd, x.device, x.data_ptr(), f.data_ptr(), _gamma_array(rate, H), _p(state_in),
+          _p(state_out), y.data_ptr(), _p(checkpoints), _strides(x, f, y), B, H, T, d, int(normalize), dt, wp, wn)
+    return (y, state_out, checkpoints) if want else (y, state_out)
+
+
+def gated_scan_bwd(x: torch.Tensor, f: torch.Tensor, rate, grad_y: torch.Tensor,
+                   state_in: Optional[torch.Tensor] = None, grad_state_out: Optional[torch.Tensor] = None,
+                   checkpoints: Optional[torch.Tensor] = None, normalize: bool = False,
+                   grad_state_in: Union[torch.Tensor, bool, None] = True, grad_x: Optional[torch.Tensor] = None,
+                   grad_f: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                   ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """Gradients of gated_scan_fwd (retention_gated_scan_bwd): (grad_x, grad_f, grad_state_in).
+
+    x, f, rate, state_in, normalize: the forward call's.  checkpoints: what that call returned; without them
+    the forward recurrence is run again.  grad_state_in: a tensor to fill (may be grad_state_out), True to
+    allocate one, False/None for none.
+    """
+    lib = load()
+    dt = _scan_inputs(x, f, 4)
+    B, H, T, d = x.shape
+    _rows(grad_y, x.shape, x, "grad_y")
+    vec = torch.Size((B, H, d))
+    state_in = _f32(state_in, vec, x, "state_in")
+    grad_state_out = _f32(grad_state_out, vec, x, "grad_state_out")
+    grad_state_in = _new_f32(grad_state_in, (B, H, d), x, "grad_state_in")
+    if checkpoints is not None:
+        _f32(checkpoints, torch.Size(gated_scan_checkpoint_shape(B, H, T, d)), x, "checkpoints")
+    gx = _out(grad_x, x, "grad_x")
+    gf = _out(grad_f, x, "grad_f")
+    ws, wp, wn = _workspace(workspace,
+                            lib.retention_gated_scan_bwd_workspace_bytes(B, H, T, d, dt, checkpoints is not None), x)
+    _call(lib.retention_gated_scan_bwd, x.device, x.data_ptr(), f.data_ptr(), _gamma_array(rate, H), _p(state_in),
+          _p(checkpoints), grad_y.data_ptr(), _p(grad_state_out), gx.data_ptr(), gf.data_ptr(), _p(grad_state_in),
+          _strides(x, f, grad_y, gx, gf), B, H, T, d, int(normalize), dt, wp, wn)
+    return gx, gf, grad_state_in
+
+
+def gated_scan_step(x: torch.Tensor, f: torch.Tensor, rate, state: torch.Tensor, normalize: bool = False,
+                    y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One decode step of the gated recurrence (retention_gated_scan_step): state <- a state + u in place,
+    returns y = state in the input dtype.  x, f [B,H,d]; state fp32 [B,H,d]."""
+    dt = _scan_inputs(x, f, 3)
+    B, H, d = x.shape
+    if state is None:
+        raise ValueError("state is required")
+    _f32(state, x.shape, x, "state")
+    y = _out(y, x, "y")
+    _call(load().retention_gated_scan_step, x.device, x.data_ptr(), f.data_ptr(), _gamma_array(rate, H),
+          state.data_ptr(), y.data_ptr(), _strides_bh(x, f, y), B, H, d, int(normalize), dt)
+    return y

@@ -23,6 +23,7 @@ MAX_DK, MAX_DV, MAX_CHUNK = 256, 512, 128
 
 # (name, restype, argtypes) of every symbol include/libretention.h declares
 _vp, _fp, _i, _sz = ctypes.c_void_p, ctypes.POINTER(ctypes.c_float), ctypes.c_int, ctypes.c_size_t
+_sp = ctypes.POINTER(ctypes.c_longlong)  # ret_strides: three per tensor
 SIGNATURES = {
     "retention_parallel_fwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     "retention_chunkwise_fwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
@@ -37,6 +38,13 @@ SIGNATURES = {
     "retention_chunkwise_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                                      _i, _vp, _sz, _vp]),
     "retention_chunkwise_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "retention_gated_scan_fwd": (_i, [_vp, _vp, _fp, _vp, _vp, _vp, _vp, _sp, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "retention_gated_scan_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "retention_gated_scan_checkpoint_bytes": (_sz, [_i, _i, _i, _i]),
+    "retention_gated_scan_bwd": (_i, [_vp, _vp, _fp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sp, _i, _i, _i, _i, _i, _i,
+                                      _vp, _sz, _vp]),
+    "retention_gated_scan_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "retention_gated_scan_step": (_i, [_vp, _vp, _fp, _vp, _vp, _sp, _i, _i, _i, _i, _i, _vp]),
     "retention_last_error": (ctypes.c_char_p, []),
     "retention_version": (_i, []),
 }

@@ -36,6 +36,8 @@ SOURCES = [
     "short_mfma.hip",
     "noalloc.hip",
     "short_bf16.hip",
+    "gated_scan.hip",
+    "block_api.cpp",
 ]
 
 ARCH = "gfx950"

@@ -4,6 +4,9 @@
 
 #include <hip/hip_runtime_api.h>
 #include <stddef.h>
+#include <stdint.h>
+
+#include <initializer_list>
 
 namespace ret {
 
@@ -152,6 +155,61 @@ hipError_t launch_chunkwise_f32_bwd(const BwdArgs& a, int B, int H, int T, int d
 // Per-head GroupNorm of a [B,H,T,dv] output (dt: 0 = fp32, 1 = bf16); out may be y.
 hipError_t launch_group_norm(const void* y, const float* weight, const float* bias, float eps, void* out, int B,
                              int H, int T, int dv, int dt, hipStream_t s);
+
+// Strides in elements of the rows (b, h, t) of a sequence tensor; the elements
+// of a row are contiguous.
+struct Strides3 {
+  long b, h, t;
+};
+
+// The widest access (in elements, a power of two up to most) that the row
+// length, every pointer and every stride allow (es: element size in bytes).
+inline int widest_access(int d, int most, int es, std::initializer_list<const void*> ptrs,
+                         std::initializer_list<Strides3> strides) {
+  auto fits = [&](int v) {
+    if (d % v != 0) return false;
+    for (const void* q : ptrs)
+      if (reinterpret_cast<uintptr_t>(q) % (static_cast<uintptr_t>(v) * es) != 0) return false;
+    for (const Strides3& s : strides)
+      if (s.b % v != 0 || s.h % v != 0 || s.t % v != 0) return false;
+    return true;
+  };
+  int v = most;
+  while (v > 1 && !fits(v)) v >>= 1;
+  return v;
+}
+
+// Gated linear recurrence (gated_scan.hip).  Head groups carry the heads'
+// decay exponents in their gamma field.  dt: 0 = fp32, 1 = bf16.
+struct GatedScanFwd {
+  const void* x;
+  const void* f;
+  const float* state_in;  // nullable
+  float* state_out;       // nullable; may be state_in
+  void* y;                // nullable: only checkpoints and state
+  float* checkpoints;     // nullable: [B, H, ceil(T / block), d], the state before every block of tokens
+  Strides3 sx, sf, sy;
+  int B, H, T, d;
+  bool normalize;
+  int dt;
+};
+struct GatedScanBwd {
+  const void* x;
+  const void* f;
+  const float* checkpoints;
+  const void* grad_y;
+  const float* grad_state_out;  // nullable
+  void* grad_x;
+  void* grad_f;
+  float* grad_state_in;  // nullable; may be grad_state_out
+  Strides3 sx, sf, sgy, sgx, sgf;
+  int B, H, T, d;
+  bool normalize;
+  int dt;
+};
+int gated_scan_block(int d);  // tokens per checkpoint
+hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s);
+hipError_t launch_gated_scan_bwd(const GatedScanBwd& p, const HeadGroup& g, hipStream_t s);
 
 // The same on fp32 MFMA for 1 <= T <= kShortMfmaMaxT (dk % 16 == 0, dv % 64 == 0).
 constexpr int kShortMfmaMaxT = 32;
