@@ -365,6 +365,82 @@ ret_status retention_gated_scan_step(const void* x, const void* f, const float* 
                                      const ret_strides* strides, int B, int H, int d, int normalize, ret_dtype dt,
                                      void* stream);
 
+/*
+ * Per-head GroupNorm of a mixer's output followed by its gate, with the heads
+ * merged: what a retention layer does between the operator and its output
+ * projection.  For each (b, h, t), over c = 0..dv-1,
+ *   n[c] = (y[c] - mu) / sqrt(var + eps) * weight[h][c] + bias[h][c]  (as retention_group_norm),
+ *   out[c] = n[c] * gate[c] * sigmoid(gate[c])   (out = n when gate is NULL).
+ *   y         : [B,H,T,dv] in dt (the layout the forwards write).
+ *   gate, out : [B,T,H,dv] in dt, i.e. token rows of H*dv channels, as a
+ *               projection takes them.  gate is nullable.  out is written.
+ *   weight, bias : nullable (ones, zeros); device fp32 [H,dv].
+ *   eps       : finite, >= 0.
+ *   strides   : y, gate, out.
+ * dv <= RET_MAX_DV.  Arithmetic is fp32; out is rounded once.  An infinite
+ * gate gives NaN where the formula does (gate = -inf: -inf * 0).
+ */
+ret_status retention_group_norm_gated(const void* y, const void* gate, const float* weight, const float* bias,
+                                      float eps, void* out, const ret_strides* strides, int B, int H, int T, int dv,
+                                      ret_dtype dt, void* stream);
+
+/*
+ * Gradients of retention_group_norm_gated (and, without a gate, of
+ * retention_group_norm) for L = sum <grad_out, out>.
+ *   grad_out    : [B,T,H,dv] in dt.
+ *   grad_y      : written, [B,H,T,dv] in dt.
+ *   grad_gate   : written, [B,T,H,dv] in dt; NULL exactly when gate is NULL.
+ *   grad_weight, grad_bias : nullable; written, fp32 [H,dv] (sums over b and t
+ *                 in a fixed order).
+ *   strides     : y, gate, grad_out, grad_y, grad_gate.
+ *   workspace   : retention_group_norm_gated_bwd_workspace_bytes() bytes when
+ *                 grad_weight or grad_bias is given (else may be NULL), 16-byte
+ *                 aligned, overlapping no other argument, contents ignored.
+ */
+ret_status retention_group_norm_gated_bwd(const void* y, const void* gate, const float* weight, const float* bias,
+                                          float eps, const void* grad_out, void* grad_y, void* grad_gate,
+                                          float* grad_weight, float* grad_bias, const ret_strides* strides, int B,
+                                          int H, int T, int dv, ret_dtype dt, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+size_t retention_group_norm_gated_bwd_workspace_bytes(int B, int H, int T, int dv);
+
+/*
+ * The residual stream after a block and the normalised input of the next one:
+ *   r = alpha x + scale[c] f,   n = norm(r) * weight[c] + bias[c]
+ * over rows of D channels; norm is LayerNorm (rms = 0) or RMSNorm (rms = 1)
+ * with eps inside the root, of r as it is stored (rounded to dt).
+ *   x, f   : [rows,D] in dt: the stream and the block's output.
+ *   weight, bias, scale : nullable (ones, zeros, ones); device fp32 [D].
+ *   alpha  : finite; the weight of the residual.     eps : finite, >= 0.
+ *   r, n   : written, [rows,D] in dt.
+ *   row_strides : HOST array of the distances between rows, in elements, of
+ *            x, f, r, n; NULL: D.  The rules of ret_strides hold.
+ * 1 <= D <= 16384, rows * D < 2^31.  Arithmetic is fp32.
+ */
+ret_status retention_residual_norm(const void* x, const void* f, const float* weight, const float* bias,
+                                   const float* scale, float alpha, float eps, int rms, void* r, void* n,
+                                   const long long* row_strides, int rows, int D, ret_dtype dt, void* stream);
+
+/*
+ * Gradients of retention_residual_norm for L = sum <grad_n, n> + <grad_r, r>,
+ * from the stored r:
+ *   g = grad_r + d norm(r)^T (grad_n * weight),  grad_x = alpha g,  grad_f = scale g,
+ *   grad_weight = sum grad_n norm(r),  grad_bias = sum grad_n,  grad_scale = sum g f.
+ *   grad_r         : nullable (zeros).     f : read only when grad_scale is given.
+ *   grad_x, grad_f : nullable; written, [rows,D] in dt.
+ *   grad_weight, grad_bias, grad_scale : nullable; written, fp32 [D] (sums over
+ *                    the rows in a fixed order).
+ *   row_strides    : r, grad_n, grad_r, f, grad_x, grad_f.
+ *   workspace      : retention_residual_norm_bwd_workspace_bytes() bytes when a
+ *                    parameter gradient is given, as above.
+ */
+ret_status retention_residual_norm_bwd(const void* r, const void* grad_n, const void* grad_r, const void* f,
+                                       const float* weight, const float* scale, float alpha, float eps, int rms,
+                                       void* grad_x, void* grad_f, float* grad_weight, float* grad_bias,
+                                       float* grad_scale, const long long* row_strides, int rows, int D,
+                                       ret_dtype dt, void* workspace, size_t workspace_bytes, void* stream);
+size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D);
+
 /* Text of the last error on this host thread ("" after a successful call).
  * Valid until the next libretention call on the same thread. */
 const char* retention_last_error(void);

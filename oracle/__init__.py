@@ -8,4 +8,5 @@ from .retention_oracle import (chunk_state_contribution, chunkwise, group_norm, 
 
 __all__ = ["recurrent", "recurrent_step", "parallel", "chunkwise", "chunk_state_contribution",
            "recurrent_backward", "group_norm"]
-from .block_oracle import gated_scan, gated_scan_backward  # noqa: F401
+from .block_oracle import (gated_scan, gated_scan_backward, group_norm_gated, group_norm_gated_backward,  # noqa: F401
+                           residual, residual_norm_backward, stream_norm)

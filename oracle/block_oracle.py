@@ -56,3 +56,71 @@ def gated_scan_backward(x, f, rate, grad_y, state_in=None, grad_state_out=None, 
         gf[:, :, t] = da * a * r * torch.sigmoid(-f[:, :, t])
         later = a * g
     return gx, gf, later
+
+
+# ----------------------------------------------------------- gated GroupNorm
+def _normalised(y: torch.Tensor, eps: float, center: bool):
+    mu = y.mean(-1, keepdim=True) if center else torch.zeros_like(y[..., :1])
+    rstd = 1.0 / torch.sqrt(((y - mu) ** 2).mean(-1, keepdim=True) + eps)
+    return (y - mu) * rstd, rstd
+
+
+def _norm_backward(xh, rstd, p, center: bool):
+    """d/dy of sum <p, xh(y)>."""
+    t = p - xh * (p * xh).mean(-1, keepdim=True)
+    if center:
+        t = t - p.mean(-1, keepdim=True)
+    return rstd * t
+
+
+def group_norm_gated(y, gate=None, weight=None, bias=None, eps: float = 1e-5) -> torch.Tensor:
+    """Per-head GroupNorm of y [B,H,T,dv] times gate sigmoid(gate), gate and result [B,T,H,dv]."""
+    y, z, w, b = _up(y), _up(gate), _up(weight), _up(bias)
+    n, _ = _normalised(y, eps, True)
+    n = n if w is None else n * w[:, None]
+    n = (n if b is None else n + b[:, None]).transpose(1, 2)
+    return n if z is None else n * z * torch.sigmoid(z)
+
+
+def group_norm_gated_backward(y, gate, grad_out, weight=None, bias=None, eps: float = 1e-5):
+    """(grad_y, grad_gate, grad_weight, grad_bias); grad_gate None without a gate."""
+    y, z, do, w, b = _up(y), _up(gate), _up(grad_out), _up(weight), _up(bias)
+    xh, rstd = _normalised(y, eps, True)
+    n = xh if w is None else xh * w[:, None]
+    n = n if b is None else n + b[:, None]
+    dz = None
+    dn = do.transpose(1, 2)
+    if z is not None:
+        zt = z.transpose(1, 2)
+        s = torch.sigmoid(zt)
+        dz = (dn * n * (s + zt * s * (1 - s))).transpose(1, 2)
+        dn = dn * zt * s
+    p = dn if w is None else dn * w[:, None]
+    return _norm_backward(xh, rstd, p, True), dz, (dn * xh).sum((0, 2)), dn.sum((0, 2))
+
+
+# ------------------------------------------------------------- residual norm
+def residual(x, f, scale=None, alpha: float = 1.0) -> torch.Tensor:
+    """The stream alpha x + scale f before it is rounded to its type."""
+    x, f, s = _up(x), _up(f), _up(scale)
+    return alpha * x + (f if s is None else s * f)
+
+
+def stream_norm(r, weight=None, bias=None, eps: float = 1e-5, rms: bool = False) -> torch.Tensor:
+    """LayerNorm or RMSNorm of the stored stream r over its last dimension."""
+    n, _ = _normalised(_up(r), eps, not rms)
+    w, b = _up(weight), _up(bias)
+    n = n if w is None else n * w
+    return n if b is None else n + b
+
+
+def residual_norm_backward(r, grad_n, grad_r=None, weight=None, f=None, scale=None, alpha: float = 1.0,
+                           eps: float = 1e-5, rms: bool = False):
+    """(grad_x, grad_f, grad_weight, grad_bias, grad_scale) from the stored r."""
+    r, dn, dr, w, f, s = _up(r), _up(grad_n), _up(grad_r), _up(weight), _up(f), _up(scale)
+    xh, rstd = _normalised(r, eps, not rms)
+    g = _norm_backward(xh, rstd, dn if w is None else dn * w, not rms)
+    g = g if dr is None else g + dr
+    rows = tuple(range(r.dim() - 1))
+    gs = None if s is None or f is None else (g * f).sum(rows)
+    return alpha * g, g if s is None else s * g, (dn * xh).sum(rows), dn.sum(rows), gs

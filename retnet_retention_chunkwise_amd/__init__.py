@@ -23,6 +23,14 @@ Around retention in a block (strided tensors: any layout with contiguous rows):
     gated_scan_bwd(x, f, rate, grad_y, state_in=None, grad_state_out=None, checkpoints=None, normalize=False)
         -> (grad_x, grad_f, grad_state_in)
     gated_scan_step(x, f, rate, state, normalize=False) -> y      (state updated in place)
+    group_norm_gated(y, gate=None, weight=None, bias=None, eps=1e-5) -> out
+        (per-head GroupNorm of y [B,H,T,dv] times silu(gate), gate and out [B,T,H,dv])
+    group_norm_gated_bwd(y, gate, grad_out, weight=None, bias=None, eps=1e-5)
+        -> (grad_y, grad_gate, grad_weight, grad_bias)      (gate=None: of group_norm)
+    residual_norm(x, f, weight=None, bias=None, scale=None, alpha=1.0, eps=1e-5, rms=False) -> (r, n)
+        (r = alpha x + scale f, n = LayerNorm or RMSNorm of r)
+    residual_norm_bwd(r, grad_n, grad_r=None, weight=None, f=None, scale=None, ...)
+        -> (grad_x, grad_f, grad_weight, grad_bias, grad_scale)
 
 Build the library with ``python -m retnet_retention_chunkwise_amd.build``.
 """
@@ -31,6 +39,10 @@ from ._block import (  # noqa: F401
     gated_scan_checkpoint_shape,
     gated_scan_fwd,
     gated_scan_step,
+    group_norm_gated,
+    group_norm_gated_bwd,
+    residual_norm,
+    residual_norm_bwd,
 )
 from ._lib import (  # noqa: F401
     LIB_PATH,

@@ -1,5 +1,5 @@
-"""ctypes binding of the operators around retention in a block: the gated scan
-(and, with it, the checks of strided tensors).
+"""ctypes binding of the operators around retention in a block: the gated scan,
+the gated per-head GroupNorm and the residual norm.
 
 As in _lib, this is argument marshalling only: tensors are checked for device,
 dtype and shape, and their pointers, strides and the current stream of their
@@ -196,3 +196,166 @@ def gated_scan_step(x: torch.Tensor, f: torch.Tensor, rate, state: torch.Tensor,
     _call(load().retention_gated_scan_step, x.device, x.data_ptr(), f.data_ptr(), _gamma_array(rate, H),
           state.data_ptr(), y.data_ptr(), _strides_bh(x, f, y), B, H, d, int(normalize), dt)
     return y
+
+
+# ----------------------------------------------------------- gated GroupNorm
+def _gate_norm_inputs(y, gate, weight, bias):
+    if y.dim() != 4:
+        raise ValueError("expected y [B,H,T,dv]")
+    dt = _dtype(y)
+    _rows(y, y.shape, y, "y")
+    B, H, T, dv = y.shape
+    token = torch.Size((B, T, H, dv))
+    if gate is not None:
+        _rows(gate, token, y, "gate")
+    _f32(weight, torch.Size((H, dv)), y, "weight")
+    _f32(bias, torch.Size((H, dv)), y, "bias")
+    return dt, B, H, T, dv, token
+
+
+def _pack(*rows):
+    return (ctypes.c_longlong * (3 * len(rows)))(*(s for r in rows for s in r))
+
+
+def _head(t):
+    return (t.stride(0), t.stride(1), t.stride(2))
+
+
+def _token(t):
+    return (0, 0, 0) if t is None else (t.stride(0), t.stride(2), t.stride(1))
+
+
+def group_norm_gated(y: torch.Tensor, gate: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                     bias: Optional[torch.Tensor] = None, eps: float = 1e-5, out: Optional[torch.Tensor] = None
+                     ) -> torch.Tensor:
+    """Per-head GroupNorm of y [B,H,T,dv] times silu(gate), heads merged (retention_group_norm_gated).
+
+    gate, out: [B,T,H,dv], any strides with contiguous rows (a [B,T,H*dv] projection viewed by heads, or a
+    slice of a fused one); without a gate the norm alone.  weight, bias: optional fp32 [H,dv].
+    """
+    dt, B, H, T, dv, token = _gate_norm_inputs(y, gate, weight, bias)
+    out = torch.empty(token, dtype=y.dtype, device=y.device) if out is None else _rows(out, token, y, "out")
+    plain = y.is_contiguous() and out.is_contiguous() and (gate is None or gate.is_contiguous())
+    _call(load().retention_group_norm_gated, y.device, y.data_ptr(), _p(gate), _p(weight), _p(bias), float(eps),
+          out.data_ptr(), None if plain else _pack(_head(y), _token(gate), _token(out)), B, H, T, dv, dt)
+    return out
+
+
+def group_norm_gated_bwd(y: torch.Tensor, gate: Optional[torch.Tensor], grad_out: torch.Tensor,
+                         weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                         eps: float = 1e-5, param_grads: bool = True, grad_y: Optional[torch.Tensor] = None,
+                         grad_gate: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                         ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor],
+                                    Optional[torch.Tensor]]:
+    """Gradients of group_norm_gated (retention_group_norm_gated_bwd): (grad_y, grad_gate, grad_weight, grad_bias).
+
+    With gate None the gradients of group_norm, for a token-major grad_out.  grad_weight and grad_bias (fp32)
+    are None where the parameter is, or with param_grads=False.
+    """
+    lib = load()
+    dt, B, H, T, dv, token = _gate_norm_inputs(y, gate, weight, bias)
+    _rows(grad_out, token, y, "grad_out")
+    gy = torch.empty(y.shape, dtype=y.dtype, device=y.device) if grad_y is None else _rows(grad_y, y.shape, y, "grad_y")
+    if gate is None:
+        gz = None
+    else:
+        gz = torch.empty(token, dtype=y.dtype, device=y.device) if grad_gate is None else _rows(grad_gate, token, y,
+                                                                                              "grad_gate")
+    gw = torch.empty_like(weight) if param_grads and weight is not None else None
+    gb = torch.empty_like(bias) if param_grads and bias is not None else None
+    need = lib.retention_group_norm_gated_bwd_workspace_bytes(B, H, T, dv) if gw is not None or gb is not None else 0
+    ws, wp, wn = _workspace(workspace, need, y)
+    plain = all(t is None or t.is_contiguous() for t in (y, gate, grad_out, gy, gz))
+    _call(lib.retention_group_norm_gated_bwd, y.device, y.data_ptr(), _p(gate), _p(weight), _p(bias), float(eps),
+          grad_out.data_ptr(), gy.data_ptr(), _p(gz), _p(gw), _p(gb),
+          None if plain else _pack(_head(y), _token(gate), _token(grad_out), _head(gy), _token(gz)), B, H, T, dv, dt,
+          wp, wn)
+    return gy, gz, gw, gb
+
+
+# ------------------------------------------------------------- residual norm
+def _row_stride(t: Optional[torch.Tensor], name: str) -> int:
+    """Distance between the rows of a [...,D] tensor whose leading dimensions walk evenly."""
+    if t is None:
+        return 0
+    if t.is_contiguous():
+        return t.shape[-1]
+    try:
+        return t.view(-1, t.shape[-1]).stride(0)
+    except RuntimeError:
+        raise ValueError(f"the rows of {name} must be evenly spaced") from None
+
+
+def _row_strides(**tensors):
+    if all(t is None or t.is_contiguous() for t in tensors.values()):
+        return None
+    return (ctypes.c_longlong * len(tensors))(*(_row_stride(t, n) for n, t in tensors.items()))
+
+
+def _count(t: torch.Tensor) -> Tuple[int, int]:
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError("expected tensors [...,D] with D >= 1")
+    return t.numel() // t.shape[-1], t.shape[-1]
+
+
+def residual_norm(x: torch.Tensor, f: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                  bias: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                  eps: float = 1e-5, rms: bool = False, r: Optional[torch.Tensor] = None,
+                  n: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """r = alpha x + scale f and n = norm(r) weight + bias (retention_residual_norm): (r, n).
+
+    x, f [...,D]: the residual stream and a block's output; weight, bias, scale: optional fp32 [D];
+    LayerNorm, or RMSNorm with rms=True.
+    """
+    dt = _dtype(x)
+    rows, D = _count(x)
+    _rows(x, x.shape, x, "x")
+    _rows(f, x.shape, x, "f")
+    for t, name in ((weight, "weight"), (bias, "bias"), (scale, "scale")):
+        _f32(t, torch.Size((D,)), x, name)
+    r = torch.empty(x.shape, dtype=x.dtype, device=x.device) if r is None else _rows(r, x.shape, x, "r")
+    n = torch.empty(x.shape, dtype=x.dtype, device=x.device) if n is None else _rows(n, x.shape, x, "n")
+    _call(load().retention_residual_norm, x.device, x.data_ptr(), f.data_ptr(), _p(weight), _p(bias), _p(scale),
+          float(alpha), float(eps), int(rms), r.data_ptr(), n.data_ptr(), _row_strides(x=x, f=f, r=r, n=n), rows, D, dt)
+    return r, n
+
+
+def residual_norm_bwd(r: torch.Tensor, grad_n: torch.Tensor, grad_r: Optional[torch.Tensor] = None,
+                      weight: Optional[torch.Tensor] = None, f: Optional[torch.Tensor] = None,
+                      scale: Optional[torch.Tensor] = None, alpha: float = 1.0, eps: float = 1e-5, rms: bool = False,
+                      bias_grad: bool = False, param_grads: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Gradients of residual_norm from its stored r (retention_residual_norm_bwd):
+    (grad_x, grad_f, grad_weight, grad_bias, grad_scale).
+
+    grad_r: what reaches r from later in the stream (None: nothing).  f is needed for grad_scale only.
+    grad_weight and grad_scale are None where the parameter is (or with param_grads=False), grad_bias without
+    bias_grad.  With alpha = 1 and no scale the gradients of x and f are equal and grad_f is grad_x itself.
+    """
+    lib = load()
+    dt = _dtype(r)
+    rows, D = _count(r)
+    _rows(r, r.shape, r, "r")
+    _rows(grad_n, r.shape, r, "grad_n")
+    for t, name in ((grad_r, "grad_r"), (f, "f")):
+        if t is not None:
+            _rows(t, r.shape, r, name)
+    for t, name in ((weight, "weight"), (scale, "scale")):
+        _f32(t, torch.Size((D,)), r, name)
+    want_scale = param_grads and scale is not None
+    if want_scale and f is None:
+        raise ValueError("f is required for the gradient of scale")
+    gx = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+    same = alpha == 1.0 and scale is None
+    gf = None if same else torch.empty_like(gx)
+    gw = torch.empty_like(weight) if param_grads and weight is not None else None
+    gb = torch.empty(D, dtype=torch.float32, device=r.device) if param_grads and bias_grad else None
+    gs = torch.empty_like(scale) if want_scale else None
+    need = 0
+    if gw is not None or gb is not None or gs is not None:
+        need = lib.retention_residual_norm_bwd_workspace_bytes(rows, D)
+    ws, wp, wn = _workspace(workspace, need, r)
+    ff = f if want_scale else None
+    _call(lib.retention_residual_norm_bwd, r.device, r.data_ptr(), grad_n.data_ptr(), _p(grad_r), _p(ff), _p(weight),
+          _p(scale), float(alpha), float(eps), int(rms), gx.data_ptr(), _p(gf), _p(gw), _p(gb), _p(gs),
+          _row_strides(r=r, grad_n=grad_n, grad_r=grad_r, f=ff, grad_x=gx, grad_f=gf), rows, D, dt, wp, wn)
+    return gx, (gx if same else gf), gw, gb, gs

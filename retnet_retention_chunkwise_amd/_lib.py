@@ -45,6 +45,15 @@ SIGNATURES = {
                                       _vp, _sz, _vp]),
     "retention_gated_scan_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "retention_gated_scan_step": (_i, [_vp, _vp, _fp, _vp, _vp, _sp, _i, _i, _i, _i, _i, _vp]),
+    "retention_group_norm_gated": (_i, [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _sp, _i, _i, _i, _i, _i, _vp]),
+    "retention_group_norm_gated_bwd": (_i, [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _sp, _i, _i,
+                                            _i, _i, _i, _vp, _sz, _vp]),
+    "retention_group_norm_gated_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "retention_residual_norm": (_i, [_vp, _vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _i, _vp, _vp, _sp, _i,
+                                     _i, _i, _vp]),
+    "retention_residual_norm_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _i, _vp, _vp,
+                                         _vp, _vp, _vp, _sp, _i, _i, _i, _vp, _sz, _vp]),
+    "retention_residual_norm_bwd_workspace_bytes": (_sz, [_i, _i]),
     "retention_last_error": (ctypes.c_char_p, []),
     "retention_version": (_i, []),
 }

@@ -37,6 +37,9 @@ SOURCES = [
     "noalloc.hip",
     "short_bf16.hip",
     "gated_scan.hip",
+    "group_norm_gated.hip",
+    "residual_norm.hip",
+    "column_sums.hip",
     "block_api.cpp",
 ]
 

@@ -84,23 +84,35 @@ Strides3 given(const ret_strides* s, int i, const Strides3& otherwise) {
 }
 
 // Whether two non-empty tensors share a byte.  Extents that meet may still be
-// disjoint when the tensors are slices of one buffer: every row of either then
-// starts at a multiple of the strides' common divisor g from the tensor's
-// start, and the two rows' places within g bytes do not meet.
+// disjoint when the tensors are slices of one buffer: dimensions that continue
+// a row (a stride of the row's length, as merged heads have) are taken into
+// it; every row of either tensor then starts a multiple of the remaining
+// strides' common divisor g from the tensor's start, and the tensors are
+// disjoint if the rows' places within g bytes do not meet.
 bool shares(const Arg& a, const Arg& b) {
   if (a.empty() || b.empty()) return false;
   if (!(a.lo() < b.hi() && b.lo() < a.hi())) return false;
-  unsigned long long g = 0;
-  for (const Arg* t : {&a, &b}) {
-    const long st[3] = {t->s.b, t->s.h, t->s.t};
+  unsigned long long g = 0, len[2];
+  const Arg* both[2] = {&a, &b};
+  for (int k = 0; k < 2; ++k) {
+    const Arg& t = *both[k];
+    const long long st[3] = {t.s.b, t.s.h, t.s.t};
+    bool open[3] = {t.n[0] > 1, t.n[1] > 1, t.n[2] > 1};
+    long long row = t.len;
+    for (int pass = 0; pass < 3; ++pass)
+      for (int i = 0; i < 3; ++i)
+        if (open[i] && st[i] == row) {
+          row *= t.n[i];
+          open[i] = false;
+        }
     for (int i = 0; i < 3; ++i)
-      if (t->n[i] > 1) g = std::gcd(g, static_cast<unsigned long long>(st[i]) * t->es);
+      if (open[i]) g = std::gcd(g, static_cast<unsigned long long>(st[i]) * t.es);
+    len[k] = static_cast<unsigned long long>(row) * t.es;
   }
-  const unsigned long long la = a.len * a.es, lb = b.len * b.es;
-  if (g == 0 || la + lb > g) return true;
+  if (g == 0 || len[0] + len[1] > g) return true;
   const unsigned long long ra = a.lo() % g, rb = b.lo() % g;
-  // [ra, ra + la) and [rb, rb + lb) on a circle of g bytes
-  return (rb + g - ra) % g < la || (ra + g - rb) % g < lb;
+  // [ra, ra + len a) and [rb, rb + len b) on a circle of g bytes
+  return (rb + g - ra) % g < len[0] || (ra + g - rb) % g < len[1];
 }
 
 // Whether the rows of a written tensor are disjoint: dimensions taken by
@@ -170,11 +182,34 @@ ret_status check_sizes(const char* fn, int B, int H, int T, int d, ret_dtype dt)
   return RET_OK;
 }
 
+ret_status check_eps(const char* fn, float eps) {
+  if (!std::isfinite(eps) || eps < 0.0f)
+    return fail(RET_ERR_INVALID_ARG, "%s: eps=%g must be finite and >= 0", fn, static_cast<double>(eps));
+  return RET_OK;
+}
+
 ret_status check_rates(const char* fn, const float* rate, int H) {
   if (rate == nullptr) return fail(RET_ERR_INVALID_ARG, "%s: rate (host array of H floats) is null", fn);
   for (int h = 0; h < H; ++h)
     if (!std::isfinite(rate[h]) || rate[h] <= 0.0f)
       return fail(RET_ERR_INVALID_ARG, "%s: rate[%d] = %g is not finite and > 0", fn, h, static_cast<double>(rate[h]));
+  return RET_OK;
+}
+
+Arg rows_arg(const char* name, const void* p, bool written, int rows, int D, long stride, ret_dtype dt) {
+  return seq(name, p, written, 1, 1, rows, D, Strides3{0, 0, stride}, dt);
+}
+
+ret_status check_rows(const char* fn, int rows, int D, float alpha, ret_dtype dt) {
+  if (rows < 0) return fail(RET_ERR_INVALID_ARG, "%s: rows=%d must be >= 0", fn, rows);
+  if (D < 1) return fail(RET_ERR_INVALID_ARG, "%s: D=%d must be >= 1", fn, D);
+  if (dt != RET_F32 && dt != RET_BF16)
+    return fail(RET_ERR_UNSUPPORTED, "%s: dtype %d is not RET_F32 or RET_BF16", fn, static_cast<int>(dt));
+  if (D > ret::kResidualMaxD) return fail(RET_ERR_UNSUPPORTED, "%s: D=%d exceeds %d", fn, D, ret::kResidualMaxD);
+  if (static_cast<long long>(rows) * D > kMaxElems)
+    return fail(RET_ERR_UNSUPPORTED, "%s: a tensor has 2^31 or more elements", fn);
+  if (!std::isfinite(alpha))
+    return fail(RET_ERR_INVALID_ARG, "%s: alpha=%g must be finite", fn, static_cast<double>(alpha));
   return RET_OK;
 }
 
@@ -309,6 +344,141 @@ ret_status retention_gated_scan_step(const void* x, const void* f, const float* 
                             dt == RET_BF16 ? 1 : 0};
   hipStream_t s = static_cast<hipStream_t>(stream);
   return for_head_groups(fn, H, rate, [&](const ret::HeadGroup& g) { return ret::launch_gated_scan_fwd(p, g, s); });
+}
+
+ret_status retention_group_norm_gated(const void* y, const void* gate, const float* weight, const float* bias,
+                                      float eps, void* out, const ret_strides* strides, int B, int H, int T, int dv,
+                                      ret_dtype dt, void* stream) {
+  const char* fn = "retention_group_norm_gated";
+  ret_status st = check_sizes(fn, B, H, T, dv, dt);
+  if (st == RET_OK) st = check_eps(fn, eps);
+  if (st != RET_OK) return st;
+  if (dv > RET_MAX_DV) return fail(RET_ERR_UNSUPPORTED, "%s: dv=%d exceeds %d", fn, dv, RET_MAX_DV);
+  const Strides3 sy = given(strides, 0, contiguous_bhtd(H, T, dv)), sz = given(strides, 1, contiguous_bthd(H, T, dv)),
+                 so = given(strides, 2, contiguous_bthd(H, T, dv));
+  const long long np = static_cast<long long>(H) * dv;
+  Arg g = seq("gate", gate, false, B, H, T, dv, sz, dt);
+  g.required = false;
+  st = check_args(fn, {seq("y", y, false, B, H, T, dv, sy, dt), g, seq("out", out, true, B, H, T, dv, so, dt),
+                       flat("weight", weight, false, false, np), flat("bias", bias, false, false, np)});
+  if (st != RET_OK) return st;
+  if (T == 0) return ok();
+  const ret::GateNormFwd a{y, gate, weight, bias, eps, out, sy, gate != nullptr ? sz : so, so, B, H, T, dv,
+                           dt == RET_BF16 ? 1 : 0};
+  return done(fn, ret::launch_gate_norm_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t retention_group_norm_gated_bwd_workspace_bytes(int B, int H, int T, int dv) {
+  const char* fn = "retention_group_norm_gated_bwd_workspace_bytes";
+  if (check_sizes(fn, B, H, T, dv, RET_F32) != RET_OK) return kBad;
+  if (dv > RET_MAX_DV) return kBad;
+  return T == 0 ? 0 : static_cast<size_t>(2) * ret::gate_norm_bwd_slabs(B, H, T, dv) * H * dv * 4;
+}
+
+ret_status retention_group_norm_gated_bwd(const void* y, const void* gate, const float* weight, const float* bias,
+                                          float eps, const void* grad_out, void* grad_y, void* grad_gate,
+                                          float* grad_weight, float* grad_bias, const ret_strides* strides, int B,
+                                          int H, int T, int dv, ret_dtype dt, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  const char* fn = "retention_group_norm_gated_bwd";
+  ret_status st = check_sizes(fn, B, H, T, dv, dt);
+  if (st == RET_OK) st = check_eps(fn, eps);
+  if (st != RET_OK) return st;
+  if (dv > RET_MAX_DV) return fail(RET_ERR_UNSUPPORTED, "%s: dv=%d exceeds %d", fn, dv, RET_MAX_DV);
+  if ((gate == nullptr) != (grad_gate == nullptr) && T > 0)
+    return fail(RET_ERR_INVALID_ARG, "%s: gate and grad_gate are given together or not at all", fn);
+  const Strides3 head = contiguous_bhtd(H, T, dv), token = contiguous_bthd(H, T, dv);
+  const Strides3 sy = given(strides, 0, head), sz = given(strides, 1, token), sdo = given(strides, 2, token),
+                 sdy = given(strides, 3, head), sdz = given(strides, 4, token);
+  const long long np = static_cast<long long>(H) * dv;
+  const bool want = grad_weight != nullptr || grad_bias != nullptr;
+  const size_t need = want ? retention_group_norm_gated_bwd_workspace_bytes(B, H, T, dv) : 0;
+  Arg g = seq("gate", gate, false, B, H, T, dv, sz, dt), gg = seq("grad_gate", grad_gate, true, B, H, T, dv, sdz, dt);
+  g.required = gg.required = false;
+  st = check_args(
+      fn, {seq("y", y, false, B, H, T, dv, sy, dt), g, seq("grad_out", grad_out, false, B, H, T, dv, sdo, dt),
+           seq("grad_y", grad_y, true, B, H, T, dv, sdy, dt), gg, flat("weight", weight, false, false, np),
+           flat("bias", bias, false, false, np), flat("grad_weight", grad_weight, true, false, np),
+           flat("grad_bias", grad_bias, true, false, np),
+           flat("workspace", need ? workspace : nullptr, true, false, (need + 3) / 4)});
+  if (st == RET_OK) st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != RET_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (T == 0) {  // no rows: the parameter gradients are empty sums
+    for (float* p : {grad_weight, grad_bias}) {
+      if (p == nullptr) continue;
+      const hipError_t e = ret::launch_fill_u32(p, np, 0, s);
+      if (e != hipSuccess) return done(fn, e);
+    }
+    return ok();
+  }
+  const ret::GateNormBwd a{y,         gate,        weight,    bias, eps, grad_out,
+                           grad_y,    grad_gate,   grad_weight, grad_bias,
+                           sy,        gate != nullptr ? sz : sdo, sdo, sdy, gate != nullptr ? sdz : sdo,
+                           B,         H,           T,         dv,   dt == RET_BF16 ? 1 : 0};
+  return done(fn, ret::launch_gate_norm_bwd(a, want ? static_cast<float*>(workspace) : nullptr, s));
+}
+
+ret_status retention_residual_norm(const void* x, const void* f, const float* weight, const float* bias,
+                                   const float* scale, float alpha, float eps, int rms, void* r, void* n,
+                                   const long long* row_strides, int rows, int D, ret_dtype dt, void* stream) {
+  const char* fn = "retention_residual_norm";
+  ret_status st = check_rows(fn, rows, D, alpha, dt);
+  if (st == RET_OK) st = check_eps(fn, eps);
+  if (st != RET_OK) return st;
+  auto s = [&](int i) { return row_strides == nullptr ? static_cast<long>(D) : static_cast<long>(row_strides[i]); };
+  st = check_args(fn, {rows_arg("x", x, false, rows, D, s(0), dt), rows_arg("f", f, false, rows, D, s(1), dt),
+                       rows_arg("r", r, true, rows, D, s(2), dt), rows_arg("n", n, true, rows, D, s(3), dt),
+                       flat("weight", weight, false, false, D), flat("bias", bias, false, false, D),
+                       flat("scale", scale, false, false, D)});
+  if (st != RET_OK) return st;
+  if (rows == 0) return ok();
+  const ret::ResidualNormFwd a{x, f, weight, bias, scale, alpha, eps, rms != 0, r, n, s(0), s(1), s(2), s(3),
+                               rows, D, dt == RET_BF16 ? 1 : 0};
+  return done(fn, ret::launch_residual_norm_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D) {
+  if (check_rows("retention_residual_norm_bwd_workspace_bytes", rows, D, 1.0f, RET_F32) != RET_OK) return kBad;
+  return rows == 0 ? 0 : static_cast<size_t>(3) * ret::residual_norm_bwd_blocks(rows, D) * D * 4;
+}
+
+ret_status retention_residual_norm_bwd(const void* r, const void* grad_n, const void* grad_r, const void* f,
+                                       const float* weight, const float* scale, float alpha, float eps, int rms,
+                                       void* grad_x, void* grad_f, float* grad_weight, float* grad_bias,
+                                       float* grad_scale, const long long* row_strides, int rows, int D, ret_dtype dt,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "retention_residual_norm_bwd";
+  ret_status st = check_rows(fn, rows, D, alpha, dt);
+  if (st == RET_OK) st = check_eps(fn, eps);
+  if (st != RET_OK) return st;
+  auto s = [&](int i) { return row_strides == nullptr ? static_cast<long>(D) : static_cast<long>(row_strides[i]); };
+  const bool want = grad_weight != nullptr || grad_bias != nullptr || grad_scale != nullptr;
+  const size_t need = want ? retention_residual_norm_bwd_workspace_bytes(rows, D) : 0;
+  Arg gr = rows_arg("grad_r", grad_r, false, rows, D, s(2), dt), ff = rows_arg("f", f, false, rows, D, s(3), dt);
+  Arg gx = rows_arg("grad_x", grad_x, true, rows, D, s(4), dt), gf = rows_arg("grad_f", grad_f, true, rows, D, s(5), dt);
+  gr.required = gx.required = gf.required = false;
+  ff.required = grad_scale != nullptr;
+  st = check_args(fn, {rows_arg("r", r, false, rows, D, s(0), dt), rows_arg("grad_n", grad_n, false, rows, D, s(1), dt),
+                       gr, ff, gx, gf, flat("weight", weight, false, false, D), flat("scale", scale, false, false, D),
+                       flat("grad_weight", grad_weight, true, false, D), flat("grad_bias", grad_bias, true, false, D),
+                       flat("grad_scale", grad_scale, true, false, D),
+                       flat("workspace", need ? workspace : nullptr, true, false, (need + 3) / 4)});
+  if (st == RET_OK) st = check_workspace(fn, workspace, workspace_bytes, need);
+  if (st != RET_OK) return st;
+  hipStream_t q = static_cast<hipStream_t>(stream);
+  if (rows == 0) {  // no rows: the parameter gradients are empty sums
+    for (float* p : {grad_weight, grad_bias, grad_scale}) {
+      if (p == nullptr) continue;
+      const hipError_t e = ret::launch_fill_u32(p, D, 0, q);
+      if (e != hipSuccess) return done(fn, e);
+    }
+    return ok();
+  }
+  const ret::ResidualNormBwd a{r, grad_n, grad_r, f, weight, scale, alpha, eps, rms != 0, grad_x, grad_f, grad_weight,
+                               grad_bias, grad_scale, s(0), s(1), s(2), s(3), s(4), s(5), rows, D,
+                               dt == RET_BF16 ? 1 : 0};
+  return done(fn, ret::launch_residual_norm_bwd(a, want ? static_cast<float*>(workspace) : nullptr, q));
 }
 
 }  // extern "C"

@@ -19,6 +19,10 @@
 #include "kernels.h"
 #include "vec_io.h"
 
+// Fused multiply-adds only where they are written: which products the compiler
+// joins would differ between the instances of a kernel, and so would their bits.
+#pragma clang fp contract(off)
+
 namespace ret {
 namespace {
 

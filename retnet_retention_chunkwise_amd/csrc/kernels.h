@@ -211,6 +211,86 @@ int gated_scan_block(int d);  // tokens per checkpoint
 hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s);
 hipError_t launch_gated_scan_bwd(const GatedScanBwd& p, const HeadGroup& g, hipStream_t s);
 
+// out[k][c] = sum over r of partial[k][r][c] for k < 3 (null outputs skipped),
+// partial [3][rows][n].
+struct ColumnSums {
+  const float* partial;
+  int rows;
+  long n;
+  float* out[3];
+};
+hipError_t launch_column_sums(const ColumnSums& a, hipStream_t s);
+
+// Per-head GroupNorm followed by a gate (group_norm_gated.hip), dv <= 512.
+struct GateNormFwd {
+  const void* y;
+  const void* gate;     // nullable: no gate
+  const float* weight;  // [H, dv] or null
+  const float* bias;    // [H, dv] or null
+  float eps;
+  void* out;
+  Strides3 sy, sz, so;
+  int B, H, T, dv, dt;
+};
+struct GateNormBwd {
+  const void* y;
+  const void* gate;
+  const float* weight;
+  const float* bias;
+  float eps;
+  const void* grad_out;
+  void* grad_y;
+  void* grad_gate;     // null without a gate
+  float* grad_weight;  // nullable
+  float* grad_bias;    // nullable
+  Strides3 sy, sz, sdo, sdy, sdz;
+  int B, H, T, dv, dt;
+};
+hipError_t launch_gate_norm_fwd(const GateNormFwd& a, hipStream_t s);
+// partial: 2 * slabs * H * dv floats when a parameter gradient is wanted, else null.
+int gate_norm_bwd_slabs(int B, int H, int T, int dv);
+hipError_t launch_gate_norm_bwd(const GateNormBwd& a, float* partial, hipStream_t s);
+
+// Residual stream and norm (residual_norm.hip), D <= kResidualMaxD; row strides
+// in elements.
+constexpr int kResidualMaxD = 16384;
+struct ResidualNormFwd {
+  const void* x;
+  const void* f;
+  const float* weight;  // [D] or null
+  const float* bias;    // [D] or null
+  const float* scale;   // [D] or null
+  float alpha, eps;
+  bool rms;
+  void* r;
+  void* n;
+  long sx, sf, sr, sn;
+  long rows;
+  int D, dt;
+};
+struct ResidualNormBwd {
+  const void* r;
+  const void* grad_n;
+  const void* grad_r;   // nullable
+  const void* f;        // read for grad_scale only
+  const float* weight;
+  const float* scale;
+  float alpha, eps;
+  bool rms;
+  void* grad_x;         // nullable
+  void* grad_f;         // nullable
+  float* grad_weight;   // nullable
+  float* grad_bias;     // nullable
+  float* grad_scale;    // nullable
+  long sr, sgn, sgr, sf, sgx, sgf;
+  long rows;
+  int D, dt;
+};
+hipError_t launch_residual_norm_fwd(const ResidualNormFwd& a, hipStream_t s);
+// partial: 3 * blocks * D floats when a parameter gradient is wanted, else null.
+int residual_norm_bwd_blocks(long rows, int D);
+hipError_t launch_residual_norm_bwd(const ResidualNormBwd& a, float* partial, hipStream_t s);
+
 // The same on fp32 MFMA for 1 <= T <= kShortMfmaMaxT (dk % 16 == 0, dv % 64 == 0).
 constexpr int kShortMfmaMaxT = 32;
 constexpr int kShortMfmaMinT = 1;  // below this the VALU streaming kernel is used

@@ -94,3 +94,61 @@ def test_scan_planted_slips_fail():
     no_rate = oracle.gated_scan_backward(x, f, [1.0], dy, normalize=True)[1]
     for slip in (plain, no_rate, -gf, gf.flip(2)):
         assert not torch.allclose(slip, want, atol=1e-4)
+
+
+# ----------------------------------------------------------- gated GroupNorm
+def test_gate_norm_against_library_routines():
+    B, H, T, dv = 2, 3, 4, 6
+    y, z, w, b = _rand(B, H, T, dv, seed=20), _rand(B, T, H, dv, seed=21), _rand(H, dv, seed=22), _rand(H, dv, seed=23)
+    merged = y.transpose(1, 2).reshape(B * T, H * dv)
+    n = torch.nn.functional.group_norm(merged, H, w.reshape(-1), b.reshape(-1), 1e-3).view(B, T, H, dv)
+    assert torch.allclose(oracle.group_norm_gated(y, None, w, b, 1e-3), n, atol=1e-12)
+    assert torch.allclose(oracle.group_norm_gated(y, z, w, b, 1e-3), n * torch.nn.functional.silu(z), atol=1e-12)
+    # without a gate and transposed back it is the plain per-head norm
+    assert torch.allclose(oracle.group_norm_gated(y, None, w, b, 1e-3).transpose(1, 2), oracle.group_norm(y, w, b, 1e-3))
+
+
+def test_gate_norm_hand_values():
+    # y = 1, 3: mu = 2, variance 1, xh = -1, 1; silu(0) = 0, silu(ln 3) = 0.75 ln 3
+    y = torch.tensor([1.0, 3.0], dtype=F64).view(1, 1, 1, 2)
+    z = torch.tensor([0.0, math.log(3.0)], dtype=F64).view(1, 1, 1, 2)
+    got = oracle.group_norm_gated(y, z, torch.tensor([[2.0, 2.0]]), torch.tensor([[1.0, 1.0]]), 0.0)
+    assert torch.allclose(got.view(-1), torch.tensor([0.0, 3.0 * 0.75 * math.log(3.0)], dtype=F64))
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_gate_norm_gradients_match_differences(gated):
+    B, H, T, dv = 2, 2, 2, 5
+    y, z = _rand(B, H, T, dv, seed=24), _rand(B, T, H, dv, seed=25) if gated else None
+    w, b, do = _rand(H, dv, seed=26), _rand(H, dv, seed=27), _rand(B, T, H, dv, seed=28)
+    loss = lambda: float((oracle.group_norm_gated(y, z, w, b, 1e-2) * do).sum())  # noqa: E731
+    gy, gz, gw, gb = oracle.group_norm_gated_backward(y, z, do, w, b, 1e-2)
+    for g, t in ((gy, y), (gz, z), (gw, w), (gb, b)):
+        if t is not None:
+            assert torch.allclose(g, differences(loss, t), atol=1e-7)
+
+
+# ------------------------------------------------------------- residual norm
+def test_stream_norm_against_library_routines():
+    r, w, b = _rand(7, 9, seed=30), _rand(9, seed=31), _rand(9, seed=32)
+    assert torch.allclose(oracle.stream_norm(r, w, b, 1e-3), torch.nn.functional.layer_norm(r, (9,), w, b, 1e-3))
+    assert torch.allclose(oracle.stream_norm(r, w, None, 1e-3, True), torch.nn.functional.rms_norm(r, (9,), w, 1e-3))
+    x = torch.tensor([2.0, -4.0], dtype=F64)
+    assert torch.equal(oracle.residual(x, x, torch.tensor([1.0, 0.5]), 3.0), torch.tensor([8.0, -14.0], dtype=F64))
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_residual_norm_gradients_match_differences(rms):
+    R, D, alpha = 3, 5, 1.5
+    x, f, w, b, s = _rand(R, D, seed=33), _rand(R, D, seed=34), _rand(D, seed=35), _rand(D, seed=36), _rand(D, seed=37)
+    dn, dr = _rand(R, D, seed=38), _rand(R, D, seed=39)
+
+    def loss():
+        r = oracle.residual(x, f, s, alpha)
+        return float((oracle.stream_norm(r, w, b, 1e-2, rms) * dn).sum() + (r * dr).sum())
+
+    got = oracle.residual_norm_backward(oracle.residual(x, f, s, alpha), dn, dr, w, f, s, alpha, 1e-2, rms)
+    for g, t in zip(got, (x, f, w, b, s)):
+        assert torch.allclose(g, differences(loss, t), atol=1e-7)
+    slip = oracle.residual_norm_backward(oracle.residual(x, f, s, alpha), dn, dr, w, f, s, alpha, 1e-2, not rms)
+    assert not torch.allclose(slip[0], differences(loss, x), atol=1e-3)
