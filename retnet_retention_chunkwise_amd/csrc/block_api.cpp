@@ -234,13 +234,16 @@ long long checkpoint_floats(int B, int H, int T, int d) {
   return static_cast<long long>(B) * H * ((T + static_cast<long long>(block) - 1) / block) * d;
 }
 
+// Bytes that n bytes of checkpoints take in front of the chain's scratch.
+size_t own_offset(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
 }  // namespace
 
 extern "C" {
 
 size_t retention_gated_scan_workspace_bytes(int B, int H, int T, int d, ret_dtype dt) {
   if (check_sizes("retention_gated_scan_workspace_bytes", B, H, T, d, dt) != RET_OK) return kBad;
-  return 0;
+  return ret::gated_scan_chain_bytes(B, H, T, d);
 }
 
 size_t retention_gated_scan_checkpoint_bytes(int B, int H, int T, int d) {
@@ -250,7 +253,8 @@ size_t retention_gated_scan_checkpoint_bytes(int B, int H, int T, int d) {
 
 size_t retention_gated_scan_bwd_workspace_bytes(int B, int H, int T, int d, ret_dtype dt, int have_checkpoints) {
   if (check_sizes("retention_gated_scan_bwd_workspace_bytes", B, H, T, d, dt) != RET_OK) return kBad;
-  return have_checkpoints ? 0 : static_cast<size_t>(checkpoint_floats(B, H, T, d)) * 4;
+  const size_t kept = have_checkpoints ? 0 : static_cast<size_t>(checkpoint_floats(B, H, T, d)) * 4;
+  return own_offset(kept) + ret::gated_scan_chain_bytes(B, H, T, d);
 }
 
 ret_status retention_gated_scan_fwd(const void* x, const void* f, const float* rate, const float* state_in,
@@ -279,7 +283,7 @@ ret_status retention_gated_scan_fwd(const void* x, const void* f, const float* r
     return state_out == nullptr || state_out == state_in ? ok() : done(fn, ret::launch_state_copy(state_in, state_out, ns, s));
   const ret::GatedScanFwd p{x, f, state_in, state_out, y, checkpoints, sx, sf, sy, B, H, T, d, normalize != 0,
                             dt == RET_BF16 ? 1 : 0};
-  return for_head_groups(fn, H, rate, [&](const ret::HeadGroup& g) { return ret::launch_gated_scan_fwd(p, g, s); });
+  return for_head_groups(fn, H, rate, [&](const ret::HeadGroup& g) { return ret::launch_gated_scan_fwd(p, workspace, g, s); });
 }
 
 ret_status retention_gated_scan_bwd(const void* x, const void* f, const float* rate, const float* state_in,
@@ -314,15 +318,17 @@ ret_status retention_gated_scan_bwd(const void* x, const void* f, const float* r
                : done(fn, ret::launch_state_copy(grad_state_out, grad_state_in, ns, s));
   const int dti = dt == RET_BF16 ? 1 : 0;
   float* own = static_cast<float*>(workspace);
+  void* chain = static_cast<char*>(workspace) +
+                (checkpoints != nullptr ? 0 : own_offset(static_cast<size_t>(checkpoint_floats(B, H, T, d)) * 4));
   const ret::GatedScanFwd again{x, f, state_in, nullptr, nullptr, own, sx, sf, sx, B, H, T, d, normalize != 0, dti};
   const ret::GatedScanBwd p{x, f, checkpoints != nullptr ? checkpoints : own, grad_y, grad_state_out, grad_x, grad_f,
                             grad_state_in, sx, sf, sgy, sgx, sgf, B, H, T, d, normalize != 0, dti};
   return for_head_groups(fn, H, rate, [&](const ret::HeadGroup& g) {
     if (checkpoints == nullptr) {
-      const hipError_t e = ret::launch_gated_scan_fwd(again, g, s);
+      const hipError_t e = ret::launch_gated_scan_fwd(again, chain, g, s);
       if (e != hipSuccess) return e;
     }
-    return ret::launch_gated_scan_bwd(p, g, s);
+    return ret::launch_gated_scan_bwd(p, chain, g, s);
   });
 }
 
@@ -343,7 +349,7 @@ ret_status retention_gated_scan_step(const void* x, const void* f, const float* 
   const ret::GatedScanFwd p{x, f, state, state, y, nullptr, sx, sf, sy, B, H, 1, d, normalize != 0,
                             dt == RET_BF16 ? 1 : 0};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return for_head_groups(fn, H, rate, [&](const ret::HeadGroup& g) { return ret::launch_gated_scan_fwd(p, g, s); });
+  return for_head_groups(fn, H, rate, [&](const ret::HeadGroup& g) { return ret::launch_gated_scan_fwd(p, nullptr, g, s); });
 }
 
 ret_status retention_group_norm_gated(const void* y, const void* gate, const float* weight, const float* bias,

@@ -29,6 +29,13 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kPerThread = 16;  // VEC * S
+// Channel runs from which on each is walked by one workgroup.  Measured at 256
+// runs (one for each compute unit): walking 50 us and chaining 68 us (B4 H8
+// T2048 d512, bf16), 515 and 665 us (B2 H16 T8192 d512 forward and backward);
+// at 64 runs 1445 and 462 us (B1 H8 T65536 d512 forward).
+constexpr int kWalkTiles = 256;
+
+typedef unsigned long long u64;
 
 struct HeadRate {
   float r[kHeadsPerLaunch];
@@ -82,45 +89,128 @@ __device__ __forceinline__ ScanTile decode_tile(int tile, int nct, int nh, int h
   return s;
 }
 
+// ---- Chaining tiles that run in different workgroups ----
+//
+// With few channels and many tokens the tiles of one channel run must work at
+// the same time, each on its own tokens, and still hand their state on.  A
+// workgroup takes a ticket; tickets go through the tiles of step 0 of the walk
+// (the first tokens, or the last ones backwards), then step 1, ...  It
+// publishes its tile's map (A, H), takes the value that enters its group of
+// kGroup steps and folds the maps of the group's earlier steps into it; the
+// last step of a group publishes the value that enters the next group.  The
+// order of all additions is fixed by the sizes, so results do not depend on
+// timing.  A workgroup waits only for lower tickets, whose workgroups already
+// run, so every wait ends; a wait of more than kSpinLimit polls (two calls on
+// one workspace at the same time, which the interface forbids) gives NaN
+// instead of hanging.  Published words carry their own "ready": the workspace
+// is filled with ones before the launch and no published NaN has that pattern.
+constexpr int kGroup = 16;
+constexpr int kSpinLimit = 1 << 20;
+constexpr size_t kChainHead = 256;  // the ticket counter
+struct Chain {
+  unsigned* ticket;
+  u64* maps;        // [steps][tiles][CW]: A in the low word, H in the high word
+  unsigned* enter;  // [groups][tiles][CW]: the value that enters a group
+  int steps, tiles;
+};
+
+__device__ __forceinline__ unsigned quiet(float x) { return x != x ? 0x7fc00000u : __float_as_uint(x); }
+
+template <typename W>
+__device__ __forceinline__ W wait_word(const W* p, W seen, W otherwise) {
+  for (int n = 0; seen == static_cast<W>(~static_cast<W>(0)); ++n) {
+    if (n == kSpinLimit) return otherwise;
+    __builtin_amdgcn_s_sleep(1);
+    seen = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  return seen;
+}
+
+// The value that enters the tile at step j, for the lane's channel; (A, H) is
+// the tile's map and first the value that enters step 0.
+template <int CW>
+__device__ __forceinline__ float chain(const Chain& c, int j, int tile, int lane, float A, float H, float first) {
+  const long per = static_cast<long>(c.tiles) * CW, at = static_cast<long>(tile) * CW + lane;
+  const int k = j % kGroup, g = j / kGroup;
+  const bool last = j == c.steps - 1;
+  if (k != kGroup - 1 && !last)
+    __hip_atomic_store(c.maps + j * per + at, static_cast<u64>(quiet(H)) << 32 | quiet(A), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+  const unsigned* enter = c.enter + g * per + at;
+  unsigned e = 0;
+  u64 m[kGroup - 1];
+  if (g > 0) e = __hip_atomic_load(enter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const u64* maps = c.maps + static_cast<long>(g) * kGroup * per + at;
+#pragma unroll
+  for (int i = 0; i < kGroup - 1; ++i)
+    if (i < k) m[i] = __hip_atomic_load(maps + i * per, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  float v = g > 0 ? __uint_as_float(wait_word(enter, e, 0x7fc00000u)) : first;
+#pragma unroll
+  for (int i = 0; i < kGroup - 1; ++i)
+    if (i < k) {
+      const u64 r = wait_word(maps + i * per, m[i], static_cast<u64>(0x7fc000007fc00000ull));
+      v = fmaf(__uint_as_float(static_cast<unsigned>(r)), v, __uint_as_float(static_cast<unsigned>(r >> 32)));
+    }
+  if (k == kGroup - 1 && !last)
+    __hip_atomic_store(c.enter + (g + 1) * per + at, quiet(fmaf(A, v, H)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return v;
+}
+
+// The workgroup's ticket; every thread gets it (a barrier inside).
+__device__ __forceinline__ unsigned take_ticket(unsigned* counter, unsigned* shared) {
+  if (threadIdx.x == 0) *shared = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return *shared;
+}
+
+// Where a thread stands in its tile.
+template <int VEC, int CW>
+struct Place {
+  static constexpr int S = kPerThread / VEC, LC = CW / VEC, TG = 64 / LC, NSEG = kWaves * TG, TT = NSEG * S;
+  int lane, wave, lc, seg;
+  __device__ Place()
+      : lane(threadIdx.x & 63), wave(threadIdx.x >> 6), lc((threadIdx.x & 63) % LC),
+        seg((threadIdx.x >> 6) * TG + (threadIdx.x & 63) / LC) {}
+};
+
+template <typename E>
+__device__ __forceinline__ E* at_row(const void* p, const Strides3& s, const ScanTile& t, int c) {
+  return const_cast<E*>(static_cast<const E*>(p)) + t.b * s.b + t.h * s.h + c;
+}
+
+// ---- Forward ----
 template <typename E, int VEC, int CW, bool kNorm>
-__global__ __launch_bounds__(kThreads) void gated_scan_fwd_kernel(GatedScanFwd p, HeadRate rates, int h0, int nh,
-                                                                  int nct) {
-  constexpr int S = kPerThread / VEC, LC = CW / VEC, TG = 64 / LC, NSEG = kWaves * TG, TT = NSEG * S;
+struct FwdThread {
+  using P = Place<VEC, CW>;
   using IO = VecIO<E, VEC>;
-  __shared__ float segA[2][NSEG][CW];
-  __shared__ float segH[2][NSEG][CW];
-
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int lc = lane % LC, seg = w * TG + lane / LC;
-  const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
-  const int c = tl.c0 + lc * VEC;
-  const bool active = c < p.d;
-  const int cc = active ? c : 0;
-  const E* xp = static_cast<const E*>(p.x) + tl.b * p.sx.b + tl.h * p.sx.h + cc;
-  const E* fp = static_cast<const E*>(p.f) + tl.b * p.sf.b + tl.h * p.sf.h + cc;
-  E* yp = static_cast<E*>(p.y) + tl.b * p.sy.b + tl.h * p.sy.h + cc;
-  const float rate = rates.r[tl.hl];
-  // the composing wave: one channel per lane
-  const int ch = tl.c0 + lane;
-  const bool mine = w == 0 && lane < CW;
-  const bool kept = mine && ch < p.d;
-  const long row = (static_cast<long>(tl.b) * p.H + tl.h) * p.d + ch;
-  float carry = kept && p.state_in != nullptr ? p.state_in[row] : 0.0f;
-  const int nchunk = (p.T + TT - 1) / TT;
-
+  static constexpr int S = P::S;
+  const E *xp, *fp;
+  E* yp;
+  long sx, sf, sy;
+  float rate;
+  int T, seg;
+  bool store;
   typename IO::Raw rx[S], rf[S];
-  auto load = [&](int chunk) __attribute__((always_inline)) {
+  float x[S][VEC], cm[S][VEC];
+
+  __device__ __forceinline__ FwdThread(const GatedScanFwd& p, const ScanTile& t, const P& pl, float r)
+      : sx(p.sx.t), sf(p.sf.t), sy(p.sy.t), rate(r), T(p.T), seg(pl.seg) {
+    const int c = t.c0 + pl.lc * VEC, cc = c < p.d ? c : 0;  // lanes past the row's end read its start, store nothing
+    xp = at_row<E>(p.x, p.sx, t, cc);
+    fp = at_row<E>(p.f, p.sf, t, cc);
+    yp = at_row<E>(p.y, p.sy, t, cc);
+    store = c < p.d && p.y != nullptr;
+  }
+  __device__ __forceinline__ void load(int chunk) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const long t = min(chunk * TT + seg * S + s, p.T - 1);  // a row past the end: the last one, masked below
-      rx[s] = IO::load(xp + t * p.sx.t);
-      rf[s] = IO::load(fp + t * p.sf.t);
+      const long t = min(chunk * P::TT + seg * S + s, T - 1);  // a token past the end: the last one, masked below
+      rx[s] = IO::load(xp + t * sx);
+      rf[s] = IO::load(fp + t * sf);
     }
-  };
-  load(0);
-  for (int chunk = 0; chunk < nchunk; ++chunk) {
-    float x[S][VEC], cm[S][VEC];
-    const int t0 = chunk * TT + seg * S;
+  }
+  __device__ __forceinline__ void unpack(int chunk) {
+    const int t0 = chunk * P::TT + seg * S;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       float f[VEC], t;
@@ -128,13 +218,16 @@ __global__ __launch_bounds__(kThreads) void gated_scan_fwd_kernel(GatedScanFwd p
       IO::unpack(rf[s], f);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        cm[s][e] = t0 + s < p.T ? decay_complement<E>(f[e], rate, &t) : 0.0f;
-        x[s][e] = t0 + s < p.T ? x[s][e] : 0.0f;
+        cm[s][e] = t0 + s < T ? decay_complement<E>(f[e], rate, &t) : 0.0f;
+        x[s][e] = t0 + s < T ? x[s][e] : 0.0f;
       }
     }
-    if (chunk + 1 < nchunk) load(chunk + 1);
-    const int q = chunk & 1;
-    float A[VEC], H[VEC];
+  }
+  __device__ __forceinline__ static float step(float c, float x, float h) {
+    return kNorm ? fmaf(c, x - h, h) : fmaf(-c, h, h) + x;
+  }
+  // the map of the thread's tokens
+  __device__ __forceinline__ void map(float (&A)[VEC], float (&H)[VEC]) const {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       A[e] = 1.0f;
@@ -142,90 +235,172 @@ __global__ __launch_bounds__(kThreads) void gated_scan_fwd_kernel(GatedScanFwd p
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         A[e] = fmaf(-cm[s][e], A[e], A[e]);
-        H[e] = kNorm ? fmaf(cm[s][e], x[s][e] - H[e], H[e]) : fmaf(-cm[s][e], H[e], H[e]) + x[s][e];
+        H[e] = step(cm[s][e], x[s][e], H[e]);
       }
-      segA[q][seg][lc * VEC + e] = A[e];
-      segH[q][seg][lc * VEC + e] = H[e];
+    }
+  }
+  // the thread's tokens from their incoming value
+  __device__ __forceinline__ void replay(int chunk, float (&h)[VEC]) const {
+    const int t0 = chunk * P::TT + seg * S;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) h[e] = step(cm[s][e], x[s][e], h[e]);
+      if (store && t0 + s < T) IO::store(yp + (t0 + s) * sy, h);
+    }
+  }
+};
+
+// One workgroup walks the tiles of a channel run from the first token on.
+template <typename E, int VEC, int CW, bool kNorm>
+__global__ __launch_bounds__(kThreads) void gated_scan_fwd_walk_kernel(GatedScanFwd p, HeadRate rates, int h0, int nh,
+                                                                       int nct) {
+  using P = Place<VEC, CW>;
+  __shared__ float segA[2][P::NSEG][CW];
+  __shared__ float segH[2][P::NSEG][CW];
+  const P pl;
+  const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
+  FwdThread<E, VEC, CW, kNorm> th(p, tl, pl, rates.r[tl.hl]);
+  // the composing wave: one channel per lane
+  const int ch = tl.c0 + pl.lane;
+  const bool mine = pl.wave == 0 && pl.lane < CW, kept = mine && ch < p.d;
+  const long bh = static_cast<long>(tl.b) * p.H + tl.h;
+  float carry = kept && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
+  const int nchunk = (p.T + P::TT - 1) / P::TT;
+  th.load(0);
+  for (int chunk = 0; chunk < nchunk; ++chunk) {
+    th.unpack(chunk);
+    if (chunk + 1 < nchunk) th.load(chunk + 1);
+    const int q = chunk & 1;
+    float A[VEC], H[VEC];
+    th.map(A, H);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      segA[q][pl.seg][pl.lc * VEC + e] = A[e];
+      segH[q][pl.seg][pl.lc * VEC + e] = H[e];
     }
     __syncthreads();
     if (mine) {
-      if (kept && p.checkpoints != nullptr)
-        p.checkpoints[((static_cast<long>(tl.b) * p.H + tl.h) * nchunk + chunk) * p.d + ch] = carry;
+      if (kept && p.checkpoints != nullptr) p.checkpoints[(bh * nchunk + chunk) * p.d + ch] = carry;
 #pragma unroll 8
-      for (int i = 0; i < NSEG; ++i) {
-        const float a = segA[q][i][lane], hh = segH[q][i][lane];
-        segH[q][i][lane] = carry;
+      for (int i = 0; i < P::NSEG; ++i) {
+        const float a = segA[q][i][pl.lane], hh = segH[q][i][pl.lane];
+        segH[q][i][pl.lane] = carry;
         carry = fmaf(a, carry, hh);
       }
     }
     __syncthreads();
-    float hcur[VEC];
+    float h[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) hcur[e] = segH[q][seg][lc * VEC + e];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        hcur[e] = kNorm ? fmaf(cm[s][e], x[s][e] - hcur[e], hcur[e]) : fmaf(-cm[s][e], hcur[e], hcur[e]) + x[s][e];
-      if (active && p.y != nullptr && t0 + s < p.T) IO::store(yp + (t0 + s) * p.sy.t, hcur);
-    }
+    for (int e = 0; e < VEC; ++e) h[e] = segH[q][pl.seg][pl.lc * VEC + e];
+    th.replay(chunk, h);
   }
-  if (kept && p.state_out != nullptr) p.state_out[row] = carry;
+  if (kept && p.state_out != nullptr) p.state_out[bh * p.d + ch] = carry;
 }
 
-// Backward, walking the tiles of a channel run from the last token to the
-// first.  g_t = dL/dh_t = dy_t + a_(t+1) g_(t+1); what crosses a token
-// boundary is G_t = a_t g_t, so a token maps G -> a_t (dy_t + G).  h_(t-1)
-// comes from replaying the tile forwards from its checkpoint:
-//   dx_t = g_t (c_t g_t),  df_t = g_t (h_(t-1) [- x_t]) a_t rate sigmoid(-f_t).
+// One workgroup per tile, chained.
 template <typename E, int VEC, int CW, bool kNorm>
-__global__ __launch_bounds__(kThreads) void gated_scan_bwd_kernel(GatedScanBwd p, HeadRate rates, int h0, int nh,
-                                                                  int nct) {
-  constexpr int S = kPerThread / VEC, LC = CW / VEC, TG = 64 / LC, NSEG = kWaves * TG, TT = NSEG * S;
+__global__ __launch_bounds__(kThreads) void gated_scan_fwd_chain_kernel(GatedScanFwd p, Chain cn, HeadRate rates,
+                                                                        int h0, int nh, int nct) {
+  using P = Place<VEC, CW>;
+  __shared__ float segA[P::NSEG][CW];
+  __shared__ float segH[P::NSEG][CW];
+  __shared__ float enter[CW];
+  __shared__ unsigned shared_ticket;
+  const unsigned ticket = take_ticket(cn.ticket, &shared_ticket);
+  if (ticket >= static_cast<unsigned>(cn.steps) * cn.tiles) return;  // the whole workgroup
+  const int chunk = ticket / cn.tiles, tile = ticket % cn.tiles;
+  const P pl;
+  const ScanTile tl = decode_tile(tile, nct, nh, h0, CW);
+  FwdThread<E, VEC, CW, kNorm> th(p, tl, pl, rates.r[tl.hl]);
+  th.load(chunk);
+  th.unpack(chunk);
+  float A[VEC], H[VEC];
+  th.map(A, H);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    segA[pl.seg][pl.lc * VEC + e] = A[e];
+    segH[pl.seg][pl.lc * VEC + e] = H[e];
+  }
+  __syncthreads();
+  if (pl.wave == 0 && pl.lane < CW) {
+    const int ch = tl.c0 + pl.lane;
+    const long bh = static_cast<long>(tl.b) * p.H + tl.h;
+    const bool kept = ch < p.d;
+    float a = 1.0f, h = 0.0f;  // the map of the segments so far
+#pragma unroll 8
+    for (int i = 0; i < P::NSEG; ++i) {
+      const float ai = segA[i][pl.lane], hi = segH[i][pl.lane];
+      segA[i][pl.lane] = a;
+      segH[i][pl.lane] = h;
+      a *= ai;
+      h = fmaf(ai, h, hi);
+    }
+    const float first = kept && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
+    const float v = chain<CW>(cn, chunk, tile, pl.lane, a, h, first);
+    enter[pl.lane] = v;
+    if (kept) {
+      if (p.checkpoints != nullptr) p.checkpoints[(bh * cn.steps + chunk) * p.d + ch] = v;
+      if (p.state_out != nullptr && chunk == cn.steps - 1) p.state_out[bh * p.d + ch] = fmaf(a, v, h);
+    }
+  }
+  __syncthreads();
+  float h[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const int c = pl.lc * VEC + e;
+    h[e] = fmaf(segA[pl.seg][c], enter[c], segH[pl.seg][c]);
+  }
+  th.replay(chunk, h);
+}
+
+// ---- Backward ----
+// g_t = dL/dh_t = dy_t + a_(t+1) g_(t+1); what crosses a token boundary is
+// G_t = a_t g_t, so a token maps G -> a_t (dy_t + G), last token first.
+// h_(t-1) comes from replaying the tile forwards from its checkpoint:
+//   dx_t = g_t (normalize: c_t g_t),  df_t = g_t (h_(t-1) [- x_t]) a_t rate sigmoid(-f_t).
+template <typename E, int VEC, int CW, bool kNorm>
+struct BwdThread {
+  using P = Place<VEC, CW>;
   using IO = VecIO<E, VEC>;
-  __shared__ float segA[2][NSEG][CW];
-  __shared__ float segH[2][NSEG][CW];
-  __shared__ float segG[2][NSEG][CW];
-
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int lc = lane % LC, seg = w * TG + lane / LC;
-  const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
-  const int c = tl.c0 + lc * VEC;
-  const bool active = c < p.d;
-  const int cc = active ? c : 0;
-  const E* xp = static_cast<const E*>(p.x) + tl.b * p.sx.b + tl.h * p.sx.h + cc;
-  const E* fp = static_cast<const E*>(p.f) + tl.b * p.sf.b + tl.h * p.sf.h + cc;
-  const E* gyp = static_cast<const E*>(p.grad_y) + tl.b * p.sgy.b + tl.h * p.sgy.h + cc;
-  E* gxp = static_cast<E*>(p.grad_x) + tl.b * p.sgx.b + tl.h * p.sgx.h + cc;
-  E* gfp = static_cast<E*>(p.grad_f) + tl.b * p.sgf.b + tl.h * p.sgf.h + cc;
-  const float rate = rates.r[tl.hl];
-  const int ch = tl.c0 + lane;
-  const bool kept = w < 2 && lane < CW && ch < p.d;  // wave 0 composes forwards, wave 1 backwards
-  const long bh = static_cast<long>(tl.b) * p.H + tl.h;
-  float carry = w == 1 && kept && p.grad_state_out != nullptr ? p.grad_state_out[bh * p.d + ch] : 0.0f;
-  const int nchunk = (p.T + TT - 1) / TT;
-
+  static constexpr int S = P::S;
+  const E *xp, *fp, *gyp;
+  E *gxp, *gfp;
+  long sx, sf, sgy, sgx, sgf;
+  float rate;
+  int T, seg;
+  bool store;
   typename IO::Raw rx[S], rf[S], rg[S];
-  auto load = [&](int chunk) __attribute__((always_inline)) {
+  float x[S][VEC], cm[S][VEC], kf[S][VEC], dy[S][VEC];
+
+  __device__ __forceinline__ BwdThread(const GatedScanBwd& p, const ScanTile& t, const P& pl, float r)
+      : sx(p.sx.t), sf(p.sf.t), sgy(p.sgy.t), sgx(p.sgx.t), sgf(p.sgf.t), rate(r), T(p.T), seg(pl.seg) {
+    const int c = t.c0 + pl.lc * VEC, cc = c < p.d ? c : 0;
+    xp = at_row<E>(p.x, p.sx, t, cc);
+    fp = at_row<E>(p.f, p.sf, t, cc);
+    gyp = at_row<E>(p.grad_y, p.sgy, t, cc);
+    gxp = at_row<E>(p.grad_x, p.sgx, t, cc);
+    gfp = at_row<E>(p.grad_f, p.sgf, t, cc);
+    store = c < p.d;
+  }
+  __device__ __forceinline__ void load(int chunk) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const long t = min(chunk * TT + seg * S + s, p.T - 1);
-      rx[s] = IO::load(xp + t * p.sx.t);
-      rf[s] = IO::load(fp + t * p.sf.t);
-      rg[s] = IO::load(gyp + t * p.sgy.t);
+      const long t = min(chunk * P::TT + seg * S + s, T - 1);
+      rx[s] = IO::load(xp + t * sx);
+      rf[s] = IO::load(fp + t * sf);
+      rg[s] = IO::load(gyp + t * sgy);
     }
-  };
-  load(nchunk - 1);
-  for (int chunk = nchunk - 1; chunk >= 0; --chunk) {
-    float x[S][VEC], cm[S][VEC], kf[S][VEC], dy[S][VEC];
-    const int t0 = chunk * TT + seg * S;
+  }
+  __device__ __forceinline__ void unpack(int chunk) {
+    const int t0 = chunk * P::TT + seg * S;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       float f[VEC];
       IO::unpack(rx[s], x[s]);
       IO::unpack(rf[s], f);
       IO::unpack(rg[s], dy[s]);
-      const bool in = t0 + s < p.T;
+      const bool in = t0 + s < T;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         float t;
@@ -236,69 +411,167 @@ __global__ __launch_bounds__(kThreads) void gated_scan_bwd_kernel(GatedScanBwd p
         dy[s][e] = in ? dy[s][e] : 0.0f;
       }
     }
-    const float ckpt = w == 0 && kept ? p.checkpoints[(bh * nchunk + chunk) * p.d + ch] : 0.0f;
-    if (chunk > 0) load(chunk - 1);
+  }
+  // the maps of the thread's tokens: h -> A h + H forwards, G -> A G + R backwards
+  __device__ __forceinline__ void map(int e, float& A, float& H, float& R) const {
+    A = 1.0f;
+    H = R = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      A = fmaf(-cm[s][e], A, A);
+      H = FwdThread<E, VEC, CW, kNorm>::step(cm[s][e], x[s][e], H);
+    }
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+      const float g = dy[s][e] + R;
+      R = fmaf(-cm[s][e], g, g);
+    }
+  }
+  // replays the tokens of element e from h before them and G behind them
+  __device__ __forceinline__ void replay(int e, float h, float G) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const float xs = x[s][e];
+      x[s][e] = kNorm ? h - xs : h;  // dh_t / da_t
+      h = FwdThread<E, VEC, CW, kNorm>::step(cm[s][e], xs, h);
+    }
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+      const float g = dy[s][e] + G;
+      G = fmaf(-cm[s][e], g, g);
+      dy[s][e] = kNorm ? g * cm[s][e] : g;
+      x[s][e] = g * x[s][e] * kf[s][e];
+    }
+  }
+  __device__ __forceinline__ void write(int chunk) const {
+    const int t0 = chunk * P::TT + seg * S;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (store && t0 + s < T) {
+        IO::store(gxp + (t0 + s) * sgx, dy[s]);
+        IO::store(gfp + (t0 + s) * sgf, x[s]);
+      }
+  }
+};
+
+// One workgroup walks the tiles of a channel run from the last token on.
+template <typename E, int VEC, int CW, bool kNorm>
+__global__ __launch_bounds__(kThreads) void gated_scan_bwd_walk_kernel(GatedScanBwd p, HeadRate rates, int h0, int nh,
+                                                                       int nct) {
+  using P = Place<VEC, CW>;
+  __shared__ float segA[2][P::NSEG][CW];
+  __shared__ float segH[2][P::NSEG][CW];
+  __shared__ float segG[2][P::NSEG][CW];
+  const P pl;
+  const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
+  BwdThread<E, VEC, CW, kNorm> th(p, tl, pl, rates.r[tl.hl]);
+  const int ch = tl.c0 + pl.lane;
+  const bool kept = pl.wave < 2 && pl.lane < CW && ch < p.d;  // wave 0 composes forwards, wave 1 backwards
+  const long bh = static_cast<long>(tl.b) * p.H + tl.h;
+  float carry = pl.wave == 1 && kept && p.grad_state_out != nullptr ? p.grad_state_out[bh * p.d + ch] : 0.0f;
+  const int nchunk = (p.T + P::TT - 1) / P::TT;
+  th.load(nchunk - 1);
+  for (int chunk = nchunk - 1; chunk >= 0; --chunk) {
+    th.unpack(chunk);
+    const float ckpt = pl.wave == 0 && kept ? p.checkpoints[(bh * nchunk + chunk) * p.d + ch] : 0.0f;
+    if (chunk > 0) th.load(chunk - 1);
     const int q = chunk & 1;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      float A = 1.0f, H = 0.0f, G = 0.0f;
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        A = fmaf(-cm[s][e], A, A);
-        H = kNorm ? fmaf(cm[s][e], x[s][e] - H, H) : fmaf(-cm[s][e], H, H) + x[s][e];
-      }
-#pragma unroll
-      for (int s = S - 1; s >= 0; --s) {
-        const float g = dy[s][e] + G;
-        G = fmaf(-cm[s][e], g, g);
-      }
-      segA[q][seg][lc * VEC + e] = A;
-      segH[q][seg][lc * VEC + e] = H;
-      segG[q][seg][lc * VEC + e] = G;
+      float A, H, R;
+      th.map(e, A, H, R);
+      segA[q][pl.seg][pl.lc * VEC + e] = A;
+      segH[q][pl.seg][pl.lc * VEC + e] = H;
+      segG[q][pl.seg][pl.lc * VEC + e] = R;
     }
     __syncthreads();
-    if (w == 0 && lane < CW) {
+    if (pl.wave == 0 && pl.lane < CW) {
       float cur = ckpt;
 #pragma unroll 8
-      for (int i = 0; i < NSEG; ++i) {
-        const float a = segA[q][i][lane], hh = segH[q][i][lane];
-        segH[q][i][lane] = cur;
+      for (int i = 0; i < P::NSEG; ++i) {
+        const float a = segA[q][i][pl.lane], hh = segH[q][i][pl.lane];
+        segH[q][i][pl.lane] = cur;
         cur = fmaf(a, cur, hh);
       }
-    } else if (w == 1 && lane < CW) {
+    } else if (pl.wave == 1 && pl.lane < CW) {
 #pragma unroll 8
-      for (int i = NSEG - 1; i >= 0; --i) {
-        const float a = segA[q][i][lane], gg = segG[q][i][lane];
-        segG[q][i][lane] = carry;
+      for (int i = P::NSEG - 1; i >= 0; --i) {
+        const float a = segA[q][i][pl.lane], gg = segG[q][i][pl.lane];
+        segG[q][i][pl.lane] = carry;
         carry = fmaf(a, carry, gg);
       }
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float hp = segH[q][seg][lc * VEC + e], G = segG[q][seg][lc * VEC + e];
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const float xs = x[s][e];
-        x[s][e] = kNorm ? hp - xs : hp;  // dh_t / da_t
-        hp = kNorm ? fmaf(cm[s][e], xs - hp, hp) : fmaf(-cm[s][e], hp, hp) + xs;
-      }
-#pragma unroll
-      for (int s = S - 1; s >= 0; --s) {
-        const float g = dy[s][e] + G;
-        G = fmaf(-cm[s][e], g, g);
-        dy[s][e] = kNorm ? g * cm[s][e] : g;
-        x[s][e] = g * x[s][e] * kf[s][e];
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-      if (active && t0 + s < p.T) {
-        IO::store(gxp + (t0 + s) * p.sgx.t, dy[s]);
-        IO::store(gfp + (t0 + s) * p.sgf.t, x[s]);
-      }
+    for (int e = 0; e < VEC; ++e) th.replay(e, segH[q][pl.seg][pl.lc * VEC + e], segG[q][pl.seg][pl.lc * VEC + e]);
+    th.write(chunk);
   }
-  if (w == 1 && kept && p.grad_state_in != nullptr) p.grad_state_in[bh * p.d + ch] = carry;
+  if (pl.wave == 1 && kept && p.grad_state_in != nullptr) p.grad_state_in[bh * p.d + ch] = carry;
+}
+
+// One workgroup per tile, chained from the last token on.
+template <typename E, int VEC, int CW, bool kNorm>
+__global__ __launch_bounds__(kThreads) void gated_scan_bwd_chain_kernel(GatedScanBwd p, Chain cn, HeadRate rates,
+                                                                        int h0, int nh, int nct) {
+  using P = Place<VEC, CW>;
+  __shared__ float segA[P::NSEG][CW];
+  __shared__ float segH[P::NSEG][CW];
+  __shared__ float segG[P::NSEG][CW];
+  __shared__ float segB[P::NSEG][CW];  // products of A behind a segment
+  __shared__ float enter[CW];
+  __shared__ unsigned shared_ticket;
+  const unsigned ticket = take_ticket(cn.ticket, &shared_ticket);
+  if (ticket >= static_cast<unsigned>(cn.steps) * cn.tiles) return;  // the whole workgroup
+  const int step = ticket / cn.tiles, tile = ticket % cn.tiles, chunk = cn.steps - 1 - step;
+  const P pl;
+  const ScanTile tl = decode_tile(tile, nct, nh, h0, CW);
+  BwdThread<E, VEC, CW, kNorm> th(p, tl, pl, rates.r[tl.hl]);
+  const int ch = tl.c0 + pl.lane;
+  const bool kept = pl.wave < 2 && pl.lane < CW && ch < p.d;
+  const long bh = static_cast<long>(tl.b) * p.H + tl.h;
+  th.load(chunk);
+  // wave 0: the state before the tile; wave 1: the gradient behind the sequence
+  float cur = 0.0f;
+  if (pl.wave == 0 && kept) cur = p.checkpoints[(bh * cn.steps + chunk) * p.d + ch];
+  if (pl.wave == 1 && kept && p.grad_state_out != nullptr) cur = p.grad_state_out[bh * p.d + ch];
+  th.unpack(chunk);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    float A, H, R;
+    th.map(e, A, H, R);
+    segA[pl.seg][pl.lc * VEC + e] = A;
+    segH[pl.seg][pl.lc * VEC + e] = H;
+    segG[pl.seg][pl.lc * VEC + e] = R;
+  }
+  __syncthreads();
+  if (pl.wave == 0 && pl.lane < CW) {
+#pragma unroll 8
+    for (int i = 0; i < P::NSEG; ++i) {
+      const float a = segA[i][pl.lane], hh = segH[i][pl.lane];
+      segH[i][pl.lane] = cur;
+      cur = fmaf(a, cur, hh);
+    }
+  } else if (pl.wave == 1 && pl.lane < CW) {
+    float a = 1.0f, g = 0.0f;  // the map of the segments behind
+#pragma unroll 8
+    for (int i = P::NSEG - 1; i >= 0; --i) {
+      const float ai = segA[i][pl.lane], gi = segG[i][pl.lane];
+      segB[i][pl.lane] = a;
+      segG[i][pl.lane] = g;
+      a *= ai;
+      g = fmaf(ai, g, gi);
+    }
+    const float v = chain<CW>(cn, step, tile, pl.lane, a, g, cur);
+    enter[pl.lane] = v;
+    if (kept && p.grad_state_in != nullptr && chunk == 0) p.grad_state_in[bh * p.d + ch] = fmaf(a, v, g);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const int c = pl.lc * VEC + e;
+    th.replay(e, segH[pl.seg][c], fmaf(segB[pl.seg][c], enter[c], segG[pl.seg][c]));
+  }
+  th.write(chunk);
 }
 
 // One token: state <- a state + u, y = state; one thread per VEC channels.
@@ -340,11 +613,56 @@ HeadRate head_rates(const HeadGroup& g) {
   return r;
 }
 
+// Tile width for a row of d channels: 64, or the next power of two for
+// narrow rows so that lanes are not left idle.
+int tile_width(int d) { return d > 32 ? 64 : d > 16 ? 32 : 16; }
+
+// The chained kernels' part of the workspace for a launch of nh heads.
+struct ChainSizes {
+  int steps, tiles;
+  size_t maps, enter;  // words of 8 and of 4 bytes
+};
+ChainSizes chain_sizes(int B, int nh, int T, int d) {
+  const int cw = tile_width(d), tt = gated_scan_block(d);
+  ChainSizes z;
+  z.steps = (T + tt - 1) / tt;
+  z.tiles = B * nh * ((d + cw - 1) / cw);
+  z.maps = static_cast<size_t>(z.steps) * z.tiles * cw;
+  z.enter = static_cast<size_t>((z.steps + kGroup - 1) / kGroup) * z.tiles * cw;
+  return z;
+}
+
+// Whether the tiles of a channel run are chained over workgroups (else one
+// workgroup walks them).
+bool chained(int B, int H, int T, int d) {
+  const ChainSizes z = chain_sizes(B, H < kHeadsPerLaunch ? H : kHeadsPerLaunch, T, d);
+  return z.steps > 1 && z.tiles < kWalkTiles;
+}
+
+hipError_t make_chain(void* ws, int B, int nh, int T, int d, Chain* c, hipStream_t s) {
+  const ChainSizes z = chain_sizes(B, nh, T, d);
+  char* base = static_cast<char*>(ws);
+  c->ticket = reinterpret_cast<unsigned*>(base);
+  c->maps = reinterpret_cast<u64*>(base + kChainHead);
+  c->enter = reinterpret_cast<unsigned*>(base + kChainHead + z.maps * 8);
+  c->steps = z.steps;
+  c->tiles = z.tiles;
+  return launch_fill_u32(c->maps, z.maps * 2 + z.enter, 0xFFFFFFFFu, s, c->ticket, 0);
+}
+
 template <typename E, int VEC, int CW, bool kNorm>
-hipError_t run_fwd(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s) {
+hipError_t run_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int nct = (p.d + CW - 1) / CW;
-  hipLaunchKernelGGL((gated_scan_fwd_kernel<E, VEC, CW, kNorm>), dim3(p.B * g.nh * nct), dim3(kThreads), 0, s, p,
-                     head_rates(g), g.h0, g.nh, nct);
+  if (!chained(p.B, p.H, p.T, p.d)) {
+    hipLaunchKernelGGL((gated_scan_fwd_walk_kernel<E, VEC, CW, kNorm>), dim3(p.B * g.nh * nct), dim3(kThreads), 0, s,
+                       p, head_rates(g), g.h0, g.nh, nct);
+    return hipGetLastError();
+  }
+  Chain c;
+  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, &c, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, kNorm>), dim3(c.steps * c.tiles), dim3(kThreads), 0, s,
+                     p, c, head_rates(g), g.h0, g.nh, nct);
   return hipGetLastError();
 }
 
@@ -357,16 +675,20 @@ hipError_t run_step(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s) {
 }
 
 template <typename E, int VEC, int CW, bool kNorm>
-hipError_t run_bwd(const GatedScanBwd& p, const HeadGroup& g, hipStream_t s) {
+hipError_t run_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int nct = (p.d + CW - 1) / CW;
-  hipLaunchKernelGGL((gated_scan_bwd_kernel<E, VEC, CW, kNorm>), dim3(p.B * g.nh * nct), dim3(kThreads), 0, s, p,
-                     head_rates(g), g.h0, g.nh, nct);
+  if (!chained(p.B, p.H, p.T, p.d)) {
+    hipLaunchKernelGGL((gated_scan_bwd_walk_kernel<E, VEC, CW, kNorm>), dim3(p.B * g.nh * nct), dim3(kThreads), 0, s,
+                       p, head_rates(g), g.h0, g.nh, nct);
+    return hipGetLastError();
+  }
+  Chain c;
+  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, &c, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, kNorm>), dim3(c.steps * c.tiles), dim3(kThreads), 0, s,
+                     p, c, head_rates(g), g.h0, g.nh, nct);
   return hipGetLastError();
 }
-
-// Tile width for a row of d channels: 64, or the next power of two for
-// narrow rows so that lanes are not left idle.
-int tile_width(int d) { return d > 32 ? 64 : d > 16 ? 32 : 16; }
 
 template <template <typename, int, int, bool> class F, typename E, int VEC, typename... A>
 hipError_t by_width(int cw, bool norm, A&&... a) {
@@ -385,14 +707,14 @@ hipError_t by_vec(int vec, int cw, bool norm, A&&... a) {
 
 template <typename E, int VEC, int CW, bool kNorm>
 struct Fwd {
-  static hipError_t run(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s) {
-    return run_fwd<E, VEC, CW, kNorm>(p, g, s);
+  static hipError_t run(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
+    return run_fwd<E, VEC, CW, kNorm>(p, ws, g, s);
   }
 };
 template <typename E, int VEC, int CW, bool kNorm>
 struct Bwd {
-  static hipError_t run(const GatedScanBwd& p, const HeadGroup& g, hipStream_t s) {
-    return run_bwd<E, VEC, CW, kNorm>(p, g, s);
+  static hipError_t run(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
+    return run_bwd<E, VEC, CW, kNorm>(p, ws, g, s);
   }
 };
 
@@ -409,7 +731,13 @@ hipError_t step_by_vec(int vec, const GatedScanFwd& p, const HeadGroup& g, hipSt
 
 int gated_scan_block(int d) { return kWaves * (kPerThread * 64 / tile_width(d)); }
 
-hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s) {
+size_t gated_scan_chain_bytes(int B, int H, int T, int d) {
+  if (T <= 1 || !chained(B, H, T, d)) return 0;
+  const ChainSizes z = chain_sizes(B, H < kHeadsPerLaunch ? H : kHeadsPerLaunch, T, d);
+  return kChainHead + z.maps * 8 + z.enter * 4;
+}
+
+hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int es = p.dt == 1 ? 2 : 4;
   const int vec = widest_access(p.d, 4, es, {p.x, p.f, p.y}, {p.sx, p.sf, p.sy});
   if (p.T == 1) {
@@ -417,16 +745,17 @@ hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, const HeadGroup& g, hipS
     return p.dt == 1 ? step_by_vec<uint16_t>(sv, p, g, s) : step_by_vec<float>(sv, p, g, s);
   }
   const int cw = tile_width(p.d);
-  return p.dt == 1 ? by_vec<Fwd, uint16_t>(vec, cw, p.normalize, p, g, s)
-                   : by_vec<Fwd, float>(vec, cw, p.normalize, p, g, s);
+  return p.dt == 1 ? by_vec<Fwd, uint16_t>(vec, cw, p.normalize, p, ws, g, s)
+                   : by_vec<Fwd, float>(vec, cw, p.normalize, p, ws, g, s);
 }
 
-hipError_t launch_gated_scan_bwd(const GatedScanBwd& p, const HeadGroup& g, hipStream_t s) {
+hipError_t launch_gated_scan_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int es = p.dt == 1 ? 2 : 4;
-  const int vec = widest_access(p.d, 4, es, {p.x, p.f, p.grad_y, p.grad_x, p.grad_f}, {p.sx, p.sf, p.sgy, p.sgx, p.sgf});
+  const int vec =
+      widest_access(p.d, 4, es, {p.x, p.f, p.grad_y, p.grad_x, p.grad_f}, {p.sx, p.sf, p.sgy, p.sgx, p.sgf});
   const int cw = tile_width(p.d);
-  return p.dt == 1 ? by_vec<Bwd, uint16_t>(vec, cw, p.normalize, p, g, s)
-                   : by_vec<Bwd, float>(vec, cw, p.normalize, p, g, s);
+  return p.dt == 1 ? by_vec<Bwd, uint16_t>(vec, cw, p.normalize, p, ws, g, s)
+                   : by_vec<Bwd, float>(vec, cw, p.normalize, p, ws, g, s);
 }
 
 }  // namespace ret

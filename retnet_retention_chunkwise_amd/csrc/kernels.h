@@ -208,8 +208,11 @@ struct GatedScanBwd {
   int dt;
 };
 int gated_scan_block(int d);  // tokens per checkpoint
-hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s);
-hipError_t launch_gated_scan_bwd(const GatedScanBwd& p, const HeadGroup& g, hipStream_t s);
+// Scratch of a launch that chains its tiles over workgroups (0: it needs none);
+// calls of more than kHeadsPerLaunch heads use it again for every head group.
+size_t gated_scan_chain_bytes(int B, int H, int T, int d);
+hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s);
+hipError_t launch_gated_scan_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s);
 
 // out[k][c] = sum over r of partial[k][r][c] for k < 3 (null outputs skipped),
 // partial [3][rows][n].

@@ -138,6 +138,11 @@ CASES = [
     (1, 8, 700, 512, torch.bfloat16, True, True, 0.005),
     (1, 130, 140, 4, torch.float32, False, True, 0),
     (1, 1, 5000, 1, torch.float32, True, True, 0.001),
+    # enough channel runs for one workgroup each
+    (4, 8, 270, 512, torch.bfloat16, True, True, 0.01),
+    (16, 16, 1050, 7, torch.float32, False, True, 0.01),
+    # many groups of chained tiles
+    (1, 2, 9000, 40, torch.bfloat16, False, True, 0.0005),
 ]
 
 
