@@ -26,14 +26,14 @@
 namespace ret {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kPerThread = 16;  // VEC * S
+constexpr int kBlockWaves = 8;  // a checkpoint's block is the tile of a workgroup of 8 waves
 // Channel runs from which on each is walked by one workgroup.  Measured at 256
 // runs (one for each compute unit): walking 50 us and chaining 68 us (B4 H8
 // T2048 d512, bf16), 515 and 665 us (B2 H16 T8192 d512 forward and backward);
 // at 64 runs 1445 and 462 us (B1 H8 T65536 d512 forward).
 constexpr int kWalkTiles = 256;
+constexpr int kTableTiles = 4;  // tiles of a workgroup from which on its gate table pays
 
 typedef unsigned long long u64;
 
@@ -49,7 +49,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // through its Taylor series where 2^z is near 1, so c keeps its relative
 // precision down to the smallest decays.  f = -inf gives c = 1 and f = +inf
 // gives c = 0 exactly.  *t_out: t.
-template <typename E>
 __device__ __forceinline__ float decay_complement(float f, float rate, float* t_out) {
   const float af = fabsf(f);
   const float p = af * kLog2e;
@@ -74,6 +73,96 @@ __device__ __forceinline__ float sigmoid_neg(float f, float t) {
   return (f > 0.0f ? t : 1.0f) * __builtin_amdgcn_rcpf(1.0f + t);
 }
 
+// ---- Gate table ----
+//
+// bf16 gates take few values: 31 * 128 magnitudes from 2^-24 to 128 in two
+// signs.  A workgroup that works on many tokens of one head evaluates the gate
+// once for each of them into LDS and then looks it up, about 5 vector
+// instructions and an LDS read per element in place of about 35 (three of them
+// at a quarter of the rate), which bounded the kernel.  The entry of a value v
+// is at rotate_left(bits(v), 1), so that both signs of a magnitude lie side by
+// side.  Magnitudes below 2^-24 take the entry of 2^-24 (c moves by less than
+// 2^-24 of itself); a thread that meets 128 or more, an infinity or a NaN
+// evaluates its tokens directly.
+constexpr int kGateLow = 103 << 7, kGateHigh = 134 << 7;  // bf16 bits of 2^-24 and of 128
+constexpr int kGateN = 2 * (kGateHigh - kGateLow);
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// Table index of two gates; top collects the largest index before clamping
+// (kGateN or more: a gate outside the table).
+__device__ __forceinline__ u16x2 gate_index(u16x2 bits, u16x2& top) {
+  const u16x2 one = 1, fifteen = 15, low = 2 * kGateLow, most = kGateN - 1;
+  const u16x2 r = __builtin_elementwise_sub_sat(static_cast<u16x2>((bits << one) | (bits >> fifteen)), low);
+  top = __builtin_elementwise_max(top, r);
+  return __builtin_elementwise_min(r, most);
+}
+
+__device__ __forceinline__ float gate_of_index(int i) {
+  return bf16_to_f32(static_cast<uint16_t>((kGateLow + (i >> 1)) | ((i & 1) << 15)));
+}
+
+// One gate: c = 1 - a and, for the backward, k = rate a sigmoid(-f).
+__device__ __forceinline__ void gate_value(float f, float rate, float* out) {
+  float t;
+  *out = decay_complement(f, rate, &t);
+}
+__device__ __forceinline__ void gate_value(float f, float rate, float2* out) {
+  float t;
+  const float c = decay_complement(f, rate, &t);
+  *out = make_float2(c, rate * (1.0f - c) * sigmoid_neg(f, t));
+}
+
+template <typename Entry>
+__device__ __forceinline__ void build_gate_table(Entry* table, float rate, int threads) {
+  for (int i = threadIdx.x; i < kGateN; i += threads) gate_value(gate_of_index(i), rate, &table[i]);
+}
+
+// The gates of S rows of VEC elements.
+template <typename E, typename Entry, int VEC, int S>
+struct Gates {
+  using IO = VecIO<E, VEC>;
+  __device__ __forceinline__ static void direct(const typename IO::Raw (&rf)[S], float rate, Entry (&out)[S][VEC]) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      float f[VEC];
+      IO::unpack(rf[s], f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) gate_value(f[e], rate, &out[s][e]);
+    }
+  }
+  // by table when one is given (bf16 only)
+  __device__ __forceinline__ static void get(const typename IO::Raw (&rf)[S], const Entry* table, float rate,
+                                             Entry (&out)[S][VEC]) {
+    if constexpr (sizeof(E) == 2) {
+      if (table != nullptr) {  // known at compile time
+        u16x2 top = 0;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          if constexpr (VEC == 1) {
+            u16x2 two;
+            two[0] = two[1] = rf[s];
+            out[s][0] = table[gate_index(two, top)[0]];
+          } else if constexpr (VEC == 2) {
+            const u16x2 i = gate_index(__builtin_bit_cast(u16x2, rf[s]), top);
+            out[s][0] = table[i[0]];
+            out[s][1] = table[i[1]];
+          } else {
+#pragma unroll
+            for (int v = 0; v < VEC / 2; ++v) {
+              const u16x2 i = gate_index(__builtin_bit_cast(u16x2, static_cast<unsigned>(rf[s][v])), top);
+              out[s][2 * v] = table[i[0]];
+              out[s][2 * v + 1] = table[i[1]];
+            }
+          }
+        }
+        if (__any(top[0] >= kGateN || top[1] >= kGateN)) direct(rf, rate, out);
+        return;
+      }
+    }
+    direct(rf, rate, out);
+  }
+};
+
 struct ScanTile {
   int b, h, hl, c0, ct;
 };
@@ -92,23 +181,25 @@ __device__ __forceinline__ ScanTile decode_tile(int tile, int nct, int nh, int h
 // ---- Chaining tiles that run in different workgroups ----
 //
 // With few channels and many tokens the tiles of one channel run must work at
-// the same time, each on its own tokens, and still hand their state on.  A
-// workgroup takes a ticket; tickets go through the tiles of step 0 of the walk
-// (the first tokens, or the last ones backwards), then step 1, ...  It
-// publishes its tile's map (A, H), takes the value that enters its group of
-// kGroup steps and folds the maps of the group's earlier steps into it; the
-// last step of a group publishes the value that enters the next group.  The
-// order of all additions is fixed by the sizes, so results do not depend on
-// timing.  A workgroup waits only for lower tickets, whose workgroups already
-// run, so every wait ends; a wait of more than kSpinLimit polls (two calls on
-// one workspace at the same time, which the interface forbids) gives NaN
+// the same time, each on its own tokens, and still hand their state on.  The
+// workgroups of a head take tickets; tickets go through the head's tiles of
+// step 0 of the walk (the first tokens, or the last ones backwards), then step
+// 1, ...  A workgroup publishes its tile's map (A, H), takes the value that
+// enters its group of kGroup steps and folds the maps of the group's earlier
+// steps into it; the last step of a group publishes the value that enters the
+// next group.  The order of all additions is fixed by the sizes, so results do
+// not depend on timing.  A workgroup works on its tickets in order, taking the
+// next one early to have its tile's loads in flight, and waits only for lower
+// tickets: the lowest unfinished ticket of all is being worked on and waits for
+// nothing, so every wait ends.  A wait of more than kSpinLimit polls (two calls
+// on one workspace at the same time, which the interface forbids) gives NaN
 // instead of hanging.  Published words carry their own "ready": the workspace
 // is filled with ones before the launch and no published NaN has that pattern.
 constexpr int kGroup = 16;
 constexpr int kSpinLimit = 1 << 20;
-constexpr size_t kChainHead = 256;  // the ticket counter
+constexpr int kCounterWords = 16;  // a head's ticket counter has a cache line's half to itself
 struct Chain {
-  unsigned* ticket;
+  unsigned* ticket;  // [heads of the launch][kCounterWords]
   u64* maps;        // [steps][tiles][CW]: A in the low word, H in the high word
   unsigned* enter;  // [groups][tiles][CW]: the value that enters a group
   int steps, tiles;
@@ -156,17 +247,17 @@ __device__ __forceinline__ float chain(const Chain& c, int j, int tile, int lane
   return v;
 }
 
-// The workgroup's ticket; every thread gets it (a barrier inside).
-__device__ __forceinline__ unsigned take_ticket(unsigned* counter, unsigned* shared) {
-  if (threadIdx.x == 0) *shared = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  return *shared;
+// The next ticket of a head's queue (counters start one below 0).
+__device__ __forceinline__ unsigned take_ticket(unsigned* counter) {
+  return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
 }
 
 // Where a thread stands in its tile.
-template <int VEC, int CW>
+template <int VEC, int CW, int NW>
 struct Place {
-  static constexpr int S = kPerThread / VEC, LC = CW / VEC, TG = 64 / LC, NSEG = kWaves * TG, TT = NSEG * S;
+  static constexpr int S = kPerThread / VEC, LC = CW / VEC, TG = 64 / LC, NSEG = NW * TG, TT = NSEG * S;
+  // checkpoints lie every kBlockWaves waves of a tile
+  static constexpr int CSEG = kBlockWaves * TG, BLOCKS = NW / kBlockWaves, BLOCK = TT / BLOCKS;
   int lane, wave, lc, seg;
   __device__ Place()
       : lane(threadIdx.x & 63), wave(threadIdx.x >> 6), lc((threadIdx.x & 63) % LC),
@@ -179,9 +270,9 @@ __device__ __forceinline__ E* at_row(const void* p, const Strides3& s, const Sca
 }
 
 // ---- Forward ----
-template <typename E, int VEC, int CW, bool kNorm>
+template <typename E, int VEC, int CW, int NW, bool kNorm>
 struct FwdThread {
-  using P = Place<VEC, CW>;
+  using P = Place<VEC, CW, NW>;
   using IO = VecIO<E, VEC>;
   static constexpr int S = P::S;
   const E *xp, *fp;
@@ -193,13 +284,17 @@ struct FwdThread {
   typename IO::Raw rx[S], rf[S];
   float x[S][VEC], cm[S][VEC];
 
-  __device__ __forceinline__ FwdThread(const GatedScanFwd& p, const ScanTile& t, const P& pl, float r)
-      : sx(p.sx.t), sf(p.sf.t), sy(p.sy.t), rate(r), T(p.T), seg(pl.seg) {
+  __device__ __forceinline__ FwdThread(const GatedScanFwd& p, const P& pl, float r)
+      : sx(p.sx.t), sf(p.sf.t), sy(p.sy.t), rate(r), T(p.T), seg(pl.seg) {}
+  __device__ __forceinline__ void aim_loads(const GatedScanFwd& p, const ScanTile& t, const P& pl) {
     const int c = t.c0 + pl.lc * VEC, cc = c < p.d ? c : 0;  // lanes past the row's end read its start, store nothing
     xp = at_row<E>(p.x, p.sx, t, cc);
     fp = at_row<E>(p.f, p.sf, t, cc);
-    yp = at_row<E>(p.y, p.sy, t, cc);
+  }
+  __device__ __forceinline__ void aim_stores(const GatedScanFwd& p, const ScanTile& t, const P& pl) {
+    const int c = t.c0 + pl.lc * VEC;
     store = c < p.d && p.y != nullptr;
+    yp = at_row<E>(p.y, p.sy, t, c < p.d ? c : 0);
   }
   __device__ __forceinline__ void load(int chunk) {
 #pragma unroll
@@ -209,19 +304,17 @@ struct FwdThread {
       rf[s] = IO::load(fp + t * sf);
     }
   }
-  __device__ __forceinline__ void unpack(int chunk) {
+  __device__ __forceinline__ void unpack(int chunk, const float* table) {
+    Gates<E, float, VEC, S>::get(rf, table, rate, cm);
+#pragma unroll
+    for (int s = 0; s < S; ++s) IO::unpack(rx[s], x[s]);
+    if ((chunk + 1) * P::TT <= T) return;  // uniform; else tokens past the end leave the state as it is
     const int t0 = chunk * P::TT + seg * S;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      float f[VEC], t;
-      IO::unpack(rx[s], x[s]);
-      IO::unpack(rf[s], f);
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        cm[s][e] = t0 + s < T ? decay_complement<E>(f[e], rate, &t) : 0.0f;
-        x[s][e] = t0 + s < T ? x[s][e] : 0.0f;
-      }
-    }
+      for (int e = 0; e < VEC; ++e)
+        if (t0 + s >= T) cm[s][e] = x[s][e] = 0.0f;
   }
   __device__ __forceinline__ static float step(float c, float x, float h) {
     return kNorm ? fmaf(c, x - h, h) : fmaf(-c, h, h) + x;
@@ -252,24 +345,33 @@ struct FwdThread {
 };
 
 // One workgroup walks the tiles of a channel run from the first token on.
-template <typename E, int VEC, int CW, bool kNorm>
-__global__ __launch_bounds__(kThreads) void gated_scan_fwd_walk_kernel(GatedScanFwd p, HeadRate rates, int h0, int nh,
+template <typename E, int VEC, int CW, int NW, bool kNorm>
+__global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanFwd p, HeadRate rates, int h0, int nh,
                                                                        int nct) {
-  using P = Place<VEC, CW>;
+  using P = Place<VEC, CW, NW>;
   __shared__ float segA[2][P::NSEG][CW];
   __shared__ float segH[2][P::NSEG][CW];
   const P pl;
   const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
-  FwdThread<E, VEC, CW, kNorm> th(p, tl, pl, rates.r[tl.hl]);
+  FwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[tl.hl]);
+  th.aim_loads(p, tl, pl);
+  th.aim_stores(p, tl, pl);
   // the composing wave: one channel per lane
   const int ch = tl.c0 + pl.lane;
   const bool mine = pl.wave == 0 && pl.lane < CW, kept = mine && ch < p.d;
   const long bh = static_cast<long>(tl.b) * p.H + tl.h;
   float carry = kept && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
-  const int nchunk = (p.T + P::TT - 1) / P::TT;
+  const int nchunk = (p.T + P::TT - 1) / P::TT, nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
   th.load(0);
+  const float* table = nullptr;
+  if constexpr (sizeof(E) == 2) {
+    __shared__ float gate[kGateN];
+    build_gate_table(gate, th.rate, 64 * NW);
+    table = gate;
+    __syncthreads();
+  }
   for (int chunk = 0; chunk < nchunk; ++chunk) {
-    th.unpack(chunk);
+    th.unpack(chunk, table);
     if (chunk + 1 < nchunk) th.load(chunk + 1);
     const int q = chunk & 1;
     float A[VEC], H[VEC];
@@ -281,12 +383,16 @@ __global__ __launch_bounds__(kThreads) void gated_scan_fwd_walk_kernel(GatedScan
     }
     __syncthreads();
     if (mine) {
-      if (kept && p.checkpoints != nullptr) p.checkpoints[(bh * nchunk + chunk) * p.d + ch] = carry;
+#pragma unroll
+      for (int k = 0; k < P::BLOCKS; ++k) {
+        const int block = chunk * P::BLOCKS + k;
+        if (kept && p.checkpoints != nullptr && block < nblock) p.checkpoints[(bh * nblock + block) * p.d + ch] = carry;
 #pragma unroll 8
-      for (int i = 0; i < P::NSEG; ++i) {
-        const float a = segA[q][i][pl.lane], hh = segH[q][i][pl.lane];
-        segH[q][i][pl.lane] = carry;
-        carry = fmaf(a, carry, hh);
+        for (int i = k * P::CSEG; i < (k + 1) * P::CSEG; ++i) {
+          const float a = segA[q][i][pl.lane], hh = segH[q][i][pl.lane];
+          segH[q][i][pl.lane] = carry;
+          carry = fmaf(a, carry, hh);
+        }
       }
     }
     __syncthreads();
@@ -298,60 +404,101 @@ __global__ __launch_bounds__(kThreads) void gated_scan_fwd_walk_kernel(GatedScan
   if (kept && p.state_out != nullptr) p.state_out[bh * p.d + ch] = carry;
 }
 
-// One workgroup per tile, chained.
-template <typename E, int VEC, int CW, bool kNorm>
-__global__ __launch_bounds__(kThreads) void gated_scan_fwd_chain_kernel(GatedScanFwd p, Chain cn, HeadRate rates,
-                                                                        int h0, int nh, int nct) {
-  using P = Place<VEC, CW>;
+// Workgroups of one head (blockIdx modulo the heads) on the tiles of its queue.
+template <typename E, int VEC, int CW, int NW, bool kNorm, bool kTable>
+__global__ __launch_bounds__(64 * NW) void gated_scan_fwd_chain_kernel(GatedScanFwd p, Chain cn, HeadRate rates,
+                                                                       int h0, int nh, int nct) {
+  using P = Place<VEC, CW, NW>;
   __shared__ float segA[P::NSEG][CW];
   __shared__ float segH[P::NSEG][CW];
   __shared__ float enter[CW];
-  __shared__ unsigned shared_ticket;
-  const unsigned ticket = take_ticket(cn.ticket, &shared_ticket);
-  if (ticket >= static_cast<unsigned>(cn.steps) * cn.tiles) return;  // the whole workgroup
-  const int chunk = ticket / cn.tiles, tile = ticket % cn.tiles;
+  __shared__ unsigned tickets[2];
+  __shared__ float gate[kTable ? kGateN : 1];
   const P pl;
-  const ScanTile tl = decode_tile(tile, nct, nh, h0, CW);
-  FwdThread<E, VEC, CW, kNorm> th(p, tl, pl, rates.r[tl.hl]);
-  th.load(chunk);
-  th.unpack(chunk);
-  float A[VEC], H[VEC];
-  th.map(A, H);
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    segA[pl.seg][pl.lc * VEC + e] = A[e];
-    segH[pl.seg][pl.lc * VEC + e] = H[e];
-  }
+  const int hl = blockIdx.x % nh, per_step = p.B * nct;
+  const unsigned total = static_cast<unsigned>(cn.steps) * per_step;
+  unsigned* counter = cn.ticket + hl * kCounterWords;
+  if (threadIdx.x < 2) tickets[threadIdx.x] = take_ticket(counter);
   __syncthreads();
-  if (pl.wave == 0 && pl.lane < CW) {
-    const int ch = tl.c0 + pl.lane;
-    const long bh = static_cast<long>(tl.b) * p.H + tl.h;
-    const bool kept = ch < p.d;
-    float a = 1.0f, h = 0.0f;  // the map of the segments so far
+  // the two lanes' additions may be served in either order
+  unsigned cur = min(tickets[0], tickets[1]), next = max(tickets[0], tickets[1]);
+  if (cur >= total) return;  // the whole workgroup
+  const int nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
+  FwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[hl]);
+  // a ticket's tile: (b, column tile) of this head at one step
+  auto tile_of = [&](unsigned ticket) __attribute__((always_inline)) {
+    const int i = ticket % per_step;
+    return decode_tile((i / nct * nh + hl) * nct + i % nct, nct, nh, h0, CW);
+  };
+  ScanTile tl = tile_of(cur);
+  th.aim_loads(p, tl, pl);
+  th.load(cur / per_step);
+  if constexpr (kTable) build_gate_table(gate, th.rate, 64 * NW);
+  __syncthreads();  // the table; and everyone has read the first tickets
+  for (;;) {
+    const int chunk = cur / per_step;
+    th.aim_stores(p, tl, pl);
+    th.unpack(chunk, kTable ? gate : nullptr);
+    float A[VEC], H[VEC];
+    th.map(A, H);
+    ScanTile nt = tl;
+    if (next < total) {
+      nt = tile_of(next);
+      th.aim_loads(p, nt, pl);
+      th.load(next / per_step);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      segA[pl.seg][pl.lc * VEC + e] = A[e];
+      segH[pl.seg][pl.lc * VEC + e] = H[e];
+    }
+    __syncthreads();
+    if (threadIdx.x == 64 && next < total) tickets[0] = take_ticket(counter);
+    if (pl.wave == 0 && pl.lane < CW) {
+      const int ch = tl.c0 + pl.lane;
+      const long bh = static_cast<long>(tl.b) * p.H + tl.h;
+      const bool kept = ch < p.d;
+      const float first = kept && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
+      float a = 1.0f, h = 0.0f, ca[P::BLOCKS], chh[P::BLOCKS];  // the map of the segments so far, and at the blocks
+#pragma unroll
+      for (int k = 0; k < P::BLOCKS; ++k) {
+        ca[k] = a;
+        chh[k] = h;
 #pragma unroll 8
-    for (int i = 0; i < P::NSEG; ++i) {
-      const float ai = segA[i][pl.lane], hi = segH[i][pl.lane];
-      segA[i][pl.lane] = a;
-      segH[i][pl.lane] = h;
-      a *= ai;
-      h = fmaf(ai, h, hi);
-    }
-    const float first = kept && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
-    const float v = chain<CW>(cn, chunk, tile, pl.lane, a, h, first);
-    enter[pl.lane] = v;
-    if (kept) {
-      if (p.checkpoints != nullptr) p.checkpoints[(bh * cn.steps + chunk) * p.d + ch] = v;
-      if (p.state_out != nullptr && chunk == cn.steps - 1) p.state_out[bh * p.d + ch] = fmaf(a, v, h);
-    }
-  }
-  __syncthreads();
-  float h[VEC];
+        for (int i = k * P::CSEG; i < (k + 1) * P::CSEG; ++i) {
+          const float ai = segA[i][pl.lane], hi = segH[i][pl.lane];
+          segA[i][pl.lane] = a;
+          segH[i][pl.lane] = h;
+          a *= ai;
+          h = fmaf(ai, h, hi);
+        }
+      }
+      const float v = chain<CW>(cn, chunk, (tl.b * nh + hl) * nct + tl.ct, pl.lane, a, h, first);
+      enter[pl.lane] = v;
+      if (kept) {
+        if (p.checkpoints != nullptr)
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    const int c = pl.lc * VEC + e;
-    h[e] = fmaf(segA[pl.seg][c], enter[c], segH[pl.seg][c]);
+          for (int k = 0; k < P::BLOCKS; ++k)
+            if (chunk * P::BLOCKS + k < nblock)
+              p.checkpoints[(bh * nblock + chunk * P::BLOCKS + k) * p.d + ch] = fmaf(ca[k], v, chh[k]);
+        if (p.state_out != nullptr && chunk == cn.steps - 1) p.state_out[bh * p.d + ch] = fmaf(a, v, h);
+      }
+    }
+    __syncthreads();
+    float h[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const int c = pl.lc * VEC + e;
+      h[e] = fmaf(segA[pl.seg][c], enter[c], segH[pl.seg][c]);
+    }
+    const unsigned after = tickets[0];
+    th.replay(chunk, h);
+    if (next >= total) break;
+    __syncthreads();  // the segments and the ticket are read
+    cur = next;
+    next = after;
+    tl = nt;
   }
-  th.replay(chunk, h);
 }
 
 // ---- Backward ----
@@ -359,9 +506,9 @@ __global__ __launch_bounds__(kThreads) void gated_scan_fwd_chain_kernel(GatedSca
 // G_t = a_t g_t, so a token maps G -> a_t (dy_t + G), last token first.
 // h_(t-1) comes from replaying the tile forwards from its checkpoint:
 //   dx_t = g_t (normalize: c_t g_t),  df_t = g_t (h_(t-1) [- x_t]) a_t rate sigmoid(-f_t).
-template <typename E, int VEC, int CW, bool kNorm>
+template <typename E, int VEC, int CW, int NW, bool kNorm>
 struct BwdThread {
-  using P = Place<VEC, CW>;
+  using P = Place<VEC, CW, NW>;
   using IO = VecIO<E, VEC>;
   static constexpr int S = P::S;
   const E *xp, *fp, *gyp;
@@ -373,12 +520,16 @@ struct BwdThread {
   typename IO::Raw rx[S], rf[S], rg[S];
   float x[S][VEC], cm[S][VEC], kf[S][VEC], dy[S][VEC];
 
-  __device__ __forceinline__ BwdThread(const GatedScanBwd& p, const ScanTile& t, const P& pl, float r)
-      : sx(p.sx.t), sf(p.sf.t), sgy(p.sgy.t), sgx(p.sgx.t), sgf(p.sgf.t), rate(r), T(p.T), seg(pl.seg) {
+  __device__ __forceinline__ BwdThread(const GatedScanBwd& p, const P& pl, float r)
+      : sx(p.sx.t), sf(p.sf.t), sgy(p.sgy.t), sgx(p.sgx.t), sgf(p.sgf.t), rate(r), T(p.T), seg(pl.seg) {}
+  __device__ __forceinline__ void aim_loads(const GatedScanBwd& p, const ScanTile& t, const P& pl) {
     const int c = t.c0 + pl.lc * VEC, cc = c < p.d ? c : 0;
     xp = at_row<E>(p.x, p.sx, t, cc);
     fp = at_row<E>(p.f, p.sf, t, cc);
     gyp = at_row<E>(p.grad_y, p.sgy, t, cc);
+  }
+  __device__ __forceinline__ void aim_stores(const GatedScanBwd& p, const ScanTile& t, const P& pl) {
+    const int c = t.c0 + pl.lc * VEC, cc = c < p.d ? c : 0;
     gxp = at_row<E>(p.grad_x, p.sgx, t, cc);
     gfp = at_row<E>(p.grad_f, p.sgf, t, cc);
     store = c < p.d;
@@ -392,25 +543,26 @@ struct BwdThread {
       rg[s] = IO::load(gyp + t * sgy);
     }
   }
-  __device__ __forceinline__ void unpack(int chunk) {
-    const int t0 = chunk * P::TT + seg * S;
+  __device__ __forceinline__ void unpack(int chunk, const float2* table) {
+    float2 g[S][VEC];
+    Gates<E, float2, VEC, S>::get(rf, table, rate, g);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      float f[VEC];
       IO::unpack(rx[s], x[s]);
-      IO::unpack(rf[s], f);
       IO::unpack(rg[s], dy[s]);
-      const bool in = t0 + s < T;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        float t;
-        const float m = decay_complement<E>(f[e], rate, &t);
-        cm[s][e] = in ? m : 0.0f;
-        kf[s][e] = rate * (1.0f - m) * sigmoid_neg(f[e], t);
-        x[s][e] = in ? x[s][e] : 0.0f;
-        dy[s][e] = in ? dy[s][e] : 0.0f;
+        cm[s][e] = g[s][e].x;
+        kf[s][e] = g[s][e].y;
       }
     }
+    if ((chunk + 1) * P::TT <= T) return;
+    const int t0 = chunk * P::TT + seg * S;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (t0 + s >= T) cm[s][e] = x[s][e] = dy[s][e] = 0.0f;
   }
   // the maps of the thread's tokens: h -> A h + H forwards, G -> A G + R backwards
   __device__ __forceinline__ void map(int e, float& A, float& H, float& R) const {
@@ -419,7 +571,7 @@ struct BwdThread {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       A = fmaf(-cm[s][e], A, A);
-      H = FwdThread<E, VEC, CW, kNorm>::step(cm[s][e], x[s][e], H);
+      H = FwdThread<E, VEC, CW, NW, kNorm>::step(cm[s][e], x[s][e], H);
     }
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
@@ -433,7 +585,7 @@ struct BwdThread {
     for (int s = 0; s < S; ++s) {
       const float xs = x[s][e];
       x[s][e] = kNorm ? h - xs : h;  // dh_t / da_t
-      h = FwdThread<E, VEC, CW, kNorm>::step(cm[s][e], xs, h);
+      h = FwdThread<E, VEC, CW, NW, kNorm>::step(cm[s][e], xs, h);
     }
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
@@ -455,25 +607,34 @@ struct BwdThread {
 };
 
 // One workgroup walks the tiles of a channel run from the last token on.
-template <typename E, int VEC, int CW, bool kNorm>
-__global__ __launch_bounds__(kThreads) void gated_scan_bwd_walk_kernel(GatedScanBwd p, HeadRate rates, int h0, int nh,
+template <typename E, int VEC, int CW, int NW, bool kNorm>
+__global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanBwd p, HeadRate rates, int h0, int nh,
                                                                        int nct) {
-  using P = Place<VEC, CW>;
+  using P = Place<VEC, CW, NW>;
   __shared__ float segA[2][P::NSEG][CW];
   __shared__ float segH[2][P::NSEG][CW];
   __shared__ float segG[2][P::NSEG][CW];
   const P pl;
   const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
-  BwdThread<E, VEC, CW, kNorm> th(p, tl, pl, rates.r[tl.hl]);
+  BwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[tl.hl]);
+  th.aim_loads(p, tl, pl);
+  th.aim_stores(p, tl, pl);
   const int ch = tl.c0 + pl.lane;
   const bool kept = pl.wave < 2 && pl.lane < CW && ch < p.d;  // wave 0 composes forwards, wave 1 backwards
   const long bh = static_cast<long>(tl.b) * p.H + tl.h;
   float carry = pl.wave == 1 && kept && p.grad_state_out != nullptr ? p.grad_state_out[bh * p.d + ch] : 0.0f;
-  const int nchunk = (p.T + P::TT - 1) / P::TT;
+  const int nchunk = (p.T + P::TT - 1) / P::TT, nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
   th.load(nchunk - 1);
+  const float2* table = nullptr;
+  if constexpr (sizeof(E) == 2) {
+    __shared__ float2 gate[kGateN];
+    build_gate_table(gate, th.rate, 64 * NW);
+    table = gate;
+    __syncthreads();
+  }
   for (int chunk = nchunk - 1; chunk >= 0; --chunk) {
-    th.unpack(chunk);
-    const float ckpt = pl.wave == 0 && kept ? p.checkpoints[(bh * nchunk + chunk) * p.d + ch] : 0.0f;
+    th.unpack(chunk, table);
+    const float ckpt = pl.wave == 0 && kept ? p.checkpoints[(bh * nblock + chunk * P::BLOCKS) * p.d + ch] : 0.0f;
     if (chunk > 0) th.load(chunk - 1);
     const int q = chunk & 1;
 #pragma unroll
@@ -509,69 +670,99 @@ __global__ __launch_bounds__(kThreads) void gated_scan_bwd_walk_kernel(GatedScan
   if (pl.wave == 1 && kept && p.grad_state_in != nullptr) p.grad_state_in[bh * p.d + ch] = carry;
 }
 
-// One workgroup per tile, chained from the last token on.
-template <typename E, int VEC, int CW, bool kNorm>
-__global__ __launch_bounds__(kThreads) void gated_scan_bwd_chain_kernel(GatedScanBwd p, Chain cn, HeadRate rates,
-                                                                        int h0, int nh, int nct) {
-  using P = Place<VEC, CW>;
+// Workgroups of one head on the tiles of its queue, from the last token on.
+template <typename E, int VEC, int CW, int NW, bool kNorm, bool kTable>
+__global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScanBwd p, Chain cn, HeadRate rates,
+                                                                       int h0, int nh, int nct) {
+  using P = Place<VEC, CW, NW>;
   __shared__ float segA[P::NSEG][CW];
   __shared__ float segH[P::NSEG][CW];
   __shared__ float segG[P::NSEG][CW];
   __shared__ float segB[P::NSEG][CW];  // products of A behind a segment
   __shared__ float enter[CW];
-  __shared__ unsigned shared_ticket;
-  const unsigned ticket = take_ticket(cn.ticket, &shared_ticket);
-  if (ticket >= static_cast<unsigned>(cn.steps) * cn.tiles) return;  // the whole workgroup
-  const int step = ticket / cn.tiles, tile = ticket % cn.tiles, chunk = cn.steps - 1 - step;
+  __shared__ unsigned tickets[2];
+  __shared__ float2 gate[kTable ? kGateN : 1];
   const P pl;
-  const ScanTile tl = decode_tile(tile, nct, nh, h0, CW);
-  BwdThread<E, VEC, CW, kNorm> th(p, tl, pl, rates.r[tl.hl]);
-  const int ch = tl.c0 + pl.lane;
-  const bool kept = pl.wave < 2 && pl.lane < CW && ch < p.d;
-  const long bh = static_cast<long>(tl.b) * p.H + tl.h;
-  th.load(chunk);
-  // wave 0: the state before the tile; wave 1: the gradient behind the sequence
-  float cur = 0.0f;
-  if (pl.wave == 0 && kept) cur = p.checkpoints[(bh * cn.steps + chunk) * p.d + ch];
-  if (pl.wave == 1 && kept && p.grad_state_out != nullptr) cur = p.grad_state_out[bh * p.d + ch];
-  th.unpack(chunk);
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    float A, H, R;
-    th.map(e, A, H, R);
-    segA[pl.seg][pl.lc * VEC + e] = A;
-    segH[pl.seg][pl.lc * VEC + e] = H;
-    segG[pl.seg][pl.lc * VEC + e] = R;
-  }
+  const int hl = blockIdx.x % nh, per_step = p.B * nct;
+  const unsigned total = static_cast<unsigned>(cn.steps) * per_step;
+  unsigned* counter = cn.ticket + hl * kCounterWords;
+  if (threadIdx.x < 2) tickets[threadIdx.x] = take_ticket(counter);
   __syncthreads();
-  if (pl.wave == 0 && pl.lane < CW) {
-#pragma unroll 8
-    for (int i = 0; i < P::NSEG; ++i) {
-      const float a = segA[i][pl.lane], hh = segH[i][pl.lane];
-      segH[i][pl.lane] = cur;
-      cur = fmaf(a, cur, hh);
+  unsigned cur = min(tickets[0], tickets[1]), next = max(tickets[0], tickets[1]);
+  if (cur >= total) return;  // the whole workgroup
+  const int nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
+  BwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[hl]);
+  auto tile_of = [&](unsigned ticket) __attribute__((always_inline)) {
+    const int i = ticket % per_step;
+    return decode_tile((i / nct * nh + hl) * nct + i % nct, nct, nh, h0, CW);
+  };
+  ScanTile tl = tile_of(cur);
+  th.aim_loads(p, tl, pl);
+  th.load(cn.steps - 1 - cur / per_step);
+  if constexpr (kTable) build_gate_table(gate, th.rate, 64 * NW);
+  __syncthreads();  // the table; and everyone has read the first tickets
+  for (;;) {
+    const int step = cur / per_step, chunk = cn.steps - 1 - step;
+    const int ch = tl.c0 + pl.lane;
+    const bool kept = pl.wave < 2 && pl.lane < CW && ch < p.d;
+    const long bh = static_cast<long>(tl.b) * p.H + tl.h;
+    // wave 0: the state before the tile; wave 1: the gradient behind the sequence
+    float start = 0.0f;
+    if (pl.wave == 0 && kept) start = p.checkpoints[(bh * nblock + chunk * P::BLOCKS) * p.d + ch];
+    if (pl.wave == 1 && kept && p.grad_state_out != nullptr) start = p.grad_state_out[bh * p.d + ch];
+    th.aim_stores(p, tl, pl);
+    th.unpack(chunk, kTable ? gate : nullptr);
+    ScanTile nt = tl;
+    if (next < total) {
+      nt = tile_of(next);
+      th.aim_loads(p, nt, pl);
+      th.load(cn.steps - 1 - next / per_step);
     }
-  } else if (pl.wave == 1 && pl.lane < CW) {
-    float a = 1.0f, g = 0.0f;  // the map of the segments behind
-#pragma unroll 8
-    for (int i = P::NSEG - 1; i >= 0; --i) {
-      const float ai = segA[i][pl.lane], gi = segG[i][pl.lane];
-      segB[i][pl.lane] = a;
-      segG[i][pl.lane] = g;
-      a *= ai;
-      g = fmaf(ai, g, gi);
-    }
-    const float v = chain<CW>(cn, step, tile, pl.lane, a, g, cur);
-    enter[pl.lane] = v;
-    if (kept && p.grad_state_in != nullptr && chunk == 0) p.grad_state_in[bh * p.d + ch] = fmaf(a, v, g);
-  }
-  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    const int c = pl.lc * VEC + e;
-    th.replay(e, segH[pl.seg][c], fmaf(segB[pl.seg][c], enter[c], segG[pl.seg][c]));
+    for (int e = 0; e < VEC; ++e) {
+      float A, H, R;
+      th.map(e, A, H, R);
+      segA[pl.seg][pl.lc * VEC + e] = A;
+      segH[pl.seg][pl.lc * VEC + e] = H;
+      segG[pl.seg][pl.lc * VEC + e] = R;
+    }
+    __syncthreads();
+    if (threadIdx.x == 128 && next < total) tickets[0] = take_ticket(counter);
+    if (pl.wave == 0 && pl.lane < CW) {
+#pragma unroll 8
+      for (int i = 0; i < P::NSEG; ++i) {
+        const float a = segA[i][pl.lane], hh = segH[i][pl.lane];
+        segH[i][pl.lane] = start;
+        start = fmaf(a, start, hh);
+      }
+    } else if (pl.wave == 1 && pl.lane < CW) {
+      float a = 1.0f, g = 0.0f;  // the map of the segments behind
+#pragma unroll 8
+      for (int i = P::NSEG - 1; i >= 0; --i) {
+        const float ai = segA[i][pl.lane], gi = segG[i][pl.lane];
+        segB[i][pl.lane] = a;
+        segG[i][pl.lane] = g;
+        a *= ai;
+        g = fmaf(ai, g, gi);
+      }
+      const float v = chain<CW>(cn, step, (tl.b * nh + hl) * nct + tl.ct, pl.lane, a, g, start);
+      enter[pl.lane] = v;
+      if (kept && p.grad_state_in != nullptr && chunk == 0) p.grad_state_in[bh * p.d + ch] = fmaf(a, v, g);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const int c = pl.lc * VEC + e;
+      th.replay(e, segH[pl.seg][c], fmaf(segB[pl.seg][c], enter[c], segG[pl.seg][c]));
+    }
+    const unsigned after = tickets[0];
+    th.write(chunk);
+    if (next >= total) break;
+    __syncthreads();  // the segments and the ticket are read
+    cur = next;
+    next = after;
+    tl = nt;
   }
-  th.write(chunk);
 }
 
 // One token: state <- a state + u, y = state; one thread per VEC channels.
@@ -600,7 +791,7 @@ __global__ __launch_bounds__(256) void gated_scan_step_kernel(GatedScanFwd p, He
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
     float t;
-    const float m = decay_complement<E>(f[e], rates.r[hl], &t);
+    const float m = decay_complement(f[e], rates.r[hl], &t);
     st[e] = kNorm ? fmaf(m, x[e] - st[e], st[e]) : fmaf(-m, st[e], st[e]) + x[e];
   }
   if (p.state_out != nullptr) VecIO<float, VEC>::store(p.state_out + row, st);
@@ -616,14 +807,15 @@ HeadRate head_rates(const HeadGroup& g) {
 // Tile width for a row of d channels: 64, or the next power of two for
 // narrow rows so that lanes are not left idle.
 int tile_width(int d) { return d > 32 ? 64 : d > 16 ? 32 : 16; }
+int tile_tokens(int d, int waves) { return waves * (kPerThread * 64 / tile_width(d)); }
 
 // The chained kernels' part of the workspace for a launch of nh heads.
 struct ChainSizes {
   int steps, tiles;
   size_t maps, enter;  // words of 8 and of 4 bytes
 };
-ChainSizes chain_sizes(int B, int nh, int T, int d) {
-  const int cw = tile_width(d), tt = gated_scan_block(d);
+ChainSizes chain_sizes(int B, int nh, int T, int d, int waves) {
+  const int cw = tile_width(d), tt = tile_tokens(d, waves);
   ChainSizes z;
   z.steps = (T + tt - 1) / tt;
   z.tiles = B * nh * ((d + cw - 1) / cw);
@@ -635,34 +827,51 @@ ChainSizes chain_sizes(int B, int nh, int T, int d) {
 // Whether the tiles of a channel run are chained over workgroups (else one
 // workgroup walks them).
 bool chained(int B, int H, int T, int d) {
-  const ChainSizes z = chain_sizes(B, H < kHeadsPerLaunch ? H : kHeadsPerLaunch, T, d);
+  const ChainSizes z = chain_sizes(B, H < kHeadsPerLaunch ? H : kHeadsPerLaunch, T, d, kBlockWaves);
   return z.steps > 1 && z.tiles < kWalkTiles;
 }
 
-hipError_t make_chain(void* ws, int B, int nh, int T, int d, Chain* c, hipStream_t s) {
-  const ChainSizes z = chain_sizes(B, nh, T, d);
-  char* base = static_cast<char*>(ws);
-  c->ticket = reinterpret_cast<unsigned*>(base);
-  c->maps = reinterpret_cast<u64*>(base + kChainHead);
-  c->enter = reinterpret_cast<unsigned*>(base + kChainHead + z.maps * 8);
+// [ticket counters][maps][enter], all ones at the start.
+hipError_t make_chain(void* ws, int B, int nh, int T, int d, int waves, Chain* c, hipStream_t s) {
+  const ChainSizes z = chain_sizes(B, nh, T, d, waves);
+  c->ticket = static_cast<unsigned*>(ws);
+  c->maps = reinterpret_cast<u64*>(c->ticket + nh * kCounterWords);
+  c->enter = reinterpret_cast<unsigned*>(c->maps + z.maps);
   c->steps = z.steps;
   c->tiles = z.tiles;
-  return launch_fill_u32(c->maps, z.maps * 2 + z.enter, 0xFFFFFFFFu, s, c->ticket, 0);
+  return launch_fill_u32(ws, static_cast<size_t>(nh) * kCounterWords + z.maps * 2 + z.enter, 0xFFFFFFFFu, s);
 }
+
+// Workgroups of a chained launch: as many as fit the device for each head, at
+// most one for each of its tiles.
+int chain_blocks(const Chain& c, int nh, int per_cu) {
+  const long per_head = static_cast<long>(c.steps) * (c.tiles / nh);
+  const long want = 256L * per_cu / nh > 1 ? 256L * per_cu / nh : 1;
+  return nh * static_cast<int>(want < per_head ? want : per_head);
+}
+// A gate table pays once a workgroup works on several tiles.
+bool use_table(const Chain& c, int blocks) { return static_cast<long>(c.steps) * c.tiles >= kTableTiles * blocks; }
 
 template <typename E, int VEC, int CW, bool kNorm>
 hipError_t run_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int nct = (p.d + CW - 1) / CW;
   if (!chained(p.B, p.H, p.T, p.d)) {
-    hipLaunchKernelGGL((gated_scan_fwd_walk_kernel<E, VEC, CW, kNorm>), dim3(p.B * g.nh * nct), dim3(kThreads), 0, s,
-                       p, head_rates(g), g.h0, g.nh, nct);
+    constexpr int NW = VEC == 1 ? 8 : 16;
+    hipLaunchKernelGGL((gated_scan_fwd_walk_kernel<E, VEC, CW, NW, kNorm>), dim3(p.B * g.nh * nct), dim3(64 * NW), 0,
+                       s, p, head_rates(g), g.h0, g.nh, nct);
     return hipGetLastError();
   }
+  constexpr int NW = 8;
   Chain c;
-  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, &c, s);
+  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, NW, &c, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, kNorm>), dim3(c.steps * c.tiles), dim3(kThreads), 0, s,
-                     p, c, head_rates(g), g.h0, g.nh, nct);
+  const int blocks = chain_blocks(c, g.nh, 3);
+  if (sizeof(E) == 2 && use_table(c, blocks))
+    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, kNorm, sizeof(E) == 2>), dim3(blocks), dim3(64 * NW),
+                       0, s, p, c, head_rates(g), g.h0, g.nh, nct);
+  else
+    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, kNorm, false>), dim3(blocks), dim3(64 * NW), 0, s,
+                       p, c, head_rates(g), g.h0, g.nh, nct);
   return hipGetLastError();
 }
 
@@ -678,15 +887,22 @@ template <typename E, int VEC, int CW, bool kNorm>
 hipError_t run_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int nct = (p.d + CW - 1) / CW;
   if (!chained(p.B, p.H, p.T, p.d)) {
-    hipLaunchKernelGGL((gated_scan_bwd_walk_kernel<E, VEC, CW, kNorm>), dim3(p.B * g.nh * nct), dim3(kThreads), 0, s,
-                       p, head_rates(g), g.h0, g.nh, nct);
+    constexpr int NW = sizeof(E) == 4 || VEC == 1 ? 8 : 16;  // what fits 512 / (NW / 4) registers without spills
+    hipLaunchKernelGGL((gated_scan_bwd_walk_kernel<E, VEC, CW, NW, kNorm>), dim3(p.B * g.nh * nct), dim3(64 * NW), 0,
+                       s, p, head_rates(g), g.h0, g.nh, nct);
     return hipGetLastError();
   }
+  constexpr int NW = 8;
   Chain c;
-  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, &c, s);
+  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, NW, &c, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, kNorm>), dim3(c.steps * c.tiles), dim3(kThreads), 0, s,
-                     p, c, head_rates(g), g.h0, g.nh, nct);
+  const int blocks = chain_blocks(c, g.nh, 1);
+  if (sizeof(E) == 2 && use_table(c, blocks))
+    hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, NW, kNorm, sizeof(E) == 2>), dim3(blocks), dim3(64 * NW),
+                       0, s, p, c, head_rates(g), g.h0, g.nh, nct);
+  else
+    hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, NW, kNorm, false>), dim3(blocks), dim3(64 * NW), 0, s,
+                       p, c, head_rates(g), g.h0, g.nh, nct);
   return hipGetLastError();
 }
 
@@ -729,12 +945,13 @@ hipError_t step_by_vec(int vec, const GatedScanFwd& p, const HeadGroup& g, hipSt
 
 }  // namespace
 
-int gated_scan_block(int d) { return kWaves * (kPerThread * 64 / tile_width(d)); }
+int gated_scan_block(int d) { return tile_tokens(d, kBlockWaves); }
 
 size_t gated_scan_chain_bytes(int B, int H, int T, int d) {
   if (T <= 1 || !chained(B, H, T, d)) return 0;
-  const ChainSizes z = chain_sizes(B, H < kHeadsPerLaunch ? H : kHeadsPerLaunch, T, d);
-  return kChainHead + z.maps * 8 + z.enter * 4;
+  const int nh = H < kHeadsPerLaunch ? H : kHeadsPerLaunch;
+  const ChainSizes z = chain_sizes(B, nh, T, d, kBlockWaves);  // wider workgroups have fewer tiles
+  return static_cast<size_t>(nh) * kCounterWords * 4 + z.maps * 8 + z.enter * 4;
 }
 
 hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
