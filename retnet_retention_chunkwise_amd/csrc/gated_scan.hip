@@ -16,6 +16,7 @@
 // NSEG segments in time order, and every thread replays its tokens from its
 // incoming value.  x and f are read once and y is written once.
 #include "common.h"
+#include "gfx950.h"
 #include "kernels.h"
 #include "vec_io.h"
 
@@ -26,8 +27,8 @@
 namespace ret {
 namespace {
 
-constexpr int kPerThread = 16;  // VEC * S
-constexpr int kBlockWaves = 8;  // a checkpoint's block is the tile of a workgroup of 8 waves
+constexpr int kPerThread = 16;   // VEC * S of most kernels
+constexpr int kBlockElems = 128;  // a checkpoint's block: as many elements per lane (8 waves of 16)
 // Channel runs from which on each is walked by one workgroup.  Measured at 256
 // runs (one for each compute unit): walking 50 us and chaining 68 us (B4 H8
 // T2048 d512, bf16), 515 and 665 us (B2 H16 T8192 d512 forward and backward);
@@ -130,36 +131,36 @@ struct Gates {
       for (int e = 0; e < VEC; ++e) gate_value(f[e], rate, &out[s][e]);
     }
   }
-  // by table when one is given (bf16 only)
+  // by table (bf16 only) or directly
+  template <bool kTable>
   __device__ __forceinline__ static void get(const typename IO::Raw (&rf)[S], const Entry* table, float rate,
                                              Entry (&out)[S][VEC]) {
-    if constexpr (sizeof(E) == 2) {
-      if (table != nullptr) {  // known at compile time
-        u16x2 top = 0;
+    if constexpr (!kTable) {
+      direct(rf, rate, out);
+    } else {
+      static_assert(sizeof(E) == 2, "gate tables are of bf16 values");
+      u16x2 top = 0;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-          if constexpr (VEC == 1) {
-            u16x2 two;
-            two[0] = two[1] = rf[s];
-            out[s][0] = table[gate_index(two, top)[0]];
-          } else if constexpr (VEC == 2) {
-            const u16x2 i = gate_index(__builtin_bit_cast(u16x2, rf[s]), top);
-            out[s][0] = table[i[0]];
-            out[s][1] = table[i[1]];
-          } else {
+      for (int s = 0; s < S; ++s) {
+        if constexpr (VEC == 1) {
+          u16x2 two;
+          two[0] = two[1] = rf[s];
+          out[s][0] = table[gate_index(two, top)[0]];
+        } else if constexpr (VEC == 2) {
+          const u16x2 i = gate_index(__builtin_bit_cast(u16x2, rf[s]), top);
+          out[s][0] = table[i[0]];
+          out[s][1] = table[i[1]];
+        } else {
 #pragma unroll
-            for (int v = 0; v < VEC / 2; ++v) {
-              const u16x2 i = gate_index(__builtin_bit_cast(u16x2, static_cast<unsigned>(rf[s][v])), top);
-              out[s][2 * v] = table[i[0]];
-              out[s][2 * v + 1] = table[i[1]];
-            }
+          for (int v = 0; v < VEC / 2; ++v) {
+            const u16x2 i = gate_index(__builtin_bit_cast(u16x2, static_cast<unsigned>(rf[s][v])), top);
+            out[s][2 * v] = table[i[0]];
+            out[s][2 * v + 1] = table[i[1]];
           }
         }
-        if (__any(top[0] >= kGateN || top[1] >= kGateN)) direct(rf, rate, out);
-        return;
       }
+      if (__any(top[0] >= kGateN || top[1] >= kGateN)) direct(rf, rate, out);
     }
-    direct(rf, rate, out);
   }
 };
 
@@ -182,26 +183,34 @@ __device__ __forceinline__ ScanTile decode_tile(int tile, int nct, int nh, int h
 //
 // With few channels and many tokens the tiles of one channel run must work at
 // the same time, each on its own tokens, and still hand their state on.  The
-// workgroups of a head take tickets; tickets go through the head's tiles of
-// step 0 of the walk (the first tokens, or the last ones backwards), then step
-// 1, ...  A workgroup publishes its tile's map (A, H), takes the value that
-// enters its group of kGroup steps and folds the maps of the group's earlier
-// steps into it; the last step of a group publishes the value that enters the
-// next group.  The order of all additions is fixed by the sizes, so results do
-// not depend on timing.  A workgroup works on its tickets in order, taking the
-// next one early to have its tile's loads in flight, and waits only for lower
-// tickets: the lowest unfinished ticket of all is being worked on and waits for
-// nothing, so every wait ends.  A wait of more than kSpinLimit polls (two calls
-// on one workspace at the same time, which the interface forbids) gives NaN
-// instead of hanging.  Published words carry their own "ready": the workspace
-// is filled with ones before the launch and no published NaN has that pattern.
-constexpr int kGroup = 16;
+// workgroups of a head take tickets, which go through the head's tiles of step
+// 0 of the walk (the first tokens, or the last ones backwards), then step 1,
+// ...  A workgroup publishes its tile's map (A, H), takes the value that enters
+// its group of kGroup steps and folds the maps of the group's earlier steps
+// into it; the last step of a group publishes the value that enters the next
+// group.  The order of all additions is fixed by the sizes, so results do not
+// depend on timing.
+//
+// Every wait ends: a workgroup works on its tickets in order, waits only for
+// words of lower tickets and publishes its tile's map before it waits, so the
+// lowest ticket that is not yet done is never held up.  A wait of more than
+// kSpinLimit polls (two calls on one workspace at the same time, which the
+// interface forbids) gives NaN instead of hanging.  Published words carry
+// their own "ready": the workspace is filled with ones before the launch and
+// no published NaN has that pattern.
+//
+// A word takes microseconds to reach another workgroup while the memory is
+// busy, so the tiles are large and several workgroups share a compute unit.
+// (Measured slower: waves that fold all maps of a channel run and publish every
+// tile's entering value, with twice the hops; replaying a tile one later.)
+constexpr int kGroup = 8;
 constexpr int kSpinLimit = 1 << 20;
-constexpr int kCounterWords = 16;  // a head's ticket counter has a cache line's half to itself
+constexpr int kCounterWords = 16;  // a counter has half a cache line to itself
+
 struct Chain {
-  unsigned* ticket;  // [heads of the launch][kCounterWords]
-  u64* maps;        // [steps][tiles][CW]: A in the low word, H in the high word
-  unsigned* enter;  // [groups][tiles][CW]: the value that enters a group
+  unsigned* counters;  // [heads of the launch][kCounterWords]: the heads' tickets
+  u64* maps;           // [steps][tiles][CW]: A in the low word, H in the high word
+  unsigned* enter;     // [groups][tiles][CW]: the value that enters a group
   int steps, tiles;
 };
 
@@ -217,51 +226,85 @@ __device__ __forceinline__ W wait_word(const W* p, W seen, W otherwise) {
   return seen;
 }
 
-// The value that enters the tile at step j, for the lane's channel; (A, H) is
-// the tile's map and first the value that enters step 0.
-template <int CW>
-__device__ __forceinline__ float chain(const Chain& c, int j, int tile, int lane, float A, float H, float first) {
-  const long per = static_cast<long>(c.tiles) * CW, at = static_cast<long>(tile) * CW + lane;
-  const int k = j % kGroup, g = j / kGroup;
-  const bool last = j == c.steps - 1;
-  if (k != kGroup - 1 && !last)
-    __hip_atomic_store(c.maps + j * per + at, static_cast<u64>(quiet(H)) << 32 | quiet(A), __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-  const unsigned* enter = c.enter + g * per + at;
-  unsigned e = 0;
-  u64 m[kGroup - 1];
-  if (g > 0) e = __hip_atomic_load(enter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const u64* maps = c.maps + static_cast<long>(g) * kGroup * per + at;
-#pragma unroll
-  for (int i = 0; i < kGroup - 1; ++i)
-    if (i < k) m[i] = __hip_atomic_load(maps + i * per, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  float v = g > 0 ? __uint_as_float(wait_word(enter, e, 0x7fc00000u)) : first;
-#pragma unroll
-  for (int i = 0; i < kGroup - 1; ++i)
-    if (i < k) {
-      const u64 r = wait_word(maps + i * per, m[i], static_cast<u64>(0x7fc000007fc00000ull));
-      v = fmaf(__uint_as_float(static_cast<unsigned>(r)), v, __uint_as_float(static_cast<unsigned>(r >> 32)));
-    }
-  if (k == kGroup - 1 && !last)
-    __hip_atomic_store(c.enter + (g + 1) * per + at, quiet(fmaf(A, v, H)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return v;
-}
+// A word of LDS that the whole wave reads, as a scalar.
+__device__ __forceinline__ unsigned uniform(unsigned x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// The next ticket of a head's queue (counters start one below 0).
-__device__ __forceinline__ unsigned take_ticket(unsigned* counter) {
+// The next number of a counter (counters start one below 0).
+__device__ __forceinline__ unsigned take(unsigned* counter) {
   return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
 }
 
+// Hands a tile's map on: the lane's channel of the tile at step j.
+template <int CW>
+__device__ __forceinline__ void publish_map(const Chain& c, int j, int tile, int lane, float A, float H) {
+  if (j % kGroup == kGroup - 1 || j == c.steps - 1) return;  // nobody folds it
+  const long per = static_cast<long>(c.tiles) * CW;
+  __hip_atomic_store(c.maps + j * per + static_cast<long>(tile) * CW + lane, static_cast<u64>(quiet(H)) << 32 | quiet(A),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The value that enters the tile at step j, for the lane's channel: begin()
+// requests the published words, end() waits for them and folds them.
+template <int CW>
+struct Entering {
+  u64 m[kGroup - 1];
+  unsigned e;
+  __device__ __forceinline__ void begin(const Chain& c, int j, int tile, int lane) {
+    const long per = static_cast<long>(c.tiles) * CW, at = static_cast<long>(tile) * CW + lane;
+    const int k = j % kGroup, g = j / kGroup;
+    if (g > 0) e = __hip_atomic_load(c.enter + g * per + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const u64* maps = c.maps + static_cast<long>(g) * kGroup * per + at;
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+      if (i < k) m[i] = __hip_atomic_load(maps + i * per, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  // (A, H): the tile's map; first: the value that enters step 0
+  __device__ __forceinline__ float end(const Chain& c, int j, int tile, int lane, float A, float H, float first) const {
+    const long per = static_cast<long>(c.tiles) * CW, at = static_cast<long>(tile) * CW + lane;
+    const int k = j % kGroup, g = j / kGroup;
+    const u64* maps = c.maps + static_cast<long>(g) * kGroup * per + at;
+    float v = g > 0 ? __uint_as_float(wait_word(c.enter + g * per + at, e, 0x7fc00000u)) : first;
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+      if (i < k) {
+        const u64 r = wait_word(maps + i * per, m[i], static_cast<u64>(0x7fc000007fc00000ull));
+        v = fmaf(__uint_as_float(static_cast<unsigned>(r)), v, __uint_as_float(static_cast<unsigned>(r >> 32)));
+      }
+    if (k == kGroup - 1 && j != c.steps - 1)
+      __hip_atomic_store(c.enter + (g + 1) * per + at, quiet(fmaf(A, v, H)), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    return v;
+  }
+};
+
+// A head's queue of tiles: ticket -> step and tile (b, column tile).
+struct Queue {
+  unsigned* counter;
+  unsigned per_step, total;
+  int hl, h0, nh, nct;
+  __device__ __forceinline__ Queue(const Chain& c, int head, int h0_, int nh_, int nct_, int B)
+      : counter(c.counters + head * kCounterWords), per_step(B * nct_), total(static_cast<unsigned>(c.steps) * B * nct_),
+        hl(head), h0(h0_), nh(nh_), nct(nct_) {}
+  __device__ __forceinline__ unsigned take() const { return ret::take(counter); }
+  __device__ __forceinline__ int step(unsigned ticket) const { return ticket / per_step; }
+  template <int CW>
+  __device__ __forceinline__ ScanTile tile(unsigned ticket) const {
+    const int i = ticket % per_step;
+    return decode_tile((i / nct * nh + hl) * nct + i % nct, nct, nh, h0, CW);
+  }
+  __device__ __forceinline__ int number(const ScanTile& t) const { return (t.b * nh + hl) * nct + t.ct; }
+};
+
 // Where a thread stands in its tile.
-template <int VEC, int CW, int NW>
+template <int VEC, int CW, int NW, int PT = kPerThread>
 struct Place {
-  static constexpr int S = kPerThread / VEC, LC = CW / VEC, TG = 64 / LC, NSEG = NW * TG, TT = NSEG * S;
-  // checkpoints lie every kBlockWaves waves of a tile
-  static constexpr int CSEG = kBlockWaves * TG, BLOCKS = NW / kBlockWaves, BLOCK = TT / BLOCKS;
+  static constexpr int S = PT / VEC, LC = CW / VEC, TG = 64 / LC, NSEG = NW * TG, TT = NSEG * S;
+  // a tile's checkpoints
+  static constexpr int BLOCKS = NW * PT / kBlockElems, CSEG = NSEG / BLOCKS, BLOCK = TT / BLOCKS;
   int lane, wave, lc, seg;
   __device__ Place()
-      : lane(threadIdx.x & 63), wave(threadIdx.x >> 6), lc((threadIdx.x & 63) % LC),
-        seg((threadIdx.x >> 6) * TG + (threadIdx.x & 63) / LC) {}
+      : lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), lc((threadIdx.x & 63) % LC),
+        seg(wave * TG + (threadIdx.x & 63) / LC) {}
 };
 
 template <typename E>
@@ -270,11 +313,11 @@ __device__ __forceinline__ E* at_row(const void* p, const Strides3& s, const Sca
 }
 
 // ---- Forward ----
-template <typename E, int VEC, int CW, int NW, bool kNorm>
+template <typename E, int VEC, int CW, int NW, int PT, bool kNorm>
 struct FwdThread {
-  using P = Place<VEC, CW, NW>;
+  using P = Place<VEC, CW, NW, PT>;
   using IO = VecIO<E, VEC>;
-  static constexpr int S = P::S;
+  static constexpr int S = P::S, kAhead = VEC >= 4 ? 2 : 8 / VEC;
   const E *xp, *fp;
   E* yp;
   long sx, sf, sy;
@@ -304,8 +347,9 @@ struct FwdThread {
       rf[s] = IO::load(fp + t * sf);
     }
   }
+  template <bool kTable>
   __device__ __forceinline__ void unpack(int chunk, const float* table) {
-    Gates<E, float, VEC, S>::get(rf, table, rate, cm);
+    Gates<E, float, VEC, S>::template get<kTable>(rf, table, rate, cm);
 #pragma unroll
     for (int s = 0; s < S; ++s) IO::unpack(rx[s], x[s]);
     if ((chunk + 1) * P::TT <= T) return;  // uniform; else tokens past the end leave the state as it is
@@ -332,13 +376,71 @@ struct FwdThread {
       }
     }
   }
-  // the thread's tokens from their incoming value
-  __device__ __forceinline__ void replay(int chunk, float (&h)[VEC]) const {
+  // The same straight from the packed registers, row by row.  With a table the
+  // gates are looked up again for the replay; without one they stay in cm.
+  template <bool kTable>
+  __device__ __forceinline__ void packed_map(int chunk, const float* table, float (&A)[VEC], float (&H)[VEC]) {
+    const int t0 = chunk * P::TT + seg * S;
+    const bool whole = (chunk + 1) * P::TT <= T;  // uniform
+    if constexpr (!kTable) Gates<E, float, VEC, S>::direct(rf, rate, cm);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      A[e] = 1.0f;
+      H[e] = 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      // a few rows' lookups at a time: all at once would take a register for each
+      if (kTable && s % kAhead == 0) __builtin_amdgcn_sched_barrier(0);
+      float c[1][VEC], u[VEC];
+      row<kTable>(s, table, c, u);
+      if (!whole && t0 + s >= T) continue;  // tokens past the end leave the state as it is
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        A[e] = fmaf(-c[0][e], A[e], A[e]);
+        H[e] = step(c[0][e], u[e], H[e]);
+      }
+    }
+  }
+  template <bool kTable>
+  __device__ __forceinline__ void packed_replay(int chunk, const float* table, float (&h)[VEC]) {
+    const int t0 = chunk * P::TT + seg * S;
+    if constexpr (kTable) {
+      // the compiler would otherwise keep the map's gates in registers, twice as many as the packed ones
+#pragma unroll
+      for (int s = 0; s < S; ++s) asm("" : "+v"(rx[s]), "+v"(rf[s]));
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      // a few rows' lookups at a time: all at once would take a register for each
+      if (kTable && s % kAhead == 0) __builtin_amdgcn_sched_barrier(0);
+      float c[1][VEC], u[VEC];
+      row<kTable>(s, table, c, u);
+      if (t0 + s >= T) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) h[e] = step(c[0][e], u[e], h[e]);
+      if (store) IO::store(yp + (t0 + s) * sy, h);
+    }
+  }
+  template <bool kTable>
+  __device__ __forceinline__ void row(int s, const float* table, float (&c)[1][VEC], float (&u)[VEC]) {
+    if constexpr (kTable) {
+      const typename IO::Raw one[1] = {rf[s]};
+      Gates<E, float, VEC, 1>::template get<true>(one, table, rate, c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) c[0][e] = cm[s][e];
+    }
+    IO::unpack(rx[s], u);
+  }
+  // a thread's tokens (c, u) from their incoming value
+  __device__ __forceinline__ void replay(int chunk, const float (&c)[S][VEC], const float (&u)[S][VEC],
+                                         float (&h)[VEC]) const {
     const int t0 = chunk * P::TT + seg * S;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) h[e] = step(cm[s][e], x[s][e], h[e]);
+      for (int e = 0; e < VEC; ++e) h[e] = step(c[s][e], u[s][e], h[e]);
       if (store && t0 + s < T) IO::store(yp + (t0 + s) * sy, h);
     }
   }
@@ -353,7 +455,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
   __shared__ float segH[2][P::NSEG][CW];
   const P pl;
   const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
-  FwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[tl.hl]);
+  FwdThread<E, VEC, CW, NW, kPerThread, kNorm> th(p, pl, rates.r[tl.hl]);
   th.aim_loads(p, tl, pl);
   th.aim_stores(p, tl, pl);
   // the composing wave: one channel per lane
@@ -363,15 +465,14 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
   float carry = kept && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
   const int nchunk = (p.T + P::TT - 1) / P::TT, nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
   th.load(0);
-  const float* table = nullptr;
-  if constexpr (sizeof(E) == 2) {
-    __shared__ float gate[kGateN];
+  constexpr bool kTable = sizeof(E) == 2;
+  __shared__ float gate[kTable ? kGateN : 1];
+  if constexpr (kTable) {
     build_gate_table(gate, th.rate, 64 * NW);
-    table = gate;
     __syncthreads();
   }
   for (int chunk = 0; chunk < nchunk; ++chunk) {
-    th.unpack(chunk, table);
+    th.template unpack<kTable>(chunk, gate);
     if (chunk + 1 < nchunk) th.load(chunk + 1);
     const int q = chunk & 1;
     float A[VEC], H[VEC];
@@ -399,66 +500,56 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
     float h[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) h[e] = segH[q][pl.seg][pl.lc * VEC + e];
-    th.replay(chunk, h);
+    th.replay(chunk, th.cm, th.x, h);
   }
   if (kept && p.state_out != nullptr) p.state_out[bh * p.d + ch] = carry;
 }
 
 // Workgroups of one head (blockIdx modulo the heads) on the tiles of its queue.
-template <typename E, int VEC, int CW, int NW, bool kNorm, bool kTable>
-__global__ __launch_bounds__(64 * NW) void gated_scan_fwd_chain_kernel(GatedScanFwd p, Chain cn, HeadRate rates,
+// A thread keeps its PT elements packed as they were read and evaluates their
+// gates twice, for the tile's map and for the replay: by table that is cheap,
+// and few registers let two workgroups with 256-token tiles share a compute
+// unit.  Without a table the tiles are half as long.
+template <typename E, int VEC, int CW, int NW, int PT, bool kNorm, bool kTable>
+__global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedScanFwd p, Chain cn, HeadRate rates,
                                                                        int h0, int nh, int nct) {
-  using P = Place<VEC, CW, NW>;
+  using P = Place<VEC, CW, NW, PT>;
+  using Th = FwdThread<E, VEC, CW, NW, PT, kNorm>;
+  constexpr int S = P::S;
   __shared__ float segA[P::NSEG][CW];
   __shared__ float segH[P::NSEG][CW];
   __shared__ float enter[CW];
-  __shared__ unsigned tickets[2];
+  __shared__ unsigned ticket;
   __shared__ float gate[kTable ? kGateN : 1];
   const P pl;
-  const int hl = blockIdx.x % nh, per_step = p.B * nct;
-  const unsigned total = static_cast<unsigned>(cn.steps) * per_step;
-  unsigned* counter = cn.ticket + hl * kCounterWords;
-  if (threadIdx.x < 2) tickets[threadIdx.x] = take_ticket(counter);
-  __syncthreads();
-  // the two lanes' additions may be served in either order
-  unsigned cur = min(tickets[0], tickets[1]), next = max(tickets[0], tickets[1]);
-  if (cur >= total) return;  // the whole workgroup
-  const int nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
-  FwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[hl]);
-  // a ticket's tile: (b, column tile) of this head at one step
-  auto tile_of = [&](unsigned ticket) __attribute__((always_inline)) {
-    const int i = ticket % per_step;
-    return decode_tile((i / nct * nh + hl) * nct + i % nct, nct, nh, h0, CW);
-  };
-  ScanTile tl = tile_of(cur);
-  th.aim_loads(p, tl, pl);
-  th.load(cur / per_step);
+  const Queue qu(cn, blockIdx.x % nh, h0, nh, nct, p.B);
+  if (threadIdx.x == 0) ticket = qu.take();
+  Th th(p, pl, rates.r[qu.hl]);
   if constexpr (kTable) build_gate_table(gate, th.rate, 64 * NW);
-  __syncthreads();  // the table; and everyone has read the first tickets
-  for (;;) {
-    const int chunk = cur / per_step;
+  __syncthreads();
+  const int nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
+  for (unsigned cur = uniform(ticket); cur < qu.total;) {
+    const int chunk = qu.step(cur);
+    const ScanTile tl = qu.template tile<CW>(cur);
+    th.aim_loads(p, tl, pl);
     th.aim_stores(p, tl, pl);
-    th.unpack(chunk, kTable ? gate : nullptr);
+    th.load(chunk);
     float A[VEC], H[VEC];
-    th.map(A, H);
-    ScanTile nt = tl;
-    if (next < total) {
-      nt = tile_of(next);
-      th.aim_loads(p, nt, pl);
-      th.load(next / per_step);
-    }
+    th.template packed_map<kTable>(chunk, gate, A, H);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       segA[pl.seg][pl.lc * VEC + e] = A[e];
       segH[pl.seg][pl.lc * VEC + e] = H[e];
     }
     __syncthreads();
-    if (threadIdx.x == 64 && next < total) tickets[0] = take_ticket(counter);
+    if (threadIdx.x == 64) ticket = qu.take();
     if (pl.wave == 0 && pl.lane < CW) {
-      const int ch = tl.c0 + pl.lane;
+      const int ch = tl.c0 + pl.lane, tile = qu.number(tl);
       const long bh = static_cast<long>(tl.b) * p.H + tl.h;
       const bool kept = ch < p.d;
-      const float first = kept && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
+      Entering<CW> in;
+      in.begin(cn, chunk, tile, pl.lane);
+      const float first = kept && chunk < kGroup && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
       float a = 1.0f, h = 0.0f, ca[P::BLOCKS], chh[P::BLOCKS];  // the map of the segments so far, and at the blocks
 #pragma unroll
       for (int k = 0; k < P::BLOCKS; ++k) {
@@ -473,7 +564,8 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_chain_kernel(GatedScan
           h = fmaf(ai, h, hi);
         }
       }
-      const float v = chain<CW>(cn, chunk, (tl.b * nh + hl) * nct + tl.ct, pl.lane, a, h, first);
+      publish_map<CW>(cn, chunk, tile, pl.lane, a, h);
+      const float v = in.end(cn, chunk, tile, pl.lane, a, h, first);
       enter[pl.lane] = v;
       if (kept) {
         if (p.checkpoints != nullptr)
@@ -491,13 +583,9 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_chain_kernel(GatedScan
       const int c = pl.lc * VEC + e;
       h[e] = fmaf(segA[pl.seg][c], enter[c], segH[pl.seg][c]);
     }
-    const unsigned after = tickets[0];
-    th.replay(chunk, h);
-    if (next >= total) break;
-    __syncthreads();  // the segments and the ticket are read
-    cur = next;
-    next = after;
-    tl = nt;
+    cur = uniform(ticket);
+    th.template packed_replay<kTable>(chunk, gate, h);
+    __syncthreads();  // the segments, the entering values and the ticket are read
   }
 }
 
@@ -543,9 +631,10 @@ struct BwdThread {
       rg[s] = IO::load(gyp + t * sgy);
     }
   }
+  template <bool kTable>
   __device__ __forceinline__ void unpack(int chunk, const float2* table) {
     float2 g[S][VEC];
-    Gates<E, float2, VEC, S>::get(rf, table, rate, g);
+    Gates<E, float2, VEC, S>::template get<kTable>(rf, table, rate, g);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       IO::unpack(rx[s], x[s]);
@@ -571,7 +660,7 @@ struct BwdThread {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       A = fmaf(-cm[s][e], A, A);
-      H = FwdThread<E, VEC, CW, NW, kNorm>::step(cm[s][e], x[s][e], H);
+      H = FwdThread<E, VEC, CW, NW, kPerThread, kNorm>::step(cm[s][e], x[s][e], H);
     }
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
@@ -579,29 +668,32 @@ struct BwdThread {
       R = fmaf(-cm[s][e], g, g);
     }
   }
-  // replays the tokens of element e from h before them and G behind them
-  __device__ __forceinline__ void replay(int e, float h, float G) {
+  // replays the tokens of element e forwards from h: kf becomes dy_t -> df_t, a_t h'_t with h'_t = dh_t / da_t
+  __device__ __forceinline__ void replay_state(int e, float h) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const float xs = x[s][e];
-      x[s][e] = kNorm ? h - xs : h;  // dh_t / da_t
-      h = FwdThread<E, VEC, CW, NW, kNorm>::step(cm[s][e], xs, h);
-    }
-#pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-      const float g = dy[s][e] + G;
-      G = fmaf(-cm[s][e], g, g);
-      dy[s][e] = kNorm ? g * cm[s][e] : g;
-      x[s][e] = g * x[s][e] * kf[s][e];
+      kf[s][e] *= kNorm ? h - x[s][e] : h;
+      h = FwdThread<E, VEC, CW, NW, kPerThread, kNorm>::step(cm[s][e], x[s][e], h);
     }
   }
-  __device__ __forceinline__ void write(int chunk) const {
+  // and backwards from G behind them: g becomes dx, k becomes df
+  __device__ __forceinline__ static void replay_grad(int e, float G, const float (&c)[S][VEC], float (&g)[S][VEC],
+                                                     float (&k)[S][VEC]) {
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+      const float gs = g[s][e] + G;
+      G = fmaf(-c[s][e], gs, gs);
+      g[s][e] = kNorm ? gs * c[s][e] : gs;
+      k[s][e] *= gs;
+    }
+  }
+  __device__ __forceinline__ void write(int chunk, const float (&dx)[S][VEC], const float (&df)[S][VEC]) const {
     const int t0 = chunk * P::TT + seg * S;
 #pragma unroll
     for (int s = 0; s < S; ++s)
       if (store && t0 + s < T) {
-        IO::store(gxp + (t0 + s) * sgx, dy[s]);
-        IO::store(gfp + (t0 + s) * sgf, x[s]);
+        IO::store(gxp + (t0 + s) * sgx, dx[s]);
+        IO::store(gfp + (t0 + s) * sgf, df[s]);
       }
   }
 };
@@ -625,15 +717,14 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanB
   float carry = pl.wave == 1 && kept && p.grad_state_out != nullptr ? p.grad_state_out[bh * p.d + ch] : 0.0f;
   const int nchunk = (p.T + P::TT - 1) / P::TT, nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
   th.load(nchunk - 1);
-  const float2* table = nullptr;
-  if constexpr (sizeof(E) == 2) {
-    __shared__ float2 gate[kGateN];
+  constexpr bool kTable = sizeof(E) == 2;
+  __shared__ float2 gate[kTable ? kGateN : 1];
+  if constexpr (kTable) {
     build_gate_table(gate, th.rate, 64 * NW);
-    table = gate;
     __syncthreads();
   }
   for (int chunk = nchunk - 1; chunk >= 0; --chunk) {
-    th.unpack(chunk, table);
+    th.template unpack<kTable>(chunk, gate);
     const float ckpt = pl.wave == 0 && kept ? p.checkpoints[(bh * nblock + chunk * P::BLOCKS) * p.d + ch] : 0.0f;
     if (chunk > 0) th.load(chunk - 1);
     const int q = chunk & 1;
@@ -664,8 +755,11 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanB
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) th.replay(e, segH[q][pl.seg][pl.lc * VEC + e], segG[q][pl.seg][pl.lc * VEC + e]);
-    th.write(chunk);
+    for (int e = 0; e < VEC; ++e) {
+      th.replay_state(e, segH[q][pl.seg][pl.lc * VEC + e]);
+      th.replay_grad(e, segG[q][pl.seg][pl.lc * VEC + e], th.cm, th.dy, th.kf);
+    }
+    th.write(chunk, th.dy, th.kf);
   }
   if (pl.wave == 1 && kept && p.grad_state_in != nullptr) p.grad_state_in[bh * p.d + ch] = carry;
 }
@@ -683,40 +777,36 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
   __shared__ unsigned tickets[2];
   __shared__ float2 gate[kTable ? kGateN : 1];
   const P pl;
-  const int hl = blockIdx.x % nh, per_step = p.B * nct;
-  const unsigned total = static_cast<unsigned>(cn.steps) * per_step;
-  unsigned* counter = cn.ticket + hl * kCounterWords;
-  if (threadIdx.x < 2) tickets[threadIdx.x] = take_ticket(counter);
+  const Queue qu(cn, blockIdx.x % nh, h0, nh, nct, p.B);
+  auto chunk_of = [&](unsigned ticket) __attribute__((always_inline)) { return cn.steps - 1 - qu.step(ticket); };
+  if (threadIdx.x == 0) tickets[0] = qu.take();
   __syncthreads();
-  unsigned cur = min(tickets[0], tickets[1]), next = max(tickets[0], tickets[1]);
-  if (cur >= total) return;  // the whole workgroup
+  unsigned cur = uniform(tickets[0]);
+  if (cur >= qu.total) return;  // the whole workgroup
+  if (threadIdx.x == 0) tickets[1] = qu.take();
   const int nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
-  BwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[hl]);
-  auto tile_of = [&](unsigned ticket) __attribute__((always_inline)) {
-    const int i = ticket % per_step;
-    return decode_tile((i / nct * nh + hl) * nct + i % nct, nct, nh, h0, CW);
-  };
-  ScanTile tl = tile_of(cur);
+  BwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[qu.hl]);
+  ScanTile tl = qu.template tile<CW>(cur);
   th.aim_loads(p, tl, pl);
-  th.load(cn.steps - 1 - cur / per_step);
+  th.load(chunk_of(cur));
   if constexpr (kTable) build_gate_table(gate, th.rate, 64 * NW);
-  __syncthreads();  // the table; and everyone has read the first tickets
+  __syncthreads();  // the table and the second ticket
+  unsigned next = uniform(tickets[1]);
   for (;;) {
-    const int step = cur / per_step, chunk = cn.steps - 1 - step;
-    const int ch = tl.c0 + pl.lane;
-    const bool kept = pl.wave < 2 && pl.lane < CW && ch < p.d;
+    const int step = qu.step(cur), chunk = cn.steps - 1 - step;
+    const int ch = tl.c0 + pl.lane, tile = qu.number(tl);
+    const bool channel = pl.lane < CW, kept = channel && ch < p.d;
     const long bh = static_cast<long>(tl.b) * p.H + tl.h;
     // wave 0: the state before the tile; wave 1: the gradient behind the sequence
     float start = 0.0f;
     if (pl.wave == 0 && kept) start = p.checkpoints[(bh * nblock + chunk * P::BLOCKS) * p.d + ch];
-    if (pl.wave == 1 && kept && p.grad_state_out != nullptr) start = p.grad_state_out[bh * p.d + ch];
+    if (pl.wave == 1 && kept && step < kGroup && p.grad_state_out != nullptr) start = p.grad_state_out[bh * p.d + ch];
     th.aim_stores(p, tl, pl);
-    th.unpack(chunk, kTable ? gate : nullptr);
-    ScanTile nt = tl;
-    if (next < total) {
-      nt = tile_of(next);
-      th.aim_loads(p, nt, pl);
-      th.load(cn.steps - 1 - next / per_step);
+    th.template unpack<kTable>(chunk, gate);
+    if (next < qu.total) {
+      tl = qu.template tile<CW>(next);
+      th.aim_loads(p, tl, pl);
+      th.load(chunk_of(next));
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -727,15 +817,17 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
       segG[pl.seg][pl.lc * VEC + e] = R;
     }
     __syncthreads();
-    if (threadIdx.x == 128 && next < total) tickets[0] = take_ticket(counter);
-    if (pl.wave == 0 && pl.lane < CW) {
+    if (threadIdx.x == 128 && next < qu.total) tickets[0] = qu.take();
+    if (pl.wave == 0 && channel) {
 #pragma unroll 8
       for (int i = 0; i < P::NSEG; ++i) {
         const float a = segA[i][pl.lane], hh = segH[i][pl.lane];
         segH[i][pl.lane] = start;
         start = fmaf(a, start, hh);
       }
-    } else if (pl.wave == 1 && pl.lane < CW) {
+    } else if (pl.wave == 1 && channel) {
+      Entering<CW> in;
+      in.begin(cn, step, tile, pl.lane);
       float a = 1.0f, g = 0.0f;  // the map of the segments behind
 #pragma unroll 8
       for (int i = P::NSEG - 1; i >= 0; --i) {
@@ -745,7 +837,8 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
         a *= ai;
         g = fmaf(ai, g, gi);
       }
-      const float v = chain<CW>(cn, step, (tl.b * nh + hl) * nct + tl.ct, pl.lane, a, g, start);
+      publish_map<CW>(cn, step, tile, pl.lane, a, g);
+      const float v = in.end(cn, step, tile, pl.lane, a, g, start);
       enter[pl.lane] = v;
       if (kept && p.grad_state_in != nullptr && chunk == 0) p.grad_state_in[bh * p.d + ch] = fmaf(a, v, g);
     }
@@ -753,15 +846,14 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const int c = pl.lc * VEC + e;
-      th.replay(e, segH[pl.seg][c], fmaf(segB[pl.seg][c], enter[c], segG[pl.seg][c]));
+      th.replay_state(e, segH[pl.seg][c]);
+      th.replay_grad(e, fmaf(segB[pl.seg][c], enter[c], segG[pl.seg][c]), th.cm, th.dy, th.kf);
     }
-    const unsigned after = tickets[0];
-    th.write(chunk);
-    if (next >= total) break;
-    __syncthreads();  // the segments and the ticket are read
     cur = next;
-    next = after;
-    tl = nt;
+    next = uniform(tickets[0]);
+    __syncthreads();  // the segments, the entering values and the ticket are read
+    th.write(chunk, th.dy, th.kf);
+    if (cur >= qu.total) break;
   }
 }
 
@@ -807,15 +899,16 @@ HeadRate head_rates(const HeadGroup& g) {
 // Tile width for a row of d channels: 64, or the next power of two for
 // narrow rows so that lanes are not left idle.
 int tile_width(int d) { return d > 32 ? 64 : d > 16 ? 32 : 16; }
-int tile_tokens(int d, int waves) { return waves * (kPerThread * 64 / tile_width(d)); }
+// Tokens of a tile with elems elements per lane over its waves.
+int tile_tokens(int d, int elems) { return elems * 64 / tile_width(d); }
 
 // The chained kernels' part of the workspace for a launch of nh heads.
 struct ChainSizes {
   int steps, tiles;
   size_t maps, enter;  // words of 8 and of 4 bytes
 };
-ChainSizes chain_sizes(int B, int nh, int T, int d, int waves) {
-  const int cw = tile_width(d), tt = tile_tokens(d, waves);
+ChainSizes chain_sizes(int B, int nh, int T, int d, int elems) {
+  const int cw = tile_width(d), tt = tile_tokens(d, elems);
   ChainSizes z;
   z.steps = (T + tt - 1) / tt;
   z.tiles = B * nh * ((d + cw - 1) / cw);
@@ -827,30 +920,34 @@ ChainSizes chain_sizes(int B, int nh, int T, int d, int waves) {
 // Whether the tiles of a channel run are chained over workgroups (else one
 // workgroup walks them).
 bool chained(int B, int H, int T, int d) {
-  const ChainSizes z = chain_sizes(B, H < kHeadsPerLaunch ? H : kHeadsPerLaunch, T, d, kBlockWaves);
+  const ChainSizes z = chain_sizes(B, H < kHeadsPerLaunch ? H : kHeadsPerLaunch, T, d, kBlockElems);
   return z.steps > 1 && z.tiles < kWalkTiles;
 }
 
-// [ticket counters][maps][enter], all ones at the start.
-hipError_t make_chain(void* ws, int B, int nh, int T, int d, int waves, Chain* c, hipStream_t s) {
-  const ChainSizes z = chain_sizes(B, nh, T, d, waves);
-  c->ticket = static_cast<unsigned*>(ws);
-  c->maps = reinterpret_cast<u64*>(c->ticket + nh * kCounterWords);
+// [counters][maps][enter], all ones at the start.
+hipError_t make_chain(void* ws, int B, int nh, int T, int d, int elems, Chain* c, hipStream_t s) {
+  const ChainSizes z = chain_sizes(B, nh, T, d, elems);
+  c->counters = static_cast<unsigned*>(ws);
+  c->maps = reinterpret_cast<u64*>(c->counters + nh * kCounterWords);
   c->enter = reinterpret_cast<unsigned*>(c->maps + z.maps);
   c->steps = z.steps;
   c->tiles = z.tiles;
   return launch_fill_u32(ws, static_cast<size_t>(nh) * kCounterWords + z.maps * 2 + z.enter, 0xFFFFFFFFu, s);
 }
 
-// Workgroups of a chained launch: as many as fit the device for each head, at
-// most one for each of its tiles.
-int chain_blocks(const Chain& c, int nh, int per_cu) {
-  const long per_head = static_cast<long>(c.steps) * (c.tiles / nh);
+// Workgroups of a chained launch: per_cu for each compute unit, shared out to
+// the heads, at most one for each tile.
+int chain_blocks(int steps, int tiles, int nh, int per_cu) {
+  const long per_head = static_cast<long>(steps) * (tiles / nh);
   const long want = 256L * per_cu / nh > 1 ? 256L * per_cu / nh : 1;
   return nh * static_cast<int>(want < per_head ? want : per_head);
 }
-// A gate table pays once a workgroup works on several tiles.
-bool use_table(const Chain& c, int blocks) { return static_cast<long>(c.steps) * c.tiles >= kTableTiles * blocks; }
+// Whether the workgroups of a chained launch have so many tiles that a gate
+// table pays.
+bool many_tiles(int B, int nh, int T, int d, int elems, int per_cu) {
+  const ChainSizes z = chain_sizes(B, nh, T, d, elems);
+  return static_cast<long>(z.steps) * z.tiles >= static_cast<long>(kTableTiles) * chain_blocks(z.steps, z.tiles, nh, per_cu);
+}
 
 template <typename E, int VEC, int CW, bool kNorm>
 hipError_t run_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
@@ -861,17 +958,19 @@ hipError_t run_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStrea
                        s, p, head_rates(g), g.h0, g.nh, nct);
     return hipGetLastError();
   }
-  constexpr int NW = 8;
+  constexpr int NW = 8, kLong = sizeof(E) == 2 && VEC > 1 ? 32 : 16;  // elements of a thread: by table, directly
+  const bool table = sizeof(E) == 2 && many_tiles(p.B, g.nh, p.T, p.d, NW * kLong, 2);
   Chain c;
-  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, NW, &c, s);
+  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, NW * (table ? kLong : 16), &c, s);
   if (e != hipSuccess) return e;
-  const int blocks = chain_blocks(c, g.nh, 3);
-  if (sizeof(E) == 2 && use_table(c, blocks))
-    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, kNorm, sizeof(E) == 2>), dim3(blocks), dim3(64 * NW),
-                       0, s, p, c, head_rates(g), g.h0, g.nh, nct);
+  if (table)
+    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, kLong, kNorm, sizeof(E) == 2>),
+                       dim3(chain_blocks(c.steps, c.tiles, g.nh, 2)), dim3(64 * NW), 0, s, p, c, head_rates(g), g.h0,
+                       g.nh, nct);
   else
-    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, kNorm, false>), dim3(blocks), dim3(64 * NW), 0, s,
-                       p, c, head_rates(g), g.h0, g.nh, nct);
+    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, 16, kNorm, false>),
+                       dim3(chain_blocks(c.steps, c.tiles, g.nh, 3)), dim3(64 * NW), 0, s, p, c, head_rates(g), g.h0,
+                       g.nh, nct);
   return hipGetLastError();
 }
 
@@ -894,10 +993,10 @@ hipError_t run_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStrea
   }
   constexpr int NW = 8;
   Chain c;
-  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, NW, &c, s);
+  const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, NW * kPerThread, &c, s);
   if (e != hipSuccess) return e;
-  const int blocks = chain_blocks(c, g.nh, 1);
-  if (sizeof(E) == 2 && use_table(c, blocks))
+  const int blocks = chain_blocks(c.steps, c.tiles, g.nh, 1);
+  if (sizeof(E) == 2 && many_tiles(p.B, g.nh, p.T, p.d, NW * kPerThread, 1))
     hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, NW, kNorm, sizeof(E) == 2>), dim3(blocks), dim3(64 * NW),
                        0, s, p, c, head_rates(g), g.h0, g.nh, nct);
   else
@@ -945,12 +1044,12 @@ hipError_t step_by_vec(int vec, const GatedScanFwd& p, const HeadGroup& g, hipSt
 
 }  // namespace
 
-int gated_scan_block(int d) { return tile_tokens(d, kBlockWaves); }
+int gated_scan_block(int d) { return tile_tokens(d, kBlockElems); }
 
 size_t gated_scan_chain_bytes(int B, int H, int T, int d) {
   if (T <= 1 || !chained(B, H, T, d)) return 0;
   const int nh = H < kHeadsPerLaunch ? H : kHeadsPerLaunch;
-  const ChainSizes z = chain_sizes(B, nh, T, d, kBlockWaves);  // wider workgroups have fewer tiles
+  const ChainSizes z = chain_sizes(B, nh, T, d, kBlockElems);  // longer tiles are fewer
   return static_cast<size_t>(nh) * kCounterWords * 4 + z.maps * 8 + z.enter * 4;
 }
 
