@@ -29,11 +29,15 @@ namespace {
 
 constexpr int kPerThread = 16;   // VEC * S of most kernels
 constexpr int kBlockElems = 128;  // a checkpoint's block: as many elements per lane (8 waves of 16)
-// Channel runs from which on each is walked by one workgroup.  Measured at 256
-// runs (one for each compute unit): walking 50 us and chaining 68 us (B4 H8
-// T2048 d512, bf16), 515 and 665 us (B2 H16 T8192 d512 forward and backward);
-// at 64 runs 1445 and 462 us (B1 H8 T65536 d512 forward).
-constexpr int kWalkTiles = 256;
+// Tiles of a channel run are chained over workgroups where the runs are fewer
+// than kWalkTiles and have kChainSteps blocks of tokens or more; else one
+// workgroup walks each run.  Measured in us, walking / chaining, d 64, bf16
+// forward (and backward), runs x tokens:
+//     32 x 512   13 / 17 (16 / 20)      32 x 1024    17 / 17 (27 / 20)
+//     32 x 4096  59 / 24 (101 / 34)    128 x 4096    62 / 53 (109 / 93)
+//    192 x 4096  68 / 74 (118 / 131)   256 x 16384  286 / 318 (504 / 668)
+// and in fp32 128 x 4096 83 / 76 (140 / 118), 256 x 4096 140 / 144 (199 / 229).
+constexpr int kWalkTiles = 160, kChainSteps = 8;
 constexpr int kTableTiles = 4;  // tiles of a workgroup from which on its gate table pays
 
 typedef unsigned long long u64;
@@ -921,7 +925,7 @@ ChainSizes chain_sizes(int B, int nh, int T, int d, int elems) {
 // workgroup walks them).
 bool chained(int B, int H, int T, int d) {
   const ChainSizes z = chain_sizes(B, H < kHeadsPerLaunch ? H : kHeadsPerLaunch, T, d, kBlockElems);
-  return z.steps > 1 && z.tiles < kWalkTiles;
+  return z.steps >= kChainSteps && z.tiles < kWalkTiles;
 }
 
 // [counters][maps][enter], all ones at the start.

@@ -253,7 +253,7 @@ int threads_per_row(int D) {
   return n;
 }
 constexpr int fwd_threads(int lpr) { return lpr > 256 ? lpr : 256; }
-constexpr int bwd_threads(int lpr) { return lpr > 256 ? lpr : 256; }
+constexpr int bwd_threads(int lpr) { return lpr > 512 ? lpr : 512; }
 
 template <typename E, int VEC, int LPR, int EPT>
 struct Fwd {
@@ -304,12 +304,12 @@ hipError_t launch_residual_norm_fwd(const ResidualNormFwd& a, hipStream_t s) {
                                                          : by_row<Fwd, float, 1>(a.D, a, s);
 }
 
-// One workgroup for each compute unit and set of rows it works on at once, up
-// to 512 threads' worth twice over: more would only add partial sums.
+// Two workgroups of 512 threads for each compute unit, as many as fit with
+// their parameter sums in registers: more would only add partial sums.
 int residual_norm_bwd_blocks(long rows, int D) {
   const int lpr = threads_per_row(D), threads = bwd_threads(lpr);
   const long most = (rows + threads / lpr - 1) / (threads / lpr);
-  const long want = 256L * (2048 / threads);
+  const long want = 256L * (1024 / threads);
   return static_cast<int>(want < most ? want : most);
 }
 

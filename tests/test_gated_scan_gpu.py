@@ -141,7 +141,11 @@ CASES = [
     # enough channel runs for one workgroup each
     (4, 8, 270, 512, torch.bfloat16, True, True, 0.01),
     (16, 16, 1050, 7, torch.float32, False, True, 0.01),
-    # many groups of chained tiles
+    # chained tiles: every access width, narrow rows, many groups
+    (1, 2, 1300, 201, torch.float32, True, True, 0.003),
+    (1, 1, 1500, 201, torch.bfloat16, False, True, 0.003),
+    (2, 1, 2300, 24, torch.bfloat16, True, True, 0.003),
+    (1, 2, 4500, 12, torch.float32, False, True, 0.003),
     (1, 2, 9000, 40, torch.bfloat16, False, True, 0.0005),
 ]
 
@@ -162,6 +166,19 @@ def test_scan_matches_oracle(B, H, T, d, dtype, normalize, state, reset):
     again = ret.gated_scan_bwd(X, F, rate, DY, S, DS, None, normalize)
     assert all(torch.equal(a, b) for a, b in zip(got, again)), "checkpoints of the call and recomputed ones differ"
     assert torch.equal(X.cpu(), x) and torch.equal(DY.cpu(), dy)
+
+
+@pytest.mark.parametrize("normalize,d", [(True, 512), (False, 510)])
+def test_long_bf16_sequence(normalize, d):
+    """Enough chained tiles for every workgroup to look its gates up, among them gates outside the table."""
+    H, T = 8, 8250
+    x, f, s, dy, ds = make(1, H, T, d, torch.bfloat16, seed=31, reset=0.002)
+    f[0, 3, 5000:5003, 7] = torch.tensor([300.0, -300.0, 1e-9]).bfloat16()
+    rate = rates(H)
+    y, last, kept = ret.gated_scan_fwd(x.to(DEV), f.to(DEV), rate, s.to(DEV), normalize=normalize, checkpoints=True)
+    check_forward(f"long bf16 {normalize}", x, f, rate, s, normalize, y, last)
+    got = ret.gated_scan_bwd(x.to(DEV), f.to(DEV), rate, dy.to(DEV), s.to(DEV), ds.to(DEV), kept, normalize)
+    check_backward(f"long bf16 {normalize}", x, f, rate, dy, s, ds, normalize, got)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -197,12 +214,12 @@ def test_prefill_then_steps(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("d", [64, 24, 19])
-def test_strided_layouts_and_untouched_surroundings(dtype, d):
+@pytest.mark.parametrize("d,T", [(64, 150), (24, 150), (19, 150), (64, 1100), (35, 1200)])
+def test_strided_layouts_and_untouched_surroundings(dtype, d, T):
     """Token-major tensors and slices of fused buffers give the scan of their rows, and what lies between
     and behind the written rows stays as it was.  (Not the contiguous call's bits: narrower accesses give a
     thread more tokens, so the maps are composed in another order.)"""
-    B, H, T, W = 2, 3, 150, 2 * d + 5
+    B, H, W = 2, 3, 2 * d + 5
     host = make(B, H, T, d, dtype, seed=6, reset=0.02)
     x, f, s, dy, ds = (t.to(DEV) for t in host)
     rate = rates(H)
