@@ -18,6 +18,7 @@ from ._lib import RET_BF16, RET_F32, RetentionError, _gamma_array, last_error, l
 
 _DT = {torch.float32: RET_F32, torch.bfloat16: RET_BF16}
 _BAD = ctypes.c_size_t(-1).value
+_current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
@@ -32,21 +33,26 @@ def _rows(t: torch.Tensor, shape, like: torch.Tensor, name: str) -> torch.Tensor
     """A sequence tensor: shape, dtype and device, and contiguous rows."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype != like.dtype or t.get_device() != like.get_device() or not t.is_cuda:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device (cuda/HIP) tensor")
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device (cuda/HIP) tensor")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"the rows (last dimension) of {name} must be contiguous")
     return t
 
 
 def _f32(t: Optional[torch.Tensor], shape, like: torch.Tensor, name: str) -> Optional[torch.Tensor]:
     """A state or parameter: contiguous fp32 on the same device."""
-    if t is not None and (t.dtype != torch.float32 or t.shape != shape or t.device != like.device or
+    if t is not None and (t.dtype != torch.float32 or t.shape != shape or t.get_device() != like.get_device() or
                           not t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous float32 {tuple(shape)} on {like.device}")
     return t
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A new contiguous tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _new_f32(t: Union[torch.Tensor, bool, None], shape, like: torch.Tensor, name: str) -> Optional[torch.Tensor]:
@@ -55,7 +61,7 @@ def _new_f32(t: Union[torch.Tensor, bool, None], shape, like: torch.Tensor, name
         return torch.empty(shape, dtype=torch.float32, device=like.device)
     if t is None or t is False:
         return None
-    return _f32(t, torch.Size(shape), like, name)
+    return _f32(t, shape, like, name)
 
 
 def _strides(*tensors):
@@ -92,7 +98,7 @@ def _workspace(t: Optional[torch.Tensor], need: int, like: torch.Tensor):
 def _call(fn, device: torch.device, *args) -> None:
     """fn(*args, stream) with the tensors' device current and on its current stream."""
     index = device.index
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(device):
             st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
     else:
@@ -137,7 +143,7 @@ def gated_scan_fwd(x: torch.Tensor, f: torch.Tensor, rate, state_in: Optional[to
     lib = load()
     dt = _scan_inputs(x, f, 4)
     B, H, T, d = x.shape
-    state_in = _f32(state_in, torch.Size((B, H, d)), x, "state_in")
+    state_in = _f32(state_in, (B, H, d), x, "state_in")
     state_out = _new_f32(state_out, (B, H, d), x, "state_out")
     y = _out(y, x, "y")
     want = checkpoints is not None and checkpoints is not False
@@ -167,12 +173,12 @@ def gated_scan_bwd(x: torch.Tensor, f: torch.Tensor, rate, grad_y: torch.Tensor,
     dt = _scan_inputs(x, f, 4)
     B, H, T, d = x.shape
     _rows(grad_y, x.shape, x, "grad_y")
-    vec = torch.Size((B, H, d))
+    vec = (B, H, d)
     state_in = _f32(state_in, vec, x, "state_in")
     grad_state_out = _f32(grad_state_out, vec, x, "grad_state_out")
     grad_state_in = _new_f32(grad_state_in, (B, H, d), x, "grad_state_in")
     if checkpoints is not None:
-        _f32(checkpoints, torch.Size(gated_scan_checkpoint_shape(B, H, T, d)), x, "checkpoints")
+        _f32(checkpoints, gated_scan_checkpoint_shape(B, H, T, d), x, "checkpoints")
     gx = _out(grad_x, x, "grad_x")
     gf = _out(grad_f, x, "grad_f")
     ws, wp, wn = _workspace(workspace,
@@ -205,11 +211,11 @@ def _gate_norm_inputs(y, gate, weight, bias):
     dt = _dtype(y)
     _rows(y, y.shape, y, "y")
     B, H, T, dv = y.shape
-    token = torch.Size((B, T, H, dv))
+    token = (B, T, H, dv)
     if gate is not None:
         _rows(gate, token, y, "gate")
-    _f32(weight, torch.Size((H, dv)), y, "weight")
-    _f32(bias, torch.Size((H, dv)), y, "bias")
+    _f32(weight, (H, dv), y, "weight")
+    _f32(bias, (H, dv), y, "bias")
     return dt, B, H, T, dv, token
 
 
@@ -234,7 +240,10 @@ def group_norm_gated(y: torch.Tensor, gate: Optional[torch.Tensor] = None, weigh
     slice of a fused one); without a gate the norm alone.  weight, bias: optional fp32 [H,dv].
     """
     dt, B, H, T, dv, token = _gate_norm_inputs(y, gate, weight, bias)
-    out = torch.empty(token, dtype=y.dtype, device=y.device) if out is None else _rows(out, token, y, "out")
+    if out is None:
+        out = torch.empty(token, dtype=y.dtype, device=y.device) if gate is None else _like(gate)
+    else:
+        _rows(out, token, y, "out")
     plain = y.is_contiguous() and out.is_contiguous() and (gate is None or gate.is_contiguous())
     _call(load().retention_group_norm_gated, y.device, y.data_ptr(), _p(gate), _p(weight), _p(bias), float(eps),
           out.data_ptr(), None if plain else _pack(_head(y), _token(gate), _token(out)), B, H, T, dv, dt)
@@ -255,12 +264,11 @@ def group_norm_gated_bwd(y: torch.Tensor, gate: Optional[torch.Tensor], grad_out
     lib = load()
     dt, B, H, T, dv, token = _gate_norm_inputs(y, gate, weight, bias)
     _rows(grad_out, token, y, "grad_out")
-    gy = torch.empty(y.shape, dtype=y.dtype, device=y.device) if grad_y is None else _rows(grad_y, y.shape, y, "grad_y")
+    gy = _like(y) if grad_y is None else _rows(grad_y, y.shape, y, "grad_y")
     if gate is None:
         gz = None
     else:
-        gz = torch.empty(token, dtype=y.dtype, device=y.device) if grad_gate is None else _rows(grad_gate, token, y,
-                                                                                              "grad_gate")
+        gz = _like(gate) if grad_gate is None else _rows(grad_gate, token, y, "grad_gate")
     gw = torch.empty_like(weight) if param_grads and weight is not None else None
     gb = torch.empty_like(bias) if param_grads and bias is not None else None
     need = lib.retention_group_norm_gated_bwd_workspace_bytes(B, H, T, dv) if gw is not None or gb is not None else 0
@@ -311,10 +319,12 @@ def residual_norm(x: torch.Tensor, f: torch.Tensor, weight: Optional[torch.Tenso
     rows, D = _count(x)
     _rows(x, x.shape, x, "x")
     _rows(f, x.shape, x, "f")
-    for t, name in ((weight, "weight"), (bias, "bias"), (scale, "scale")):
-        _f32(t, torch.Size((D,)), x, name)
-    r = torch.empty(x.shape, dtype=x.dtype, device=x.device) if r is None else _rows(r, x.shape, x, "r")
-    n = torch.empty(x.shape, dtype=x.dtype, device=x.device) if n is None else _rows(n, x.shape, x, "n")
+    vec = (D,)
+    _f32(weight, vec, x, "weight")
+    _f32(bias, vec, x, "bias")
+    _f32(scale, vec, x, "scale")
+    r = _like(x) if r is None else _rows(r, x.shape, x, "r")
+    n = _like(x) if n is None else _rows(n, x.shape, x, "n")
     _call(load().retention_residual_norm, x.device, x.data_ptr(), f.data_ptr(), _p(weight), _p(bias), _p(scale),
           float(alpha), float(eps), int(rms), r.data_ptr(), n.data_ptr(), _row_strides(x=x, f=f, r=r, n=n), rows, D, dt)
     return r, n
@@ -339,12 +349,13 @@ def residual_norm_bwd(r: torch.Tensor, grad_n: torch.Tensor, grad_r: Optional[to
     for t, name in ((grad_r, "grad_r"), (f, "f")):
         if t is not None:
             _rows(t, r.shape, r, name)
-    for t, name in ((weight, "weight"), (scale, "scale")):
-        _f32(t, torch.Size((D,)), r, name)
+    vec = (D,)
+    _f32(weight, vec, r, "weight")
+    _f32(scale, vec, r, "scale")
     want_scale = param_grads and scale is not None
     if want_scale and f is None:
         raise ValueError("f is required for the gradient of scale")
-    gx = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+    gx = _like(r)
     same = alpha == 1.0 and scale is None
     gf = None if same else torch.empty_like(gx)
     gw = torch.empty_like(weight) if param_grads and weight is not None else None
