@@ -4,8 +4,9 @@
 // and, with s = sigmoid(z), dn = dout z s, p = dn w:
 //   dz = dout n (s + z s (1 - s)),  dy = rstd (p - mean(p) - xh mean(p xh)),
 //   dw = sum dn xh,  dbias = sum dn   (over b and t).
-// Rows move in 16-byte pieces, every element once: LPR lanes hold a row in
-// registers (8 elements each), so narrow heads share a wave.  Sums over a row
+// Rows move in 16-byte pieces at any alignment, every element once (vec_io.h):
+// LPR lanes hold a row in registers (8 elements each), so narrow heads share a
+// wave.  Sums over a row
 // are fp32: sum y (and p) first, then the squares and products about the
 // mean.  HBM bound: 3 elements move per value forward, 5 backward.
 #include "common.h"
@@ -39,6 +40,9 @@ __global__ __launch_bounds__(kThreads) void gate_norm_fwd_kernel(GateNormFwd a, 
   using IO = VecIO<E, VEC>;
   const int l = threadIdx.x % LPR, g = threadIdx.x / LPR;
   const unsigned row0 = (blockIdx.x * G + g) * kRows;
+  Piece pc[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) pc[i] = Piece(VEC * (l + LPR * i), a.dv, VEC);
   typename IO::Raw ry[kRows][NI], rz[kRows][NI];
   int hh[kRows];
   E* op[kRows];
@@ -52,10 +56,8 @@ __global__ __launch_bounds__(kThreads) void gate_norm_fwd_kernel(GateNormFwd a, 
     op[r] = const_cast<E*>(row_of<E>(a.out, a.so, b, h, t));
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int c = VEC * (l + LPR * i);
-      const int cc = c < a.dv ? c : 0;
-      ry[r][i] = IO::load(yp + cc);
-      if (a.gate != nullptr) rz[r][i] = IO::load(zp + cc);
+      ry[r][i] = IO::load(yp + pc[i].at);
+      if (a.gate != nullptr) rz[r][i] = IO::load(zp + pc[i].at);
     }
   }
   const float inv = 1.0f / static_cast<float>(a.dv);
@@ -65,9 +67,8 @@ __global__ __launch_bounds__(kThreads) void gate_norm_fwd_kernel(GateNormFwd a, 
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       IO::unpack(ry[r][i], y[i]);
-      if (VEC * (l + LPR * i) < a.dv)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += y[i][e];
+      for (int e = 0; e < VEC; ++e) s += pc[i].own(e) ? y[i][e] : 0.0f;
     }
     const float mu = lanes_sum<LPR>(s) * inv;
 #pragma unroll
@@ -75,14 +76,14 @@ __global__ __launch_bounds__(kThreads) void gate_norm_fwd_kernel(GateNormFwd a, 
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         y[i][e] -= mu;
-        if (VEC * (l + LPR * i) < a.dv) q = fmaf(y[i][e], y[i][e], q);
+        q = pc[i].own(e) ? fmaf(y[i][e], y[i][e], q) : q;
       }
     const float rstd = 1.0f / sqrtf(lanes_sum<LPR>(q) * inv + a.eps);
     if (row0 + r >= rows) continue;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int c = VEC * (l + LPR * i);
-      if (c >= a.dv) continue;
+      const int c = pc[i].at;
+      if (!pc[i].in) continue;
       float w[VEC], bi[VEC], z[VEC], o[VEC];
       if (a.weight != nullptr) load_params<VEC>(a.weight + static_cast<long>(hh[r]) * a.dv + c, w);
       if (a.bias != nullptr) load_params<VEC>(a.bias + static_cast<long>(hh[r]) * a.dv + c, bi);
@@ -113,12 +114,11 @@ __global__ __launch_bounds__(kThreads) void gate_norm_bwd_kernel(GateNormBwd a, 
   const unsigned step = gridDim.x * G;
   const float inv = 1.0f / static_cast<float>(a.dv);
   float w[NI][VEC], bi[NI][VEC], dw[NI][VEC], db[NI][VEC];
-  bool in[NI];
+  Piece pc[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int c = VEC * (l + LPR * i);
-    in[i] = c < a.dv;
-    const long k = static_cast<long>(h) * a.dv + (in[i] ? c : 0);
+    pc[i] = Piece(VEC * (l + LPR * i), a.dv, VEC);
+    const long k = static_cast<long>(h) * a.dv + pc[i].at;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       w[i][e] = 1.0f;
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void gate_norm_bwd_kernel(GateNormBwd a, 
     const E* dp = row_of<E>(a.grad_out, a.sdo, b, h, t);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int cc = in[i] ? VEC * (l + LPR * i) : 0;
+      const int cc = pc[i].at;
       ry[i] = IO::load(yp + cc);
       if (a.gate != nullptr) rz[i] = IO::load(zp + cc);
       rd[i] = IO::load(dp + cc);
@@ -165,10 +165,8 @@ __global__ __launch_bounds__(kThreads) void gate_norm_bwd_kernel(GateNormBwd a, 
           kz[i][e] = d[i][e] * fmaf(sg[i][e], 1.0f - s, s);
           d[i][e] *= sg[i][e];  // dn
         }
-        if (in[i]) {
-          s0 += y[i][e];
-          s1 = fmaf(d[i][e], w[i][e], s1);
-        }
+        s0 += pc[i].own(e) ? y[i][e] : 0.0f;
+        s1 = pc[i].own(e) ? fmaf(d[i][e], w[i][e], s1) : s1;
       }
     const float mu = lanes_sum<LPR>(s0) * inv, mp = lanes_sum<LPR>(s1) * inv;
     float q = 0.0f, px = 0.0f;
@@ -177,10 +175,8 @@ __global__ __launch_bounds__(kThreads) void gate_norm_bwd_kernel(GateNormBwd a, 
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         y[i][e] -= mu;
-        if (in[i]) {
-          q = fmaf(y[i][e], y[i][e], q);
-          px = fmaf(d[i][e] * w[i][e], y[i][e], px);
-        }
+        q = pc[i].own(e) ? fmaf(y[i][e], y[i][e], q) : q;
+        px = pc[i].own(e) ? fmaf(d[i][e] * w[i][e], y[i][e], px) : px;
       }
     const float rstd = 1.0f / sqrtf(lanes_sum<LPR>(q) * inv + a.eps);
     const float mpx = lanes_sum<LPR>(px) * inv * rstd;
@@ -200,10 +196,9 @@ __global__ __launch_bounds__(kThreads) void gate_norm_bwd_kernel(GateNormBwd a, 
           db[i][e] += dn;
         }
       }
-      if (in[i]) {
-        const int c = VEC * (l + LPR * i);
-        IO::store(gyp + c, gy);
-        if (a.gate != nullptr) IO::store(gzp + c, gz);
+      if (pc[i].in) {
+        IO::store(gyp + pc[i].at, gy);
+        if (a.gate != nullptr) IO::store(gzp + pc[i].at, gz);
       }
     }
   }
@@ -213,7 +208,8 @@ __global__ __launch_bounds__(kThreads) void gate_norm_bwd_kernel(GateNormBwd a, 
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[g][VEC * (l + LPR * i) + e] = k == 0 ? dw[i][e] : db[i][e];
+        for (int e = 0; e < VEC; ++e)
+          if (pc[i].in) acc[g][pc[i].at + e] = k == 0 ? dw[i][e] : db[i][e];  // shared elements have equal sums
       __syncthreads();
       float* to = partial + ((static_cast<long>(k) * gridDim.x + blockIdx.x) * a.H + h) * a.dv;
       for (int c = threadIdx.x; c < a.dv; c += kThreads) {
@@ -250,20 +246,28 @@ hipError_t run_bwd(const GateNormBwd& a, float* partial, int slabs, hipStream_t 
 
 template <typename E, int VEC>
 hipError_t fwd_by_lanes(const GateNormFwd& a, hipStream_t s) {
-  switch (lanes_for(a.dv)) {
-    case 64: return run_fwd<E, VEC, 64>(a, s);
-    case 32: return run_fwd<E, VEC, 32>(a, s);
-    case 16: return run_fwd<E, VEC, 16>(a, s);
-    default: return run_fwd<E, VEC, 8>(a, s);
+  if constexpr (VEC == 1) {
+    return run_fwd<E, VEC, 8>(a, s);  // rows of fewer than 8 elements
+  } else {
+    switch (lanes_for(a.dv)) {
+      case 64: return run_fwd<E, VEC, 64>(a, s);
+      case 32: return run_fwd<E, VEC, 32>(a, s);
+      case 16: return run_fwd<E, VEC, 16>(a, s);
+      default: return run_fwd<E, VEC, 8>(a, s);
+    }
   }
 }
 template <typename E, int VEC>
 hipError_t bwd_by_lanes(const GateNormBwd& a, float* partial, int slabs, hipStream_t s) {
-  switch (lanes_for(a.dv)) {
-    case 64: return run_bwd<E, VEC, 64>(a, partial, slabs, s);
-    case 32: return run_bwd<E, VEC, 32>(a, partial, slabs, s);
-    case 16: return run_bwd<E, VEC, 16>(a, partial, slabs, s);
-    default: return run_bwd<E, VEC, 8>(a, partial, slabs, s);
+  if constexpr (VEC == 1) {
+    return run_bwd<E, VEC, 8>(a, partial, slabs, s);
+  } else {
+    switch (lanes_for(a.dv)) {
+      case 64: return run_bwd<E, VEC, 64>(a, partial, slabs, s);
+      case 32: return run_bwd<E, VEC, 32>(a, partial, slabs, s);
+      case 16: return run_bwd<E, VEC, 16>(a, partial, slabs, s);
+      default: return run_bwd<E, VEC, 8>(a, partial, slabs, s);
+    }
   }
 }
 
@@ -271,10 +275,8 @@ hipError_t bwd_by_lanes(const GateNormBwd& a, float* partial, int slabs, hipStre
 
 hipError_t launch_gate_norm_fwd(const GateNormFwd& a, hipStream_t s) {
   if (a.dt == 1)
-    return widest_access(a.dv, 8, 2, {a.y, a.gate, a.out}, {a.sy, a.sz, a.so}) == 8 ? fwd_by_lanes<uint16_t, 8>(a, s)
-                                                                                   : fwd_by_lanes<uint16_t, 1>(a, s);
-  return widest_access(a.dv, 4, 4, {a.y, a.gate, a.out}, {a.sy, a.sz, a.so}) == 4 ? fwd_by_lanes<float, 4>(a, s)
-                                                                                 : fwd_by_lanes<float, 1>(a, s);
+    return a.dv >= 8 ? fwd_by_lanes<uint16_t, 8>(a, s) : fwd_by_lanes<uint16_t, 1>(a, s);
+  return a.dv >= 4 ? fwd_by_lanes<float, 4>(a, s) : fwd_by_lanes<float, 1>(a, s);
 }
 
 int gate_norm_bwd_slabs(int B, int H, int T, int dv) {
@@ -287,16 +289,11 @@ int gate_norm_bwd_slabs(int B, int H, int T, int dv) {
 
 hipError_t launch_gate_norm_bwd(const GateNormBwd& a, float* partial, hipStream_t s) {
   const int slabs = gate_norm_bwd_slabs(a.B, a.H, a.T, a.dv);
-  const auto tensors = {a.y, a.gate, a.grad_out, static_cast<const void*>(a.grad_y),
-                        static_cast<const void*>(a.grad_gate)};
-  const auto strides = {a.sy, a.sz, a.sdo, a.sdy, a.sdz};
   hipError_t e;
   if (a.dt == 1)
-    e = widest_access(a.dv, 8, 2, tensors, strides) == 8 ? bwd_by_lanes<uint16_t, 8>(a, partial, slabs, s)
-                                                         : bwd_by_lanes<uint16_t, 1>(a, partial, slabs, s);
+    e = a.dv >= 8 ? bwd_by_lanes<uint16_t, 8>(a, partial, slabs, s) : bwd_by_lanes<uint16_t, 1>(a, partial, slabs, s);
   else
-    e = widest_access(a.dv, 4, 4, tensors, strides) == 4 ? bwd_by_lanes<float, 4>(a, partial, slabs, s)
-                                                         : bwd_by_lanes<float, 1>(a, partial, slabs, s);
+    e = a.dv >= 4 ? bwd_by_lanes<float, 4>(a, partial, slabs, s) : bwd_by_lanes<float, 1>(a, partial, slabs, s);
   if (e != hipSuccess || partial == nullptr) return e;
   return launch_column_sums(
       ColumnSums{partial, slabs, static_cast<long>(a.H) * a.dv, {a.grad_weight, a.grad_bias, nullptr}}, s);

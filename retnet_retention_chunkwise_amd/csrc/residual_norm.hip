@@ -6,8 +6,8 @@
 //   g = dr + rstd (p - mean(p) - xh mean(p xh)),  dx = alpha g,  df = scale g,
 //   dw = sum dn xh,  db = sum dn,  dscale = sum g f   (mean(p) only for LayerNorm).
 // A row is held in registers by LPR threads, 8 elements each (16 for the
-// widest rows), in 16-byte pieces; every element is read and written once, so
-// the call is HBM bound.  Row sums are fp32 (row_sum.h): first sum r (and p),
+// widest rows), in 16-byte pieces at any alignment (vec_io.h); every element is
+// read and written once, so the call is HBM bound.  Row sums are fp32 (row_sum.h): first sum r (and p),
 // then squares and products about the mean, so a mean far from zero costs no
 // precision.  mu and rstd are found again in the backward: its rows are in
 // registers anyway.
@@ -54,30 +54,27 @@ __global__ __launch_bounds__(THREADS) void residual_norm_fwd_kernel(ResidualNorm
   const E* xp = static_cast<const E*>(a.x) + rr * a.sx;
   const E* fp = static_cast<const E*>(a.f) + rr * a.sf;
   typename IO::Raw rx[NI], rf[NI];
+  Piece pc[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int c = VEC * (l + LPR * i), cc = c < a.D ? c : 0;
-    rx[i] = IO::load(xp + cc);
-    rf[i] = IO::load(fp + cc);
+    pc[i] = Piece(VEC * (l + LPR * i), a.D, VEC);
+    rx[i] = IO::load(xp + pc[i].at);
+    rf[i] = IO::load(fp + pc[i].at);
   }
   float r[NI][VEC], s = 0.0f, q = 0.0f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int c = VEC * (l + LPR * i);
-    const bool in = c < a.D;
     float x[VEC], f[VEC], sc[VEC];
     IO::unpack(rx[i], x);
     IO::unpack(rf[i], f);
-    params<VEC>(a.scale, in ? c : 0, 1.0f, sc);
+    params<VEC>(a.scale, pc[i].at, 1.0f, sc);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       r[i][e] = as_held<E>(fmaf(a.alpha, x[e], sc[e] * f[e]));
-      if (in) {
-        s += r[i][e];
-        q = fmaf(r[i][e], r[i][e], q);
-      }
+      s += pc[i].own(e) ? r[i][e] : 0.0f;
+      q = pc[i].own(e) ? fmaf(r[i][e], r[i][e], q) : q;
     }
-    if (in && valid) IO::store(static_cast<E*>(a.r) + rr * a.sr + c, r[i]);
+    if (pc[i].in && valid) IO::store(static_cast<E*>(a.r) + rr * a.sr + pc[i].at, r[i]);
   }
   const float inv = 1.0f / static_cast<float>(a.D);
   row_sums<LPR>(s, q, ex, phase);
@@ -87,17 +84,16 @@ __global__ __launch_bounds__(THREADS) void residual_norm_fwd_kernel(ResidualNorm
     q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      if (VEC * (l + LPR * i) < a.D)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) q = fmaf(r[i][e] - mu, r[i][e] - mu, q);
+      for (int e = 0; e < VEC; ++e) q = pc[i].own(e) ? fmaf(r[i][e] - mu, r[i][e] - mu, q) : q;
     row_sums<LPR>(q, none, ex, phase);
   }
   const float rstd = 1.0f / sqrtf(q * inv + a.eps);
   if (!valid) return;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int c = VEC * (l + LPR * i);
-    if (c >= a.D) continue;
+    const int c = pc[i].at;
+    if (!pc[i].in) continue;
     float w[VEC], b[VEC], n[VEC];
     params<VEC>(a.weight, c, 1.0f, w);
     params<VEC>(a.bias, c, 0.0f, b);
@@ -121,13 +117,12 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
   const float inv = 1.0f / static_cast<float>(a.D);
   const bool with_f = kParam && a.grad_scale != nullptr;
   float w[NI][VEC], sc[NI][VEC], dw[NI][VEC], db[NI][VEC], ds[NI][VEC];
-  bool in[NI];
+  Piece pc[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int c = VEC * (l + LPR * i);
-    in[i] = c < a.D;
-    params<VEC>(a.weight, in[i] ? c : 0, 1.0f, w[i]);
-    params<VEC>(a.scale, in[i] ? c : 0, 1.0f, sc[i]);
+    pc[i] = Piece(VEC * (l + LPR * i), a.D, VEC);
+    params<VEC>(a.weight, pc[i].at, 1.0f, w[i]);
+    params<VEC>(a.scale, pc[i].at, 1.0f, sc[i]);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = ds[i][e] = 0.0f;
   }
@@ -136,7 +131,7 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
     row = row < a.rows ? row : a.rows - 1;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int cc = in[i] ? VEC * (l + LPR * i) : 0;
+      const int cc = pc[i].at;
       rr[i] = IO::load(static_cast<const E*>(a.r) + row * a.sr + cc);
       rn[i] = IO::load(static_cast<const E*>(a.grad_n) + row * a.sgn + cc);
       if (a.grad_r != nullptr) rd[i] = IO::load(static_cast<const E*>(a.grad_r) + row * a.sgr + cc);
@@ -167,12 +162,11 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
     if (!a.rms) {  // uniform
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (in[i])
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            s0 += r[i][e];
-            s1 = fmaf(p[i][e], w[i][e], s1);
-          }
+        for (int e = 0; e < VEC; ++e) {
+          s0 += pc[i].own(e) ? r[i][e] : 0.0f;
+          s1 = pc[i].own(e) ? fmaf(p[i][e], w[i][e], s1) : s1;
+        }
       row_sums<LPR>(s0, s1, ex, phase);
       mu = s0 * inv;
       mp = s1 * inv;
@@ -183,10 +177,8 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         r[i][e] -= mu;
-        if (in[i]) {
-          q = fmaf(r[i][e], r[i][e], q);
-          px = fmaf(p[i][e] * w[i][e], r[i][e], px);
-        }
+        q = pc[i].own(e) ? fmaf(r[i][e], r[i][e], q) : q;
+        px = pc[i].own(e) ? fmaf(p[i][e] * w[i][e], r[i][e], px) : px;
       }
     row_sums<LPR>(q, px, ex, phase);
     const float rstd = 1.0f / sqrtf(q * inv + a.eps);
@@ -208,8 +200,8 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
           }
         }
       }
-      if (in[i] && valid) {
-        const int c = VEC * (l + LPR * i);
+      if (pc[i].in && valid) {
+        const int c = pc[i].at;
         if (a.grad_x != nullptr) IO::store(static_cast<E*>(a.grad_x) + row * a.sgx + c, gx);
         if (a.grad_f != nullptr) IO::store(static_cast<E*>(a.grad_f) + row * a.sgf + c, gf);
       }
@@ -225,7 +217,7 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int e = 0; e < VEC; ++e)
-            acc[g][VEC * (l + LPR * i) + e] = k == 0 ? dw[i][e] : k == 1 ? db[i][e] : ds[i][e];
+            if (pc[i].in) acc[g][pc[i].at + e] = k == 0 ? dw[i][e] : k == 1 ? db[i][e] : ds[i][e];
         __syncthreads();
         for (int c = threadIdx.x; c < a.D; c += THREADS) {
           float s = acc[0][c];
@@ -236,10 +228,10 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
       } else {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (in[i])
+          if (pc[i].in)
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-              to[VEC * (l + LPR * i) + e] = k == 0 ? dw[i][e] : k == 1 ? db[i][e] : ds[i][e];
+              to[pc[i].at + e] = k == 0 ? dw[i][e] : k == 1 ? db[i][e] : ds[i][e];
       }
     }
   }
@@ -280,28 +272,27 @@ struct Bwd {
 
 template <template <typename, int, int, int> class F, typename E, int VEC, typename... A>
 hipError_t by_row(int D, A&&... a) {
-  switch (threads_per_row(D)) {
-    case 8: return F<E, VEC, 8, 8>::run(a...);
-    case 16: return F<E, VEC, 16, 8>::run(a...);
-    case 32: return F<E, VEC, 32, 8>::run(a...);
-    case 64: return F<E, VEC, 64, 8>::run(a...);
-    case 128: return F<E, VEC, 128, 8>::run(a...);
-    case 256: return F<E, VEC, 256, 8>::run(a...);
-    case 512: return F<E, VEC, 512, 8>::run(a...);
-    default: return D <= 8192 ? F<E, VEC, 1024, 8>::run(a...) : F<E, VEC, 1024, 16>::run(a...);
+  if constexpr (VEC == 1) {
+    return F<E, VEC, 8, 8>::run(a...);  // rows of fewer than 8 elements
+  } else {
+    switch (threads_per_row(D)) {
+      case 8: return F<E, VEC, 8, 8>::run(a...);
+      case 16: return F<E, VEC, 16, 8>::run(a...);
+      case 32: return F<E, VEC, 32, 8>::run(a...);
+      case 64: return F<E, VEC, 64, 8>::run(a...);
+      case 128: return F<E, VEC, 128, 8>::run(a...);
+      case 256: return F<E, VEC, 256, 8>::run(a...);
+      case 512: return F<E, VEC, 512, 8>::run(a...);
+      default: return D <= 8192 ? F<E, VEC, 1024, 8>::run(a...) : F<E, VEC, 1024, 16>::run(a...);
+    }
   }
 }
 
 }  // namespace
 
 hipError_t launch_residual_norm_fwd(const ResidualNormFwd& a, hipStream_t s) {
-  const auto tensors = {a.x, a.f, static_cast<const void*>(a.r), static_cast<const void*>(a.n)};
-  const auto strides = {Strides3{0, 0, a.sx}, Strides3{0, 0, a.sf}, Strides3{0, 0, a.sr}, Strides3{0, 0, a.sn}};
-  if (a.dt == 1)
-    return widest_access(a.D, 8, 2, tensors, strides) == 8 ? by_row<Fwd, uint16_t, 8>(a.D, a, s)
-                                                           : by_row<Fwd, uint16_t, 1>(a.D, a, s);
-  return widest_access(a.D, 4, 4, tensors, strides) == 4 ? by_row<Fwd, float, 4>(a.D, a, s)
-                                                         : by_row<Fwd, float, 1>(a.D, a, s);
+  if (a.dt == 1) return a.D >= 8 ? by_row<Fwd, uint16_t, 8>(a.D, a, s) : by_row<Fwd, uint16_t, 1>(a.D, a, s);
+  return a.D >= 4 ? by_row<Fwd, float, 4>(a.D, a, s) : by_row<Fwd, float, 1>(a.D, a, s);
 }
 
 // Two workgroups of 512 threads for each compute unit, as many as fit with
@@ -315,19 +306,11 @@ int residual_norm_bwd_blocks(long rows, int D) {
 
 hipError_t launch_residual_norm_bwd(const ResidualNormBwd& a, float* partial, hipStream_t s) {
   const int blocks = residual_norm_bwd_blocks(a.rows, a.D);
-  const bool with_f = a.grad_scale != nullptr;
-  const auto tensors = {a.r, a.grad_n, a.grad_r, with_f ? a.f : nullptr, static_cast<const void*>(a.grad_x),
-                        static_cast<const void*>(a.grad_f)};
-  const auto strides = {Strides3{0, 0, a.sr},  Strides3{0, 0, a.sgn}, Strides3{0, 0, a.grad_r ? a.sgr : 0},
-                        Strides3{0, 0, with_f ? a.sf : 0}, Strides3{0, 0, a.grad_x ? a.sgx : 0},
-                        Strides3{0, 0, a.grad_f ? a.sgf : 0}};
   hipError_t e;
   if (a.dt == 1)
-    e = widest_access(a.D, 8, 2, tensors, strides) == 8 ? by_row<Bwd, uint16_t, 8>(a.D, a, partial, blocks, s)
-                                                        : by_row<Bwd, uint16_t, 1>(a.D, a, partial, blocks, s);
+    e = a.D >= 8 ? by_row<Bwd, uint16_t, 8>(a.D, a, partial, blocks, s) : by_row<Bwd, uint16_t, 1>(a.D, a, partial, blocks, s);
   else
-    e = widest_access(a.D, 4, 4, tensors, strides) == 4 ? by_row<Bwd, float, 4>(a.D, a, partial, blocks, s)
-                                                        : by_row<Bwd, float, 1>(a.D, a, partial, blocks, s);
+    e = a.D >= 4 ? by_row<Bwd, float, 4>(a.D, a, partial, blocks, s) : by_row<Bwd, float, 1>(a.D, a, partial, blocks, s);
   if (e != hipSuccess || partial == nullptr) return e;
   return launch_column_sums(ColumnSums{partial, blocks, a.D, {a.grad_weight, a.grad_bias, a.grad_scale}}, s);
 }

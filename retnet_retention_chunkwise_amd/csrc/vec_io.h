@@ -1,7 +1,7 @@
 // VEC consecutive elements of a row as fp32, for the streaming kernels: one
-// access of VEC * sizeof(element) bytes (at most 16).  The caller guarantees
-// that every address is a multiple of that size.  All accesses are
-// non-temporal: each element is used once per call.
+// access of VEC * sizeof(element) bytes (at most 16) at any address that is a
+// multiple of the element's size (global memory takes unaligned vectors).  All
+// accesses are non-temporal: each element is used once per call.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -11,31 +11,52 @@
 
 namespace ret {
 
-template <int BYTES>
+// type: a value of BYTES bytes; at: the same in memory at multiples of ALIGN bytes.
+template <int BYTES, int ALIGN>
 struct RawOf;
 template <>
-struct RawOf<2> {
+struct RawOf<2, 2> {
   typedef uint16_t type;
+  typedef uint16_t at;
 };
 template <>
-struct RawOf<4> {
+struct RawOf<4, 2> {
   typedef unsigned int type;
+  typedef unsigned int at __attribute__((aligned(2)));
 };
 template <>
-struct RawOf<8> {
+struct RawOf<8, 2> {
   typedef unsigned int type __attribute__((ext_vector_type(2)));
+  typedef unsigned int at __attribute__((ext_vector_type(2), aligned(2)));
 };
 template <>
-struct RawOf<16> {
+struct RawOf<16, 2> {
   typedef unsigned int type __attribute__((ext_vector_type(4)));
+  typedef unsigned int at __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct RawOf<4, 4> {
+  typedef unsigned int type;
+  typedef unsigned int at __attribute__((aligned(4)));
+};
+template <>
+struct RawOf<8, 4> {
+  typedef unsigned int type __attribute__((ext_vector_type(2)));
+  typedef unsigned int at __attribute__((ext_vector_type(2), aligned(4)));
+};
+template <>
+struct RawOf<16, 4> {
+  typedef unsigned int type __attribute__((ext_vector_type(4)));
+  typedef unsigned int at __attribute__((ext_vector_type(4), aligned(4)));
 };
 
 template <typename E, int VEC>
 struct VecIO {
-  typedef typename RawOf<VEC * static_cast<int>(sizeof(E))>::type Raw;
+  typedef RawOf<VEC * static_cast<int>(sizeof(E)), static_cast<int>(sizeof(E))> R;
+  typedef typename R::type Raw;
 
   __device__ __forceinline__ static Raw load(const E* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const Raw*>(p));
+    return __builtin_nontemporal_load(reinterpret_cast<const typename R::at*>(p));
   }
   __device__ __forceinline__ static void unpack(Raw r, float (&x)[VEC]) {
     if constexpr (sizeof(E) == 4) {
@@ -81,7 +102,7 @@ struct VecIO {
           r[i] = static_cast<uint32_t>(f32_to_bf16(x[2 * i])) | (static_cast<uint32_t>(f32_to_bf16(x[2 * i + 1])) << 16);
       }
     }
-    __builtin_nontemporal_store(r, reinterpret_cast<Raw*>(p));
+    __builtin_nontemporal_store(r, reinterpret_cast<typename R::at*>(p));
   }
 };
 
@@ -89,7 +110,7 @@ struct VecIO {
 template <int VEC>
 __device__ __forceinline__ void load_params(const float* p, float (&x)[VEC]) {
   if constexpr (VEC % 4 == 0) {
-    typedef float f32v4 __attribute__((ext_vector_type(4)));
+    typedef float f32v4 __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
     for (int k = 0; k < VEC / 4; ++k) {
       const f32v4 v = *reinterpret_cast<const f32v4*>(p + 4 * k);
@@ -100,5 +121,19 @@ __device__ __forceinline__ void load_params(const float* p, float (&x)[VEC]) {
     for (int e = 0; e < VEC; ++e) x[e] = p[e];
   }
 }
+
+// A thread's piece of a row of n elements (n >= VEC): the VEC elements from c
+// on, or, where the row ends inside them, the row's last VEC elements, of which
+// the first skip belong to the piece before (it has them too, with the same
+// values, and stores them too).
+struct Piece {
+  int at, skip;
+  bool in;
+  __device__ __forceinline__ Piece() {}
+  __device__ __forceinline__ Piece(int c, int n, int vec)
+      : at(c + vec <= n ? c : c < n ? n - vec : 0), skip(c + vec <= n ? 0 : c < n ? c + vec - n : vec), in(c < n) {}
+  // whether element e counts in a sum over the row
+  __device__ __forceinline__ bool own(int e) const { return e >= skip; }
+};
 
 }  // namespace ret
