@@ -316,8 +316,36 @@ __device__ __forceinline__ E* at_row(const void* p, const Strides3& s, const Sca
   return const_cast<E*>(static_cast<const E*>(p)) + t.b * s.b + t.h * s.h + c;
 }
 
+// A thread's columns in its tile's LDS rows.  Rows that are whole vectors
+// (kWhole): VEC columns from lc * VEC on.  Else the row's last vector reaches
+// back over skip elements that belong to the lane before, which this lane
+// neither hands on nor stores.
+template <int VEC, bool kWhole>
+struct Columns {
+  int first, skip;
+  __device__ __forceinline__ Columns() {}
+  __device__ __forceinline__ Columns(const Piece& p, int lc)
+      : first(lc * VEC - (kWhole ? 0 : p.skip)), skip(kWhole ? 0 : p.skip) {}
+  __device__ __forceinline__ void put(float* row, int e, float x) const {
+    if (kWhole || e >= skip) row[first + e] = x;
+  }
+  __device__ __forceinline__ float get(const float* row, int e) const {
+    return kWhole || e >= skip ? row[first + e] : 0.0f;
+  }
+  template <typename E>
+  __device__ __forceinline__ void store(E* p, const float (&x)[VEC]) const {
+    if (kWhole || skip == 0) {
+      VecIO<E, VEC>::store(p, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e >= skip) Elem<E>::store(p, e, x[e]);
+    }
+  }
+};
+
 // ---- Forward ----
-template <typename E, int VEC, int CW, int NW, int PT, bool kNorm>
+template <typename E, int VEC, int CW, int NW, int PT, bool kNorm, bool kWhole>
 struct FwdThread {
   using P = Place<VEC, CW, NW, PT>;
   using IO = VecIO<E, VEC>;
@@ -328,20 +356,22 @@ struct FwdThread {
   float rate;
   int T, seg;
   bool store;
+  Columns<VEC, kWhole> cols;
   typename IO::Raw rx[S], rf[S];
   float x[S][VEC], cm[S][VEC];
 
   __device__ __forceinline__ FwdThread(const GatedScanFwd& p, const P& pl, float r)
       : sx(p.sx.t), sf(p.sf.t), sy(p.sy.t), rate(r), T(p.T), seg(pl.seg) {}
   __device__ __forceinline__ void aim_loads(const GatedScanFwd& p, const ScanTile& t, const P& pl) {
-    const int c = t.c0 + pl.lc * VEC, cc = c < p.d ? c : 0;  // lanes past the row's end read its start, store nothing
-    xp = at_row<E>(p.x, p.sx, t, cc);
-    fp = at_row<E>(p.f, p.sf, t, cc);
+    const int c = Piece(t.c0 + pl.lc * VEC, p.d, VEC).at;  // lanes past the row's end read its start
+    xp = at_row<E>(p.x, p.sx, t, c);
+    fp = at_row<E>(p.f, p.sf, t, c);
   }
   __device__ __forceinline__ void aim_stores(const GatedScanFwd& p, const ScanTile& t, const P& pl) {
-    const int c = t.c0 + pl.lc * VEC;
-    store = c < p.d && p.y != nullptr;
-    yp = at_row<E>(p.y, p.sy, t, c < p.d ? c : 0);
+    const Piece pc(t.c0 + pl.lc * VEC, p.d, VEC);
+    cols = Columns<VEC, kWhole>(pc, pl.lc);
+    store = pc.in && p.y != nullptr;
+    yp = at_row<E>(p.y, p.sy, t, pc.at);
   }
   __device__ __forceinline__ void load(int chunk) {
 #pragma unroll
@@ -423,7 +453,7 @@ struct FwdThread {
       if (t0 + s >= T) continue;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) h[e] = step(c[0][e], u[e], h[e]);
-      if (store) IO::store(yp + (t0 + s) * sy, h);
+      if (store) cols.template store<E>(yp + (t0 + s) * sy, h);
     }
   }
   template <bool kTable>
@@ -445,13 +475,13 @@ struct FwdThread {
     for (int s = 0; s < S; ++s) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) h[e] = step(c[s][e], u[s][e], h[e]);
-      if (store && t0 + s < T) IO::store(yp + (t0 + s) * sy, h);
+      if (store && t0 + s < T) cols.template store<E>(yp + (t0 + s) * sy, h);
     }
   }
 };
 
 // One workgroup walks the tiles of a channel run from the first token on.
-template <typename E, int VEC, int CW, int NW, bool kNorm>
+template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole>
 __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanFwd p, HeadRate rates, int h0, int nh,
                                                                        int nct) {
   using P = Place<VEC, CW, NW>;
@@ -459,7 +489,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
   __shared__ float segH[2][P::NSEG][CW];
   const P pl;
   const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
-  FwdThread<E, VEC, CW, NW, kPerThread, kNorm> th(p, pl, rates.r[tl.hl]);
+  FwdThread<E, VEC, CW, NW, kPerThread, kNorm, kWhole> th(p, pl, rates.r[tl.hl]);
   th.aim_loads(p, tl, pl);
   th.aim_stores(p, tl, pl);
   // the composing wave: one channel per lane
@@ -483,8 +513,8 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
     th.map(A, H);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      segA[q][pl.seg][pl.lc * VEC + e] = A[e];
-      segH[q][pl.seg][pl.lc * VEC + e] = H[e];
+      th.cols.put(segA[q][pl.seg], e, A[e]);
+      th.cols.put(segH[q][pl.seg], e, H[e]);
     }
     __syncthreads();
     if (mine) {
@@ -503,7 +533,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
     __syncthreads();
     float h[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) h[e] = segH[q][pl.seg][pl.lc * VEC + e];
+    for (int e = 0; e < VEC; ++e) h[e] = th.cols.get(segH[q][pl.seg], e);
     th.replay(chunk, th.cm, th.x, h);
   }
   if (kept && p.state_out != nullptr) p.state_out[bh * p.d + ch] = carry;
@@ -514,12 +544,11 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
 // gates twice, for the tile's map and for the replay: by table that is cheap,
 // and few registers let two workgroups with 256-token tiles share a compute
 // unit.  Without a table the tiles are half as long.
-template <typename E, int VEC, int CW, int NW, int PT, bool kNorm, bool kTable>
+template <typename E, int VEC, int CW, int NW, int PT, bool kNorm, bool kWhole, bool kTable>
 __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedScanFwd p, Chain cn, HeadRate rates,
                                                                        int h0, int nh, int nct) {
   using P = Place<VEC, CW, NW, PT>;
-  using Th = FwdThread<E, VEC, CW, NW, PT, kNorm>;
-  constexpr int S = P::S;
+  using Th = FwdThread<E, VEC, CW, NW, PT, kNorm, kWhole>;
   __shared__ float segA[P::NSEG][CW];
   __shared__ float segH[P::NSEG][CW];
   __shared__ float enter[CW];
@@ -542,8 +571,8 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
     th.template packed_map<kTable>(chunk, gate, A, H);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      segA[pl.seg][pl.lc * VEC + e] = A[e];
-      segH[pl.seg][pl.lc * VEC + e] = H[e];
+      th.cols.put(segA[pl.seg], e, A[e]);
+      th.cols.put(segH[pl.seg], e, H[e]);
     }
     __syncthreads();
     if (threadIdx.x == 64) ticket = qu.take();
@@ -583,10 +612,8 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
     __syncthreads();
     float h[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = pl.lc * VEC + e;
-      h[e] = fmaf(segA[pl.seg][c], enter[c], segH[pl.seg][c]);
-    }
+    for (int e = 0; e < VEC; ++e)
+      h[e] = fmaf(th.cols.get(segA[pl.seg], e), th.cols.get(enter, e), th.cols.get(segH[pl.seg], e));
     cur = uniform(ticket);
     th.template packed_replay<kTable>(chunk, gate, h);
     __syncthreads();  // the segments, the entering values and the ticket are read
@@ -598,7 +625,7 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
 // G_t = a_t g_t, so a token maps G -> a_t (dy_t + G), last token first.
 // h_(t-1) comes from replaying the tile forwards from its checkpoint:
 //   dx_t = g_t (normalize: c_t g_t),  df_t = g_t (h_(t-1) [- x_t]) a_t rate sigmoid(-f_t).
-template <typename E, int VEC, int CW, int NW, bool kNorm>
+template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole>
 struct BwdThread {
   using P = Place<VEC, CW, NW>;
   using IO = VecIO<E, VEC>;
@@ -609,22 +636,24 @@ struct BwdThread {
   float rate;
   int T, seg;
   bool store;
+  Columns<VEC, kWhole> cols;
   typename IO::Raw rx[S], rf[S], rg[S];
   float x[S][VEC], cm[S][VEC], kf[S][VEC], dy[S][VEC];
 
   __device__ __forceinline__ BwdThread(const GatedScanBwd& p, const P& pl, float r)
       : sx(p.sx.t), sf(p.sf.t), sgy(p.sgy.t), sgx(p.sgx.t), sgf(p.sgf.t), rate(r), T(p.T), seg(pl.seg) {}
   __device__ __forceinline__ void aim_loads(const GatedScanBwd& p, const ScanTile& t, const P& pl) {
-    const int c = t.c0 + pl.lc * VEC, cc = c < p.d ? c : 0;
-    xp = at_row<E>(p.x, p.sx, t, cc);
-    fp = at_row<E>(p.f, p.sf, t, cc);
-    gyp = at_row<E>(p.grad_y, p.sgy, t, cc);
+    const int c = Piece(t.c0 + pl.lc * VEC, p.d, VEC).at;
+    xp = at_row<E>(p.x, p.sx, t, c);
+    fp = at_row<E>(p.f, p.sf, t, c);
+    gyp = at_row<E>(p.grad_y, p.sgy, t, c);
   }
   __device__ __forceinline__ void aim_stores(const GatedScanBwd& p, const ScanTile& t, const P& pl) {
-    const int c = t.c0 + pl.lc * VEC, cc = c < p.d ? c : 0;
-    gxp = at_row<E>(p.grad_x, p.sgx, t, cc);
-    gfp = at_row<E>(p.grad_f, p.sgf, t, cc);
-    store = c < p.d;
+    const Piece pc(t.c0 + pl.lc * VEC, p.d, VEC);
+    cols = Columns<VEC, kWhole>(pc, pl.lc);
+    gxp = at_row<E>(p.grad_x, p.sgx, t, pc.at);
+    gfp = at_row<E>(p.grad_f, p.sgf, t, pc.at);
+    store = pc.in;
   }
   __device__ __forceinline__ void load(int chunk) {
 #pragma unroll
@@ -664,7 +693,7 @@ struct BwdThread {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       A = fmaf(-cm[s][e], A, A);
-      H = FwdThread<E, VEC, CW, NW, kPerThread, kNorm>::step(cm[s][e], x[s][e], H);
+      H = FwdThread<E, VEC, CW, NW, kPerThread, kNorm, kWhole>::step(cm[s][e], x[s][e], H);
     }
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
@@ -677,7 +706,7 @@ struct BwdThread {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       kf[s][e] *= kNorm ? h - x[s][e] : h;
-      h = FwdThread<E, VEC, CW, NW, kPerThread, kNorm>::step(cm[s][e], x[s][e], h);
+      h = FwdThread<E, VEC, CW, NW, kPerThread, kNorm, kWhole>::step(cm[s][e], x[s][e], h);
     }
   }
   // and backwards from G behind them: g becomes dx, k becomes df
@@ -696,14 +725,14 @@ struct BwdThread {
 #pragma unroll
     for (int s = 0; s < S; ++s)
       if (store && t0 + s < T) {
-        IO::store(gxp + (t0 + s) * sgx, dx[s]);
-        IO::store(gfp + (t0 + s) * sgf, df[s]);
+        cols.template store<E>(gxp + (t0 + s) * sgx, dx[s]);
+        cols.template store<E>(gfp + (t0 + s) * sgf, df[s]);
       }
   }
 };
 
 // One workgroup walks the tiles of a channel run from the last token on.
-template <typename E, int VEC, int CW, int NW, bool kNorm>
+template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole>
 __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanBwd p, HeadRate rates, int h0, int nh,
                                                                        int nct) {
   using P = Place<VEC, CW, NW>;
@@ -712,7 +741,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanB
   __shared__ float segG[2][P::NSEG][CW];
   const P pl;
   const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
-  BwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[tl.hl]);
+  BwdThread<E, VEC, CW, NW, kNorm, kWhole> th(p, pl, rates.r[tl.hl]);
   th.aim_loads(p, tl, pl);
   th.aim_stores(p, tl, pl);
   const int ch = tl.c0 + pl.lane;
@@ -736,9 +765,9 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanB
     for (int e = 0; e < VEC; ++e) {
       float A, H, R;
       th.map(e, A, H, R);
-      segA[q][pl.seg][pl.lc * VEC + e] = A;
-      segH[q][pl.seg][pl.lc * VEC + e] = H;
-      segG[q][pl.seg][pl.lc * VEC + e] = R;
+      th.cols.put(segA[q][pl.seg], e, A);
+      th.cols.put(segH[q][pl.seg], e, H);
+      th.cols.put(segG[q][pl.seg], e, R);
     }
     __syncthreads();
     if (pl.wave == 0 && pl.lane < CW) {
@@ -760,8 +789,8 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanB
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      th.replay_state(e, segH[q][pl.seg][pl.lc * VEC + e]);
-      th.replay_grad(e, segG[q][pl.seg][pl.lc * VEC + e], th.cm, th.dy, th.kf);
+      th.replay_state(e, th.cols.get(segH[q][pl.seg], e));
+      th.replay_grad(e, th.cols.get(segG[q][pl.seg], e), th.cm, th.dy, th.kf);
     }
     th.write(chunk, th.dy, th.kf);
   }
@@ -769,7 +798,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanB
 }
 
 // Workgroups of one head on the tiles of its queue, from the last token on.
-template <typename E, int VEC, int CW, int NW, bool kNorm, bool kTable>
+template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole, bool kTable>
 __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScanBwd p, Chain cn, HeadRate rates,
                                                                        int h0, int nh, int nct) {
   using P = Place<VEC, CW, NW>;
@@ -789,7 +818,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
   if (cur >= qu.total) return;  // the whole workgroup
   if (threadIdx.x == 0) tickets[1] = qu.take();
   const int nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
-  BwdThread<E, VEC, CW, NW, kNorm> th(p, pl, rates.r[qu.hl]);
+  BwdThread<E, VEC, CW, NW, kNorm, kWhole> th(p, pl, rates.r[qu.hl]);
   ScanTile tl = qu.template tile<CW>(cur);
   th.aim_loads(p, tl, pl);
   th.load(chunk_of(cur));
@@ -816,9 +845,9 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
     for (int e = 0; e < VEC; ++e) {
       float A, H, R;
       th.map(e, A, H, R);
-      segA[pl.seg][pl.lc * VEC + e] = A;
-      segH[pl.seg][pl.lc * VEC + e] = H;
-      segG[pl.seg][pl.lc * VEC + e] = R;
+      th.cols.put(segA[pl.seg], e, A);
+      th.cols.put(segH[pl.seg], e, H);
+      th.cols.put(segG[pl.seg], e, R);
     }
     __syncthreads();
     if (threadIdx.x == 128 && next < qu.total) tickets[0] = qu.take();
@@ -849,9 +878,9 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const int c = pl.lc * VEC + e;
-      th.replay_state(e, segH[pl.seg][c]);
-      th.replay_grad(e, fmaf(segB[pl.seg][c], enter[c], segG[pl.seg][c]), th.cm, th.dy, th.kf);
+      th.replay_state(e, th.cols.get(segH[pl.seg], e));
+      th.replay_grad(e, fmaf(th.cols.get(segB[pl.seg], e), th.cols.get(enter, e), th.cols.get(segG[pl.seg], e)), th.cm,
+                     th.dy, th.kf);
     }
     cur = next;
     next = uniform(tickets[0]);
@@ -953,12 +982,12 @@ bool many_tiles(int B, int nh, int T, int d, int elems, int per_cu) {
   return static_cast<long>(z.steps) * z.tiles >= static_cast<long>(kTableTiles) * chain_blocks(z.steps, z.tiles, nh, per_cu);
 }
 
-template <typename E, int VEC, int CW, bool kNorm>
+template <typename E, int VEC, int CW, bool kNorm, bool kWhole>
 hipError_t run_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int nct = (p.d + CW - 1) / CW;
   if (!chained(p.B, p.H, p.T, p.d)) {
     constexpr int NW = VEC == 1 ? 8 : 16;
-    hipLaunchKernelGGL((gated_scan_fwd_walk_kernel<E, VEC, CW, NW, kNorm>), dim3(p.B * g.nh * nct), dim3(64 * NW), 0,
+    hipLaunchKernelGGL((gated_scan_fwd_walk_kernel<E, VEC, CW, NW, kNorm, kWhole>), dim3(p.B * g.nh * nct), dim3(64 * NW), 0,
                        s, p, head_rates(g), g.h0, g.nh, nct);
     return hipGetLastError();
   }
@@ -968,11 +997,11 @@ hipError_t run_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStrea
   const hipError_t e = make_chain(ws, p.B, g.nh, p.T, p.d, NW * (table ? kLong : 16), &c, s);
   if (e != hipSuccess) return e;
   if (table)
-    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, kLong, kNorm, sizeof(E) == 2>),
+    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, kLong, kNorm, kWhole, sizeof(E) == 2>),
                        dim3(chain_blocks(c.steps, c.tiles, g.nh, 2)), dim3(64 * NW), 0, s, p, c, head_rates(g), g.h0,
                        g.nh, nct);
   else
-    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, 16, kNorm, false>),
+    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<E, VEC, CW, NW, 16, kNorm, kWhole, false>),
                        dim3(chain_blocks(c.steps, c.tiles, g.nh, 3)), dim3(64 * NW), 0, s, p, c, head_rates(g), g.h0,
                        g.nh, nct);
   return hipGetLastError();
@@ -986,12 +1015,12 @@ hipError_t run_step(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename E, int VEC, int CW, bool kNorm>
+template <typename E, int VEC, int CW, bool kNorm, bool kWhole>
 hipError_t run_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int nct = (p.d + CW - 1) / CW;
   if (!chained(p.B, p.H, p.T, p.d)) {
     constexpr int NW = sizeof(E) == 4 || VEC == 1 ? 8 : 16;  // what fits 512 / (NW / 4) registers without spills
-    hipLaunchKernelGGL((gated_scan_bwd_walk_kernel<E, VEC, CW, NW, kNorm>), dim3(p.B * g.nh * nct), dim3(64 * NW), 0,
+    hipLaunchKernelGGL((gated_scan_bwd_walk_kernel<E, VEC, CW, NW, kNorm, kWhole>), dim3(p.B * g.nh * nct), dim3(64 * NW), 0,
                        s, p, head_rates(g), g.h0, g.nh, nct);
     return hipGetLastError();
   }
@@ -1001,49 +1030,45 @@ hipError_t run_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStrea
   if (e != hipSuccess) return e;
   const int blocks = chain_blocks(c.steps, c.tiles, g.nh, 1);
   if (sizeof(E) == 2 && many_tiles(p.B, g.nh, p.T, p.d, NW * kPerThread, 1))
-    hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, NW, kNorm, sizeof(E) == 2>), dim3(blocks), dim3(64 * NW),
+    hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, NW, kNorm, kWhole, sizeof(E) == 2>), dim3(blocks), dim3(64 * NW),
                        0, s, p, c, head_rates(g), g.h0, g.nh, nct);
   else
-    hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, NW, kNorm, false>), dim3(blocks), dim3(64 * NW), 0, s,
+    hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<E, VEC, CW, NW, kNorm, kWhole, false>), dim3(blocks), dim3(64 * NW), 0, s,
                        p, c, head_rates(g), g.h0, g.nh, nct);
   return hipGetLastError();
 }
 
-template <template <typename, int, int, bool> class F, typename E, int VEC, typename... A>
+// Rows of 4 channels or more move in vectors of 4 at any alignment, narrower
+// ones by the channel.
+template <template <typename, int, int, bool, bool> class F, typename E, int VEC, bool kWhole, typename... A>
 hipError_t by_width(int cw, bool norm, A&&... a) {
-  if (cw == 64) return norm ? F<E, VEC, 64, true>::run(a...) : F<E, VEC, 64, false>::run(a...);
-  if (cw == 32) return norm ? F<E, VEC, 32, true>::run(a...) : F<E, VEC, 32, false>::run(a...);
-  return norm ? F<E, VEC, 16, true>::run(a...) : F<E, VEC, 16, false>::run(a...);
+  if (cw == 64) return norm ? F<E, VEC, 64, true, kWhole>::run(a...) : F<E, VEC, 64, false, kWhole>::run(a...);
+  if (cw == 32) return norm ? F<E, VEC, 32, true, kWhole>::run(a...) : F<E, VEC, 32, false, kWhole>::run(a...);
+  return norm ? F<E, VEC, 16, true, kWhole>::run(a...) : F<E, VEC, 16, false, kWhole>::run(a...);
 }
-template <template <typename, int, int, bool> class F, typename E, typename... A>
-hipError_t by_vec(int vec, int cw, bool norm, A&&... a) {
-  switch (vec) {
-    case 4: return by_width<F, E, 4>(cw, norm, a...);
-    case 2: return by_width<F, E, 2>(cw, norm, a...);
-    default: return by_width<F, E, 1>(cw, norm, a...);
-  }
+template <template <typename, int, int, bool, bool> class F, typename E, typename... A>
+hipError_t by_row(int d, bool norm, A&&... a) {
+  if (d < 4) return norm ? F<E, 1, 16, true, true>::run(a...) : F<E, 1, 16, false, true>::run(a...);
+  return d % 4 == 0 ? by_width<F, E, 4, true>(tile_width(d), norm, a...) : by_width<F, E, 4, false>(tile_width(d), norm, a...);
 }
 
-template <typename E, int VEC, int CW, bool kNorm>
+template <typename E, int VEC, int CW, bool kNorm, bool kWhole>
 struct Fwd {
   static hipError_t run(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
-    return run_fwd<E, VEC, CW, kNorm>(p, ws, g, s);
+    return run_fwd<E, VEC, CW, kNorm, kWhole>(p, ws, g, s);
   }
 };
-template <typename E, int VEC, int CW, bool kNorm>
+template <typename E, int VEC, int CW, bool kNorm, bool kWhole>
 struct Bwd {
   static hipError_t run(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
-    return run_bwd<E, VEC, CW, kNorm>(p, ws, g, s);
+    return run_bwd<E, VEC, CW, kNorm, kWhole>(p, ws, g, s);
   }
 };
 
 template <typename E>
-hipError_t step_by_vec(int vec, const GatedScanFwd& p, const HeadGroup& g, hipStream_t s) {
-  switch (vec) {
-    case 4: return p.normalize ? run_step<E, 4, true>(p, g, s) : run_step<E, 4, false>(p, g, s);
-    case 2: return p.normalize ? run_step<E, 2, true>(p, g, s) : run_step<E, 2, false>(p, g, s);
-    default: return p.normalize ? run_step<E, 1, true>(p, g, s) : run_step<E, 1, false>(p, g, s);
-  }
+hipError_t step_by_row(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s) {
+  if (p.d % 4 == 0) return p.normalize ? run_step<E, 4, true>(p, g, s) : run_step<E, 4, false>(p, g, s);
+  return p.normalize ? run_step<E, 1, true>(p, g, s) : run_step<E, 1, false>(p, g, s);
 }
 
 }  // namespace
@@ -1058,24 +1083,14 @@ size_t gated_scan_chain_bytes(int B, int H, int T, int d) {
 }
 
 hipError_t launch_gated_scan_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
-  const int es = p.dt == 1 ? 2 : 4;
-  const int vec = widest_access(p.d, 4, es, {p.x, p.f, p.y}, {p.sx, p.sf, p.sy});
-  if (p.T == 1) {
-    const int sv = widest_access(p.d, vec, 4, {p.state_in, p.state_out}, {});
-    return p.dt == 1 ? step_by_vec<uint16_t>(sv, p, g, s) : step_by_vec<float>(sv, p, g, s);
-  }
-  const int cw = tile_width(p.d);
-  return p.dt == 1 ? by_vec<Fwd, uint16_t>(vec, cw, p.normalize, p, ws, g, s)
-                   : by_vec<Fwd, float>(vec, cw, p.normalize, p, ws, g, s);
+  if (p.T == 1) return p.dt == 1 ? step_by_row<uint16_t>(p, g, s) : step_by_row<float>(p, g, s);
+  return p.dt == 1 ? by_row<Fwd, uint16_t>(p.d, p.normalize, p, ws, g, s)
+                   : by_row<Fwd, float>(p.d, p.normalize, p, ws, g, s);
 }
 
 hipError_t launch_gated_scan_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
-  const int es = p.dt == 1 ? 2 : 4;
-  const int vec =
-      widest_access(p.d, 4, es, {p.x, p.f, p.grad_y, p.grad_x, p.grad_f}, {p.sx, p.sf, p.sgy, p.sgx, p.sgf});
-  const int cw = tile_width(p.d);
-  return p.dt == 1 ? by_vec<Bwd, uint16_t>(vec, cw, p.normalize, p, ws, g, s)
-                   : by_vec<Bwd, float>(vec, cw, p.normalize, p, ws, g, s);
+  return p.dt == 1 ? by_row<Bwd, uint16_t>(p.d, p.normalize, p, ws, g, s)
+                   : by_row<Bwd, float>(p.d, p.normalize, p, ws, g, s);
 }
 
 }  // namespace ret

@@ -4,9 +4,6 @@
 
 #include <hip/hip_runtime_api.h>
 #include <stddef.h>
-#include <stdint.h>
-
-#include <initializer_list>
 
 namespace ret {
 
@@ -161,23 +158,6 @@ hipError_t launch_group_norm(const void* y, const float* weight, const float* bi
 struct Strides3 {
   long b, h, t;
 };
-
-// The widest access (in elements, a power of two up to most) that the row
-// length, every pointer and every stride allow (es: element size in bytes).
-inline int widest_access(int d, int most, int es, std::initializer_list<const void*> ptrs,
-                         std::initializer_list<Strides3> strides) {
-  auto fits = [&](int v) {
-    if (d % v != 0) return false;
-    for (const void* q : ptrs)
-      if (reinterpret_cast<uintptr_t>(q) % (static_cast<uintptr_t>(v) * es) != 0) return false;
-    for (const Strides3& s : strides)
-      if (s.b % v != 0 || s.h % v != 0 || s.t % v != 0) return false;
-    return true;
-  };
-  int v = most;
-  while (v > 1 && !fits(v)) v >>= 1;
-  return v;
-}
 
 // Gated linear recurrence (gated_scan.hip).  Head groups carry the heads'
 // decay exponents in their gamma field.  dt: 0 = fp32, 1 = bf16.
