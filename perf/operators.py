@@ -209,6 +209,10 @@ def _own_scan(s):
     out = {"y": y, "state": last, "dx": dx, "df": df}
     if state is not None:
         out["dstate"] = ds
+        if s["dy"].dtype == torch.float32:
+            # float() is no copy in 32 bits, so the plain pass leaves the state's gradient added to the last
+            # token's dy: a second pass on the same state starts from that, here as there
+            s["dy"][:, :, -1] += s["dstate"]
     return out
 
 
