@@ -284,9 +284,9 @@ ret_status retention_recurrent_step(const void* q, const void* k, const void* v,
  * span at most 2^46 elements; rows of a written tensor must not
  * overlap each other (RET_ERR_INVALID_ARG).  A written tensor may interleave
  * with other tensors (slices of one buffer) but must share no element with
- * them.  Any alignment of sequence tensors that is a multiple of their element
- * is accepted; rows whose pointers, strides and length are multiples of 16
- * bytes are moved fastest.  fp32 tensors (states, checkpoints, parameters and
+ * them.  Sequence tensors may have any alignment that is a multiple of their
+ * element; rows whose length, start and strides are multiples of 16 bytes are
+ * moved fastest.  fp32 tensors (states, checkpoints, parameters and
  * their gradients) are contiguous and 16-byte aligned.
  */
 typedef struct {
@@ -317,7 +317,7 @@ typedef struct {
  *                 Calls that overlap in time need workspaces of their own.
  * T = 0 copies state_in (or zeros) to state_out.  Arithmetic, states and
  * checkpoints are fp32; y is rounded to dt.  Limits: T <= 2^30, every tensor's
- * element count below 2^31.  Results do not depend on timing: the same call
+ * element count below 2^31, B*H*ceil(d/16) <= 2^21 for T > 1.  Results do not depend on timing: the same call
  * gives the same bits.
  */
 ret_status retention_gated_scan_fwd(const void* x, const void* f, const float* rate, const float* state_in,
@@ -377,7 +377,7 @@ ret_status retention_gated_scan_step(const void* x, const void* f, const float* 
  *   weight, bias : nullable (ones, zeros); device fp32 [H,dv].
  *   eps       : finite, >= 0.
  *   strides   : y, gate, out.
- * dv <= RET_MAX_DV.  Arithmetic is fp32; out is rounded once.  An infinite
+ * dv <= RET_MAX_DV, H <= 65535, B*H*T <= 2^28.  Arithmetic is fp32; out is rounded once.  An infinite
  * gate gives NaN where the formula does (gate = -inf: -inf * 0).
  */
 ret_status retention_group_norm_gated(const void* y, const void* gate, const float* weight, const float* bias,
@@ -415,7 +415,7 @@ size_t retention_group_norm_gated_bwd_workspace_bytes(int B, int H, int T, int d
  *   r, n   : written, [rows,D] in dt.
  *   row_strides : HOST array of the distances between rows, in elements, of
  *            x, f, r, n; NULL: D.  The rules of ret_strides hold.
- * 1 <= D <= 16384, rows * D < 2^31.  Arithmetic is fp32.
+ * 1 <= D <= 16384, rows <= 2^28, rows * D < 2^31.  Arithmetic is fp32.
  */
 ret_status retention_residual_norm(const void* x, const void* f, const float* weight, const float* bias,
                                    const float* scale, float alpha, float eps, int rms, void* r, void* n,

@@ -182,6 +182,25 @@ ret_status check_sizes(const char* fn, int B, int H, int T, int d, ret_dtype dt)
   return RET_OK;
 }
 
+// Launch sizes: a grid has fewer than 2^32 threads, 65535 workgroups along y.
+constexpr long long kMaxRuns = 1LL << 21;  // tiles of channels of a scan
+constexpr long long kMaxRows = 1LL << 28;  // rows of a norm
+constexpr int kMaxNormHeads = 65535;
+
+ret_status check_runs(const char* fn, int B, int H, int T, int d) {
+  if (T > 1 && static_cast<long long>(B) * H * ((d + 15LL) / 16) > kMaxRuns)
+    return fail(RET_ERR_UNSUPPORTED, "%s: B*H*ceil(d/16) exceeds 2^21", fn);
+  return RET_OK;
+}
+
+ret_status check_norm(const char* fn, int B, int H, int T, int dv) {
+  if (dv > RET_MAX_DV) return fail(RET_ERR_UNSUPPORTED, "%s: dv=%d exceeds %d", fn, dv, RET_MAX_DV);
+  if (H > kMaxNormHeads) return fail(RET_ERR_UNSUPPORTED, "%s: H=%d exceeds %d", fn, H, kMaxNormHeads);
+  if (static_cast<long long>(B) * H * T > kMaxRows)
+    return fail(RET_ERR_UNSUPPORTED, "%s: B*H*T exceeds 2^28", fn);
+  return RET_OK;
+}
+
 ret_status check_eps(const char* fn, float eps) {
   if (!std::isfinite(eps) || eps < 0.0f)
     return fail(RET_ERR_INVALID_ARG, "%s: eps=%g must be finite and >= 0", fn, static_cast<double>(eps));
@@ -206,6 +225,7 @@ ret_status check_rows(const char* fn, int rows, int D, float alpha, ret_dtype dt
   if (dt != RET_F32 && dt != RET_BF16)
     return fail(RET_ERR_UNSUPPORTED, "%s: dtype %d is not RET_F32 or RET_BF16", fn, static_cast<int>(dt));
   if (D > ret::kResidualMaxD) return fail(RET_ERR_UNSUPPORTED, "%s: D=%d exceeds %d", fn, D, ret::kResidualMaxD);
+  if (rows > kMaxRows) return fail(RET_ERR_UNSUPPORTED, "%s: rows=%d exceeds 2^28", fn, rows);
   if (static_cast<long long>(rows) * D > kMaxElems)
     return fail(RET_ERR_UNSUPPORTED, "%s: a tensor has 2^31 or more elements", fn);
   if (!std::isfinite(alpha))
@@ -243,6 +263,7 @@ extern "C" {
 
 size_t retention_gated_scan_workspace_bytes(int B, int H, int T, int d, ret_dtype dt) {
   if (check_sizes("retention_gated_scan_workspace_bytes", B, H, T, d, dt) != RET_OK) return kBad;
+  if (check_runs("retention_gated_scan_workspace_bytes", B, H, T, d) != RET_OK) return kBad;
   return ret::gated_scan_chain_bytes(B, H, T, d);
 }
 
@@ -253,6 +274,7 @@ size_t retention_gated_scan_checkpoint_bytes(int B, int H, int T, int d) {
 
 size_t retention_gated_scan_bwd_workspace_bytes(int B, int H, int T, int d, ret_dtype dt, int have_checkpoints) {
   if (check_sizes("retention_gated_scan_bwd_workspace_bytes", B, H, T, d, dt) != RET_OK) return kBad;
+  if (check_runs("retention_gated_scan_bwd_workspace_bytes", B, H, T, d) != RET_OK) return kBad;
   const size_t kept = have_checkpoints ? 0 : static_cast<size_t>(checkpoint_floats(B, H, T, d)) * 4;
   return own_offset(kept) + ret::gated_scan_chain_bytes(B, H, T, d);
 }
@@ -263,6 +285,7 @@ ret_status retention_gated_scan_fwd(const void* x, const void* f, const float* r
                                     size_t workspace_bytes, void* stream) {
   const char* fn = "retention_gated_scan_fwd";
   ret_status st = check_sizes(fn, B, H, T, d, dt);
+  if (st == RET_OK) st = check_runs(fn, B, H, T, d);
   if (st == RET_OK) st = check_rates(fn, rate, H);
   if (st != RET_OK) return st;
   const Strides3 c = contiguous_bhtd(H, T, d);
@@ -293,6 +316,7 @@ ret_status retention_gated_scan_bwd(const void* x, const void* f, const float* r
                                     size_t workspace_bytes, void* stream) {
   const char* fn = "retention_gated_scan_bwd";
   ret_status st = check_sizes(fn, B, H, T, d, dt);
+  if (st == RET_OK) st = check_runs(fn, B, H, T, d);
   if (st == RET_OK) st = check_rates(fn, rate, H);
   if (st != RET_OK) return st;
   const Strides3 c = contiguous_bhtd(H, T, d);
@@ -359,7 +383,8 @@ ret_status retention_group_norm_gated(const void* y, const void* gate, const flo
   ret_status st = check_sizes(fn, B, H, T, dv, dt);
   if (st == RET_OK) st = check_eps(fn, eps);
   if (st != RET_OK) return st;
-  if (dv > RET_MAX_DV) return fail(RET_ERR_UNSUPPORTED, "%s: dv=%d exceeds %d", fn, dv, RET_MAX_DV);
+  st = check_norm(fn, B, H, T, dv);
+  if (st != RET_OK) return st;
   const Strides3 sy = given(strides, 0, contiguous_bhtd(H, T, dv)), sz = given(strides, 1, contiguous_bthd(H, T, dv)),
                  so = given(strides, 2, contiguous_bthd(H, T, dv));
   const long long np = static_cast<long long>(H) * dv;
@@ -377,7 +402,7 @@ ret_status retention_group_norm_gated(const void* y, const void* gate, const flo
 size_t retention_group_norm_gated_bwd_workspace_bytes(int B, int H, int T, int dv) {
   const char* fn = "retention_group_norm_gated_bwd_workspace_bytes";
   if (check_sizes(fn, B, H, T, dv, RET_F32) != RET_OK) return kBad;
-  if (dv > RET_MAX_DV) return kBad;
+  if (check_norm(fn, B, H, T, dv) != RET_OK) return kBad;
   return T == 0 ? 0 : static_cast<size_t>(2) * ret::gate_norm_bwd_slabs(B, H, T, dv) * H * dv * 4;
 }
 
@@ -390,7 +415,8 @@ ret_status retention_group_norm_gated_bwd(const void* y, const void* gate, const
   ret_status st = check_sizes(fn, B, H, T, dv, dt);
   if (st == RET_OK) st = check_eps(fn, eps);
   if (st != RET_OK) return st;
-  if (dv > RET_MAX_DV) return fail(RET_ERR_UNSUPPORTED, "%s: dv=%d exceeds %d", fn, dv, RET_MAX_DV);
+  st = check_norm(fn, B, H, T, dv);
+  if (st != RET_OK) return st;
   if ((gate == nullptr) != (grad_gate == nullptr) && T > 0)
     return fail(RET_ERR_INVALID_ARG, "%s: gate and grad_gate are given together or not at all", fn);
   const Strides3 head = contiguous_bhtd(H, T, dv), token = contiguous_bthd(H, T, dv);

@@ -46,6 +46,7 @@ C = (256, 128, 16)  # contiguous strides of [1,2,8,16]
     (dict(T=(1 << 30) + 1, d=1, H=1, rate=fl(1.0)), UNSUPPORTED, "2^30"),
     (dict(B=1 << 10, T=1 << 20), UNSUPPORTED, "2^31"),
     (dict(B=1 << 30, H=1 << 30, rate=fl(1.0)), UNSUPPORTED, "2^31"),
+    (dict(B=(1 << 21) + 1, H=1, T=2, rate=fl(1.0)), UNSUPPORTED, "2^21"),
     (dict(rate=None), INVALID, "rate"),
     (dict(rate=fl(1.0, 0.0)), INVALID, "rate[1]"),
     (dict(rate=fl(-1.0, 1.0)), INVALID, "rate[0]"),
@@ -146,6 +147,8 @@ def gnb(lib, y=at(1), z=at(2), w=at(8), b=None, eps=1e-5, do=at(3), gy=at(4), gz
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(B=0), INVALID, "B=0"),
     (dict(dv=513), UNSUPPORTED, "513"),
+    (dict(H=65536), UNSUPPORTED, "65536"),
+    (dict(T=1 << 28, dv=1), UNSUPPORTED, "2^28"),
     (dict(dt=2), UNSUPPORTED, "dtype"),
     (dict(eps=-1e-5), INVALID, "eps"),
     (dict(eps=float("nan")), INVALID, "eps"),
@@ -200,6 +203,7 @@ def ll(*v):
     (dict(rows=-1), INVALID, "rows=-1"),
     (dict(D=0), INVALID, "D=0"),
     (dict(D=16385), UNSUPPORTED, "16385"),
+    (dict(rows=(1 << 28) + 1, D=1), UNSUPPORTED, "2^28"),
     (dict(rows=1 << 20, D=4096), UNSUPPORTED, "2^31"),
     (dict(alpha=float("inf")), INVALID, "alpha"),
     (dict(eps=-1.0), INVALID, "eps"),

@@ -146,6 +146,9 @@ CASES = [
     (1, 1, 1500, 201, torch.bfloat16, False, True, 0.003),
     (2, 1, 2300, 24, torch.bfloat16, True, True, 0.003),
     (1, 2, 4500, 12, torch.float32, False, True, 0.003),
+    (1, 130, 4300, 4, torch.bfloat16, True, True, 0.001),  # two head groups on one workspace
+    (1, 1, 8000, 3, torch.float32, False, True, 0.001),
+    (2, 2, 1200, 65, torch.float32, True, True, 0.003),  # one channel in the last tile
     (1, 2, 9000, 40, torch.bfloat16, False, True, 0.0005),
 ]
 
@@ -344,6 +347,45 @@ def test_graph_replays_and_other_streams(B, H, T, d):
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
         ret.gated_scan_fwd(x[:, :, : T // 2], f[:, :, : T // 2], rate)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("B,H,T,d,dtype", [(2, 4, 1500, 64, torch.bfloat16), (3, 5, 1337, 201, torch.float32)])
+def test_other_inputs_on_the_same_workspace(B, H, T, d, dtype):
+    """Calls of different inputs one after the other, on workspaces that hold the last call's words: each
+    gives the bits it gives alone.  A call over another call's inputs in a captured graph too."""
+    rate = rates(H)
+    sets = [[t.to(DEV) for t in make(B, H, T, d, dtype, seed=60 + i, reset=0.003)] for i in range(3)]
+    lib = ret.load()
+    fb = lib.retention_gated_scan_workspace_bytes(B, H, T, d, 1)
+    bb = lib.retention_gated_scan_bwd_workspace_bytes(B, H, T, d, 1, 1)
+    assert fb > 0 and bb > 0
+    ws, wb = (torch.full((n,), 0xA5, dtype=torch.uint8, device=DEV) for n in (fb, bb))
+
+    def step(v):
+        x, f, s, dy, ds = v
+        y, last, kept = ret.gated_scan_fwd(x, f, rate, s, normalize=True, checkpoints=True, workspace=ws)
+        return [y, last, *ret.gated_scan_bwd(x, f, rate, dy, s, ds, kept, True, workspace=wb)]
+
+    alone = []
+    for v in sets:
+        alone.append([t.clone() for t in step(v)])
+        torch.cuda.synchronize()
+    for _ in range(5):
+        got = [step(v) for v in sets]
+        torch.cuda.synchronize()
+        for g, a in zip(got, alone):
+            assert all(torch.equal(p, q) for p, q in zip(g, a))
+    held = [t.clone() for t in sets[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(held)
+    for i in (1, 2, 0, 1):
+        for t, v in zip(held, sets[i]):
+            t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, alone[i])), i
+        step(sets[(i + 1) % 3])
 
 
 def test_binding_refuses():
