@@ -8,7 +8,9 @@
 // LPR lanes hold a row in registers (8 elements each), so narrow heads share a
 // wave.  Sums over a row
 // are fp32: sum y (and p) first, then the squares and products about the
-// mean.  HBM bound: 3 elements move per value forward, 5 backward.
+// mean.  HBM bound: 3 elements move per value forward, 5 backward.  Measured:
+// B1 H8 T65536 dv512 bf16 forward 307 us (5.2 TB/s), B4 H8 T2048 dv512 bf16
+// backward 67 us with the column sums (5.0 TB/s).
 #include "common.h"
 #include "kernels.h"
 #include "row_sum.h"
