@@ -12,9 +12,10 @@
 // one access of up to 16 bytes) and then along time, so a wave reads whole
 // runs of CW channels; every thread walks S consecutive tokens of its VEC
 // channels in registers.  Affine maps h -> A h + H compose associatively: each
-// thread forms the map of its S tokens, one wave composes the maps of the
-// NSEG segments in time order, and every thread replays its tokens from its
-// incoming value.  x and f are read once and y is written once.  Measured, bf16:
+// thread forms the map of its S tokens, the maps are composed in time order
+// (within a wave, then over the waves), and every thread replays its tokens
+// from its incoming value.  x and f are read once and y is written once.
+// Measured, bf16:
 // B4 H8 T2048 d512 forward 41 us (4.9 TB/s), B2 H16 T8192 d512 forward 160 us
 // and backward 284 us (5.0 and 4.7 TB/s), B1 H8 T65536 d512 forward 333 us with
 // the workspace's fill (4.8 TB/s).
@@ -306,8 +307,8 @@ struct Queue {
 template <int VEC, int CW, int NW, int PT = kPerThread>
 struct Place {
   static constexpr int S = PT / VEC, LC = CW / VEC, TG = 64 / LC, NSEG = NW * TG, TT = NSEG * S;
-  // a tile's checkpoints
-  static constexpr int BLOCKS = NW * PT / kBlockElems, CSEG = NSEG / BLOCKS, BLOCK = TT / BLOCKS;
+  // a tile's checkpoints, one every PER waves
+  static constexpr int BLOCKS = NW * PT / kBlockElems, PER = NW / BLOCKS, BLOCK = TT / BLOCKS;
   int lane, wave, lc, seg;
   __device__ Place()
       : lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), lc((threadIdx.x & 63) % LC),
@@ -346,6 +347,63 @@ struct Columns {
     }
   }
 };
+
+// A tile's maps are composed in two steps: every wave those of its own TG
+// segments, which only its own lanes have written, then one wave those of the
+// NW waves.  With one wave over all segments the others waited longer (bf16:
+// B4 H8 T2048 d512 forward 43.7 us in place of 42.0; B1 H8 T32768 d512 forward
+// and backward 536 in place of 498).
+__device__ __forceinline__ void wave_sync() {  // LDS writes of the wave's lanes before, reads after
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// segA, segH: the segments' maps h -> A h + H, replaced by the map of the
+// wave's segments before each; wA, wH: the wave's map.
+template <typename P, int CW>
+__device__ __forceinline__ void compose_wave(const P& pl, float (*segA)[CW], float (*segH)[CW], float (*wA)[CW],
+                                             float (*wH)[CW]) {
+  wave_sync();
+  if (pl.lane < CW) {
+    float a = 1.0f, h = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P::TG; ++i) {
+      const int k = pl.wave * P::TG + i;
+      const float ai = segA[k][pl.lane], hi = segH[k][pl.lane];
+      segA[k][pl.lane] = a;
+      segH[k][pl.lane] = h;
+      a *= ai;
+      h = fmaf(ai, h, hi);
+    }
+    wA[pl.wave][pl.lane] = a;
+    wH[pl.wave][pl.lane] = h;
+  }
+  wave_sync();
+}
+
+// The same in both directions: also G -> A G + segG from the wave's last
+// segment on, replaced with its products segB by the map of the segments
+// behind each.
+template <typename P, int CW>
+__device__ __forceinline__ void compose_wave(const P& pl, float (*segA)[CW], float (*segH)[CW], float (*segB)[CW],
+                                             float (*segG)[CW], float (*wA)[CW], float (*wH)[CW], float (*wG)[CW]) {
+  wave_sync();
+  if (pl.lane < CW) {
+    float b = 1.0f, g = 0.0f;
+#pragma unroll 2
+    for (int i = P::TG - 1; i >= 0; --i) {
+      const int k = pl.wave * P::TG + i;
+      const float ai = segA[k][pl.lane], gi = segG[k][pl.lane];
+      segB[k][pl.lane] = b;
+      segG[k][pl.lane] = g;
+      b *= ai;
+      g = fmaf(ai, g, gi);
+    }
+    wG[pl.wave][pl.lane] = g;
+  }
+  compose_wave<P, CW>(pl, segA, segH, wA, wH);
+}
 
 // ---- Forward ----
 template <typename E, int VEC, int CW, int NW, int PT, bool kNorm, bool kWhole>
@@ -488,8 +546,10 @@ template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole>
 __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanFwd p, HeadRate rates, int h0, int nh,
                                                                        int nct) {
   using P = Place<VEC, CW, NW>;
-  __shared__ float segA[2][P::NSEG][CW];
-  __shared__ float segH[2][P::NSEG][CW];
+  __shared__ float segA[P::NSEG][CW];
+  __shared__ float segH[P::NSEG][CW];
+  __shared__ float waveA[2][NW][CW];
+  __shared__ float waveH[2][NW][CW];
   const P pl;
   const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
   FwdThread<E, VEC, CW, NW, kPerThread, kNorm, kWhole> th(p, pl, rates.r[tl.hl]);
@@ -516,19 +576,20 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
     th.map(A, H);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      th.cols.put(segA[q][pl.seg], e, A[e]);
-      th.cols.put(segH[q][pl.seg], e, H[e]);
+      th.cols.put(segA[pl.seg], e, A[e]);
+      th.cols.put(segH[pl.seg], e, H[e]);
     }
+    compose_wave<P, CW>(pl, segA, segH, waveA[q], waveH[q]);
     __syncthreads();
     if (mine) {
 #pragma unroll
       for (int k = 0; k < P::BLOCKS; ++k) {
         const int block = chunk * P::BLOCKS + k;
         if (kept && p.checkpoints != nullptr && block < nblock) p.checkpoints[(bh * nblock + block) * p.d + ch] = carry;
-#pragma unroll 8
-        for (int i = k * P::CSEG; i < (k + 1) * P::CSEG; ++i) {
-          const float a = segA[q][i][pl.lane], hh = segH[q][i][pl.lane];
-          segH[q][i][pl.lane] = carry;
+#pragma unroll
+        for (int i = k * P::PER; i < (k + 1) * P::PER; ++i) {
+          const float a = waveA[q][i][pl.lane], hh = waveH[q][i][pl.lane];
+          waveH[q][i][pl.lane] = carry;
           carry = fmaf(a, carry, hh);
         }
       }
@@ -536,7 +597,8 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
     __syncthreads();
     float h[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) h[e] = th.cols.get(segH[q][pl.seg], e);
+    for (int e = 0; e < VEC; ++e)
+      h[e] = fmaf(th.cols.get(segA[pl.seg], e), th.cols.get(waveH[q][pl.wave], e), th.cols.get(segH[pl.seg], e));
     th.replay(chunk, th.cm, th.x, h);
   }
   if (kept && p.state_out != nullptr) p.state_out[bh * p.d + ch] = carry;
@@ -554,6 +616,8 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
   using Th = FwdThread<E, VEC, CW, NW, PT, kNorm, kWhole>;
   __shared__ float segA[P::NSEG][CW];
   __shared__ float segH[P::NSEG][CW];
+  __shared__ float waveA[NW][CW];
+  __shared__ float waveH[NW][CW];
   __shared__ float enter[CW];
   __shared__ unsigned ticket;
   __shared__ float gate[kTable ? kGateN : 1];
@@ -577,6 +641,7 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
       th.cols.put(segA[pl.seg], e, A[e]);
       th.cols.put(segH[pl.seg], e, H[e]);
     }
+    compose_wave<P, CW>(pl, segA, segH, waveA, waveH);
     __syncthreads();
     if (threadIdx.x == 64) ticket = qu.take();
     if (pl.wave == 0 && pl.lane < CW) {
@@ -586,16 +651,16 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
       Entering<CW> in;
       in.begin(cn, chunk, tile, pl.lane);
       const float first = kept && chunk < kGroup && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
-      float a = 1.0f, h = 0.0f, ca[P::BLOCKS], chh[P::BLOCKS];  // the map of the segments so far, and at the blocks
+      float a = 1.0f, h = 0.0f, ca[P::BLOCKS], chh[P::BLOCKS];  // the map of the waves so far, and at the blocks
 #pragma unroll
       for (int k = 0; k < P::BLOCKS; ++k) {
         ca[k] = a;
         chh[k] = h;
-#pragma unroll 8
-        for (int i = k * P::CSEG; i < (k + 1) * P::CSEG; ++i) {
-          const float ai = segA[i][pl.lane], hi = segH[i][pl.lane];
-          segA[i][pl.lane] = a;
-          segH[i][pl.lane] = h;
+#pragma unroll
+        for (int i = k * P::PER; i < (k + 1) * P::PER; ++i) {
+          const float ai = waveA[i][pl.lane], hi = waveH[i][pl.lane];
+          waveA[i][pl.lane] = a;
+          waveH[i][pl.lane] = h;
           a *= ai;
           h = fmaf(ai, h, hi);
         }
@@ -615,11 +680,13 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
     __syncthreads();
     float h[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      h[e] = fmaf(th.cols.get(segA[pl.seg], e), th.cols.get(enter, e), th.cols.get(segH[pl.seg], e));
+    for (int e = 0; e < VEC; ++e) {
+      const float v = fmaf(th.cols.get(waveA[pl.wave], e), th.cols.get(enter, e), th.cols.get(waveH[pl.wave], e));
+      h[e] = fmaf(th.cols.get(segA[pl.seg], e), v, th.cols.get(segH[pl.seg], e));
+    }
     cur = uniform(ticket);
     th.template packed_replay<kTable>(chunk, gate, h);
-    __syncthreads();  // the segments, the entering values and the ticket are read
+    __syncthreads();  // the waves' maps, the entering values and the ticket are read
   }
 }
 
@@ -739,9 +806,13 @@ template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole>
 __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanBwd p, HeadRate rates, int h0, int nh,
                                                                        int nct) {
   using P = Place<VEC, CW, NW>;
-  __shared__ float segA[2][P::NSEG][CW];
-  __shared__ float segH[2][P::NSEG][CW];
-  __shared__ float segG[2][P::NSEG][CW];
+  __shared__ float segA[P::NSEG][CW];
+  __shared__ float segH[P::NSEG][CW];
+  __shared__ float segB[P::NSEG][CW];  // products of A behind a segment
+  __shared__ float segG[P::NSEG][CW];
+  __shared__ float waveA[2][NW][CW];
+  __shared__ float waveH[2][NW][CW];
+  __shared__ float waveG[2][NW][CW];
   const P pl;
   const ScanTile tl = decode_tile(blockIdx.x, nct, nh, h0, CW);
   BwdThread<E, VEC, CW, NW, kNorm, kWhole> th(p, pl, rates.r[tl.hl]);
@@ -768,32 +839,38 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanB
     for (int e = 0; e < VEC; ++e) {
       float A, H, R;
       th.map(e, A, H, R);
-      th.cols.put(segA[q][pl.seg], e, A);
-      th.cols.put(segH[q][pl.seg], e, H);
-      th.cols.put(segG[q][pl.seg], e, R);
+      th.cols.put(segA[pl.seg], e, A);
+      th.cols.put(segH[pl.seg], e, H);
+      th.cols.put(segG[pl.seg], e, R);
     }
+    compose_wave<P, CW>(pl, segA, segH, segB, segG, waveA[q], waveH[q], waveG[q]);
     __syncthreads();
     if (pl.wave == 0 && pl.lane < CW) {
       float cur = ckpt;
-#pragma unroll 8
-      for (int i = 0; i < P::NSEG; ++i) {
-        const float a = segA[q][i][pl.lane], hh = segH[q][i][pl.lane];
-        segH[q][i][pl.lane] = cur;
+#pragma unroll 4
+      for (int i = 0; i < NW; ++i) {
+        const float a = waveA[q][i][pl.lane], hh = waveH[q][i][pl.lane];
+        waveH[q][i][pl.lane] = cur;
         cur = fmaf(a, cur, hh);
       }
     } else if (pl.wave == 1 && pl.lane < CW) {
-#pragma unroll 8
-      for (int i = P::NSEG - 1; i >= 0; --i) {
-        const float a = segA[q][i][pl.lane], gg = segG[q][i][pl.lane];
-        segG[q][i][pl.lane] = carry;
+#pragma unroll 4
+      for (int i = NW - 1; i >= 0; --i) {
+        const float a = waveA[q][i][pl.lane], gg = waveG[q][i][pl.lane];
+        waveG[q][i][pl.lane] = carry;
         carry = fmaf(a, carry, gg);
       }
     }
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      th.replay_state(e, th.cols.get(segH[q][pl.seg], e));
-      th.replay_grad(e, th.cols.get(segG[q][pl.seg], e), th.cm, th.dy, th.kf);
+      // one channel at a time: interleaved they hold more registers (B2 H16 T8192
+      // d512 bf16, forward and backward, 452 us in place of 440)
+      __builtin_amdgcn_sched_barrier(0);
+      th.replay_state(e, fmaf(th.cols.get(segA[pl.seg], e), th.cols.get(waveH[q][pl.wave], e),
+                              th.cols.get(segH[pl.seg], e)));
+      th.replay_grad(e, fmaf(th.cols.get(segB[pl.seg], e), th.cols.get(waveG[q][pl.wave], e),
+                             th.cols.get(segG[pl.seg], e)), th.cm, th.dy, th.kf);
     }
     th.write(chunk, th.dy, th.kf);
   }
@@ -809,6 +886,10 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
   __shared__ float segH[P::NSEG][CW];
   __shared__ float segG[P::NSEG][CW];
   __shared__ float segB[P::NSEG][CW];  // products of A behind a segment
+  __shared__ float waveA[NW][CW];
+  __shared__ float waveH[NW][CW];
+  __shared__ float waveB[NW][CW];
+  __shared__ float waveG[NW][CW];
   __shared__ float enter[CW];
   __shared__ unsigned tickets[2];
   __shared__ float2 gate[kTable ? kGateN : 1];
@@ -852,24 +933,25 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
       th.cols.put(segH[pl.seg], e, H);
       th.cols.put(segG[pl.seg], e, R);
     }
+    compose_wave<P, CW>(pl, segA, segH, segB, segG, waveA, waveH, waveG);
     __syncthreads();
     if (threadIdx.x == 128 && next < qu.total) tickets[0] = qu.take();
     if (pl.wave == 0 && channel) {
-#pragma unroll 8
-      for (int i = 0; i < P::NSEG; ++i) {
-        const float a = segA[i][pl.lane], hh = segH[i][pl.lane];
-        segH[i][pl.lane] = start;
+#pragma unroll 4
+      for (int i = 0; i < NW; ++i) {
+        const float a = waveA[i][pl.lane], hh = waveH[i][pl.lane];
+        waveH[i][pl.lane] = start;
         start = fmaf(a, start, hh);
       }
     } else if (pl.wave == 1 && channel) {
       Entering<CW> in;
       in.begin(cn, step, tile, pl.lane);
-      float a = 1.0f, g = 0.0f;  // the map of the segments behind
-#pragma unroll 8
-      for (int i = P::NSEG - 1; i >= 0; --i) {
-        const float ai = segA[i][pl.lane], gi = segG[i][pl.lane];
-        segB[i][pl.lane] = a;
-        segG[i][pl.lane] = g;
+      float a = 1.0f, g = 0.0f;  // the map of the waves behind
+#pragma unroll 4
+      for (int i = NW - 1; i >= 0; --i) {
+        const float ai = waveA[i][pl.lane], gi = waveG[i][pl.lane];
+        waveB[i][pl.lane] = a;
+        waveG[i][pl.lane] = g;
         a *= ai;
         g = fmaf(ai, g, gi);
       }
@@ -881,13 +963,14 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      th.replay_state(e, th.cols.get(segH[pl.seg], e));
-      th.replay_grad(e, fmaf(th.cols.get(segB[pl.seg], e), th.cols.get(enter, e), th.cols.get(segG[pl.seg], e)), th.cm,
-                     th.dy, th.kf);
+      th.replay_state(e, fmaf(th.cols.get(segA[pl.seg], e), th.cols.get(waveH[pl.wave], e),
+                              th.cols.get(segH[pl.seg], e)));
+      const float v = fmaf(th.cols.get(waveB[pl.wave], e), th.cols.get(enter, e), th.cols.get(waveG[pl.wave], e));
+      th.replay_grad(e, fmaf(th.cols.get(segB[pl.seg], e), v, th.cols.get(segG[pl.seg], e)), th.cm, th.dy, th.kf);
     }
     cur = next;
     next = uniform(tickets[0]);
-    __syncthreads();  // the segments, the entering values and the ticket are read
+    __syncthreads();  // the waves' maps, the entering values and the ticket are read
     th.write(chunk, th.dy, th.kf);
     if (cur >= qu.total) break;
   }
