@@ -43,6 +43,10 @@ constexpr int kBlockElems = 128;  // a checkpoint's block: as many elements per 
 // and in fp32 128 x 4096 83 / 76 (140 / 118), 256 x 4096 140 / 144 (199 / 229).
 constexpr int kWalkTiles = 160, kChainSteps = 8;
 constexpr int kTableTiles = 4;  // tiles of a workgroup from which on its gate table pays
+// A workgroup that walks a run uses a table, and 16 waves, where the run is
+// longer than so many blocks of tokens.  With / without, us, 1280 runs of d 64:
+//   T 128   28 / 17 (backward 40 / 31)    T 256   32 / 29 (45 / 53)    T 512   52 / 54 (76 / 104)
+constexpr int kTableStepsFwd = 2, kTableStepsBwd = 1;
 
 typedef unsigned long long u64;
 
@@ -542,7 +546,7 @@ struct FwdThread {
 };
 
 // One workgroup walks the tiles of a channel run from the first token on.
-template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole>
+template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole, bool kTable>
 __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanFwd p, HeadRate rates, int h0, int nh,
                                                                        int nct) {
   using P = Place<VEC, CW, NW>;
@@ -562,7 +566,6 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
   float carry = kept && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
   const int nchunk = (p.T + P::TT - 1) / P::TT, nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
   th.load(0);
-  constexpr bool kTable = sizeof(E) == 2;
   __shared__ float gate[kTable ? kGateN : 1];
   if constexpr (kTable) {
     build_gate_table(gate, th.rate, 64 * NW);
@@ -802,7 +805,7 @@ struct BwdThread {
 };
 
 // One workgroup walks the tiles of a channel run from the last token on.
-template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole>
+template <typename E, int VEC, int CW, int NW, bool kNorm, bool kWhole, bool kTable>
 __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanBwd p, HeadRate rates, int h0, int nh,
                                                                        int nct) {
   using P = Place<VEC, CW, NW>;
@@ -824,7 +827,6 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_walk_kernel(GatedScanB
   float carry = pl.wave == 1 && kept && p.grad_state_out != nullptr ? p.grad_state_out[bh * p.d + ch] : 0.0f;
   const int nchunk = (p.T + P::TT - 1) / P::TT, nblock = (p.T + P::BLOCK - 1) / P::BLOCK;
   th.load(nchunk - 1);
-  constexpr bool kTable = sizeof(E) == 2;
   __shared__ float2 gate[kTable ? kGateN : 1];
   if constexpr (kTable) {
     build_gate_table(gate, th.rate, 64 * NW);
@@ -1067,13 +1069,21 @@ bool many_tiles(int B, int nh, int T, int d, int elems, int per_cu) {
   const ChainSizes z = chain_sizes(B, nh, T, d, elems);
   return static_cast<long>(z.steps) * z.tiles >= static_cast<long>(kTableTiles) * chain_blocks(z.steps, z.tiles, nh, per_cu);
 }
+// Whether a run is longer than so many blocks.
+bool longer(int T, int d, int blocks) { return T > blocks * tile_tokens(d, kBlockElems); }
 
 template <typename E, int VEC, int CW, bool kNorm, bool kWhole>
 hipError_t run_fwd(const GatedScanFwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int nct = (p.d + CW - 1) / CW;
   if (!chained(p.B, p.H, p.T, p.d)) {
+    const dim3 runs(p.B * g.nh * nct);
+    if (sizeof(E) == 2 && !longer(p.T, p.d, kTableStepsFwd)) {
+      hipLaunchKernelGGL((gated_scan_fwd_walk_kernel<E, VEC, CW, 8, kNorm, kWhole, false>), runs, dim3(64 * 8), 0, s, p,
+                         head_rates(g), g.h0, g.nh, nct);
+      return hipGetLastError();
+    }
     constexpr int NW = VEC == 1 ? 8 : 16;
-    hipLaunchKernelGGL((gated_scan_fwd_walk_kernel<E, VEC, CW, NW, kNorm, kWhole>), dim3(p.B * g.nh * nct), dim3(64 * NW), 0,
+    hipLaunchKernelGGL((gated_scan_fwd_walk_kernel<E, VEC, CW, NW, kNorm, kWhole, sizeof(E) == 2>), runs, dim3(64 * NW), 0,
                        s, p, head_rates(g), g.h0, g.nh, nct);
     return hipGetLastError();
   }
@@ -1105,8 +1115,14 @@ template <typename E, int VEC, int CW, bool kNorm, bool kWhole>
 hipError_t run_bwd(const GatedScanBwd& p, void* ws, const HeadGroup& g, hipStream_t s) {
   const int nct = (p.d + CW - 1) / CW;
   if (!chained(p.B, p.H, p.T, p.d)) {
-    constexpr int NW = sizeof(E) == 4 || VEC == 1 ? 8 : 16;  // what fits 512 / (NW / 4) registers without spills
-    hipLaunchKernelGGL((gated_scan_bwd_walk_kernel<E, VEC, CW, NW, kNorm, kWhole>), dim3(p.B * g.nh * nct), dim3(64 * NW), 0,
+    const dim3 runs(p.B * g.nh * nct);
+    if (sizeof(E) == 2 && !longer(p.T, p.d, kTableStepsBwd)) {
+      hipLaunchKernelGGL((gated_scan_bwd_walk_kernel<E, VEC, CW, 8, kNorm, kWhole, false>), runs, dim3(64 * 8), 0, s, p,
+                         head_rates(g), g.h0, g.nh, nct);
+      return hipGetLastError();
+    }
+    constexpr int NW = sizeof(E) == 4 || VEC == 1 ? 8 : 16;  // by the registers of a thread, 512 / (NW / 4)
+    hipLaunchKernelGGL((gated_scan_bwd_walk_kernel<E, VEC, CW, NW, kNorm, kWhole, sizeof(E) == 2>), runs, dim3(64 * NW), 0,
                        s, p, head_rates(g), g.h0, g.nh, nct);
     return hipGetLastError();
   }

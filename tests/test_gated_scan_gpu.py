@@ -171,6 +171,25 @@ def test_scan_matches_oracle(B, H, T, d, dtype, normalize, state, reset):
     assert torch.equal(X.cpu(), x) and torch.equal(DY.cpu(), dy)
 
 
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize(
+    "T,d",
+    [(2, 64), (128, 39), (129, 64), (200, 66), (256, 68), (257, 39), (700, 64), (900, 65),
+     (256, 32), (512, 29), (513, 32), (1700, 30), (512, 16), (1024, 13), (1025, 16), (3000, 9), (1025, 3), (3000, 2)],
+)
+def test_walked_bf16_runs(T, d, normalize):
+    """Few blocks of tokens, on both sides of the lengths from which a run's gates are looked up."""
+    H = 3
+    x, f, s, dy, ds = make(2, H, T, d, torch.bfloat16, seed=7 * T + d, reset=0.004)
+    f[1, 1, T // 2, d // 2] = 300.0
+    f[0, 2, T - 1, 0] = -300.0
+    rate = rates(H)
+    y, last, kept = ret.gated_scan_fwd(x.to(DEV), f.to(DEV), rate, s.to(DEV), normalize=normalize, checkpoints=True)
+    check_forward(f"walked {T} {d} {normalize}", x, f, rate, s, normalize, y, last)
+    got = ret.gated_scan_bwd(x.to(DEV), f.to(DEV), rate, dy.to(DEV), s.to(DEV), ds.to(DEV), kept, normalize)
+    check_backward(f"walked {T} {d} {normalize}", x, f, rate, dy, s, ds, normalize, got)
+
+
 @pytest.mark.parametrize("normalize,d", [(True, 512), (False, 510)])
 def test_long_bf16_sequence(normalize, d):
     """Enough chained tiles for every workgroup to look its gates up, among them gates outside the table."""
