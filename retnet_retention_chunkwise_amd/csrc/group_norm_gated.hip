@@ -246,6 +246,9 @@ hipError_t run_bwd(const GateNormBwd& a, float* partial, int slabs, hipStream_t 
   return hipGetLastError();
 }
 
+// Rows of at most 4 pieces take 4 lanes.  Against 8 (110 heads of 4454 tokens,
+// us, forward and backward): bf16 dv 8 24 + 39 / 35 + 66, dv 32 30 + 52 / 34 + 67;
+// fp32 dv 16 37 + 60 / 36 + 63, but dv 32, two pieces to a lane, 51 + 96 / 39 + 79.
 template <typename E, int VEC>
 hipError_t fwd_by_lanes(const GateNormFwd& a, hipStream_t s) {
   if constexpr (VEC == 1) {
@@ -255,7 +258,7 @@ hipError_t fwd_by_lanes(const GateNormFwd& a, hipStream_t s) {
       case 64: return run_fwd<E, VEC, 64>(a, s);
       case 32: return run_fwd<E, VEC, 32>(a, s);
       case 16: return run_fwd<E, VEC, 16>(a, s);
-      default: return run_fwd<E, VEC, 8>(a, s);
+      default: return a.dv > 4 * VEC ? run_fwd<E, VEC, 8>(a, s) : run_fwd<E, VEC, 4>(a, s);
     }
   }
 }
@@ -268,7 +271,7 @@ hipError_t bwd_by_lanes(const GateNormBwd& a, float* partial, int slabs, hipStre
       case 64: return run_bwd<E, VEC, 64>(a, partial, slabs, s);
       case 32: return run_bwd<E, VEC, 32>(a, partial, slabs, s);
       case 16: return run_bwd<E, VEC, 16>(a, partial, slabs, s);
-      default: return run_bwd<E, VEC, 8>(a, partial, slabs, s);
+      default: return a.dv > 4 * VEC ? run_bwd<E, VEC, 8>(a, partial, slabs, s) : run_bwd<E, VEC, 4>(a, partial, slabs, s);
     }
   }
 }
@@ -283,7 +286,7 @@ hipError_t launch_gate_norm_fwd(const GateNormFwd& a, hipStream_t s) {
 
 int gate_norm_bwd_slabs(int B, int H, int T, int dv) {
   const long groups = static_cast<long>(B) * T;  // rows of one head
-  const long per = kThreads / lanes_for(dv);     // rows in a workgroup at once
+  const long per = kThreads / lanes_for(dv);     // rows in a workgroup at once (twice that with 4 lanes)
   const long most = (groups + per - 1) / per;
   const long want = (1024 + H - 1) / H;  // about four workgroups on each of 256 compute units
   return static_cast<int>(want < most ? want : most);

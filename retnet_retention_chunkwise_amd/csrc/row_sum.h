@@ -15,10 +15,10 @@ __device__ __forceinline__ float dpp_add(float v) {
 
 template <int N>
 __device__ __forceinline__ float lanes_sum(float v) {
-  static_assert(N == 8 || N == 16 || N == 32 || N == 64, "lanes per row");
+  static_assert(N == 4 || N == 8 || N == 16 || N == 32 || N == 64, "lanes per row");
   v = dpp_add<0xB1>(v);                     // quad_perm [1,0,3,2]
   v = dpp_add<0x4E>(v);                     // quad_perm [2,3,0,1]
-  v = dpp_add<0x141>(v);                    // row_half_mirror: the other quad of 8 lanes
+  if constexpr (N >= 8) v = dpp_add<0x141>(v);   // row_half_mirror: the other quad of 8 lanes
   if constexpr (N >= 16) v = dpp_add<0x140>(v);  // row_mirror: the other 8 lanes of 16
   if constexpr (N >= 32) {
     const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);

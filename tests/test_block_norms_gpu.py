@@ -154,6 +154,15 @@ def test_gate_norm_without_gate_is_group_norm():
     assert rel_l2(out.transpose(1, 2), ret.group_norm(y, w, b)) <= 2.0 ** -8  # each rounds once
 
 
+NARROW = [(B, H, T, dv, dt) for B, H, T in ((1, 1, 1), (2, 3, 67), (3, 2, 700))
+          for dv in (1, 3, 4, 7, 8, 9, 15, 16, 25, 31, 32, 33) for dt in (torch.float32, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("B,H,T,dv,dtype", NARROW)
+def test_gate_norm_of_narrow_heads(B, H, T, dv, dtype):
+    test_gate_norm_matches_oracle(B, H, T, dv, dtype, True, True, True)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("dv", [64, 40, 33])
 def test_gate_norm_layouts_and_untouched_surroundings(dtype, dv):
