@@ -246,9 +246,16 @@ __device__ __forceinline__ unsigned take(unsigned* counter) {
   return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
 }
 
-// Hands a tile's map on: the lane's channel of the tile at step j.
+// Hands a tile's map on: the lane's channel of the tile at step j.  Only step 0
+// takes the value that enters the run (first), and publishes the constant map
+// of what leaves it: the call's final state may lie over its incoming one, and
+// the tile that writes it has waited for words that came from this read.
 template <int CW>
-__device__ __forceinline__ void publish_map(const Chain& c, int j, int tile, int lane, float A, float H) {
+__device__ __forceinline__ void publish_map(const Chain& c, int j, int tile, int lane, float A, float H, float first) {
+  if (j == 0) {
+    H = fmaf(A, first, H);
+    A = 0.0f;
+  }
   if (j % kGroup == kGroup - 1 || j == c.steps - 1) return;  // nobody folds it
   const long per = static_cast<long>(c.tiles) * CW;
   __hip_atomic_store(c.maps + j * per + static_cast<long>(tile) * CW + lane, static_cast<u64>(quiet(H)) << 32 | quiet(A),
@@ -270,7 +277,7 @@ struct Entering {
     for (int i = 0; i < kGroup - 1; ++i)
       if (i < k) m[i] = __hip_atomic_load(maps + i * per, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  // (A, H): the tile's map; first: the value that enters step 0
+  // (A, H): the tile's map; first: the value that enters step 0, finite at later steps (a constant map follows)
   __device__ __forceinline__ float end(const Chain& c, int j, int tile, int lane, float A, float H, float first) const {
     const long per = static_cast<long>(c.tiles) * CW, at = static_cast<long>(tile) * CW + lane;
     const int k = j % kGroup, g = j / kGroup;
@@ -653,7 +660,7 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
       const bool kept = ch < p.d;
       Entering<CW> in;
       in.begin(cn, chunk, tile, pl.lane);
-      const float first = kept && chunk < kGroup && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
+      const float first = kept && chunk == 0 && p.state_in != nullptr ? p.state_in[bh * p.d + ch] : 0.0f;
       float a = 1.0f, h = 0.0f, ca[P::BLOCKS], chh[P::BLOCKS];  // the map of the waves so far, and at the blocks
 #pragma unroll
       for (int k = 0; k < P::BLOCKS; ++k) {
@@ -668,7 +675,7 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_scan_fwd_chain_kernel(GatedS
           h = fmaf(ai, h, hi);
         }
       }
-      publish_map<CW>(cn, chunk, tile, pl.lane, a, h);
+      publish_map<CW>(cn, chunk, tile, pl.lane, a, h, first);
       const float v = in.end(cn, chunk, tile, pl.lane, a, h, first);
       enter[pl.lane] = v;
       if (kept) {
@@ -919,7 +926,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
     // wave 0: the state before the tile; wave 1: the gradient behind the sequence
     float start = 0.0f;
     if (pl.wave == 0 && kept) start = p.checkpoints[(bh * nblock + chunk * P::BLOCKS) * p.d + ch];
-    if (pl.wave == 1 && kept && step < kGroup && p.grad_state_out != nullptr) start = p.grad_state_out[bh * p.d + ch];
+    if (pl.wave == 1 && kept && step == 0 && p.grad_state_out != nullptr) start = p.grad_state_out[bh * p.d + ch];
     th.aim_stores(p, tl, pl);
     th.template unpack<kTable>(chunk, gate);
     if (next < qu.total) {
@@ -957,7 +964,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_bwd_chain_kernel(GatedScan
         a *= ai;
         g = fmaf(ai, g, gi);
       }
-      publish_map<CW>(cn, step, tile, pl.lane, a, g);
+      publish_map<CW>(cn, step, tile, pl.lane, a, g, start);
       const float v = in.end(cn, step, tile, pl.lane, a, g, start);
       enter[pl.lane] = v;
       if (kept && p.grad_state_in != nullptr && chunk == 0) p.grad_state_in[bh * p.d + ch] = fmaf(a, v, g);
