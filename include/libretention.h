@@ -347,6 +347,7 @@ size_t retention_gated_scan_checkpoint_bytes(int B, int H, int T, int d);
  *   grad_state_in  : nullable; written, fp32 [B,H,d]; may be grad_state_out exactly.
  *   strides        : x, f, grad_y, grad_x, grad_f.
  *   workspace      : retention_gated_scan_bwd_workspace_bytes() bytes, as above.
+ * Limits as above, and B*H*ceil(d/16) <= 2^21 for one token too.
  */
 ret_status retention_gated_scan_bwd(const void* x, const void* f, const float* rate, const float* state_in,
                                     const float* checkpoints, const void* grad_y, const float* grad_state_out,

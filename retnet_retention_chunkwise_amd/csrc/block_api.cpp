@@ -187,8 +187,9 @@ constexpr long long kMaxRuns = 1LL << 21;  // tiles of channels of a scan
 constexpr long long kMaxRows = 1LL << 28;  // rows of a norm
 constexpr int kMaxNormHeads = 65535;
 
-ret_status check_runs(const char* fn, int B, int H, int T, int d) {
-  if (T > 1 && static_cast<long long>(B) * H * ((d + 15LL) / 16) > kMaxRuns)
+// A forward call of one token has no runs: its kernel goes by the element.
+ret_status check_runs(const char* fn, int B, int H, int T, int d, bool backward) {
+  if (T > (backward ? 0 : 1) && static_cast<long long>(B) * H * ((d + 15LL) / 16) > kMaxRuns)
     return fail(RET_ERR_UNSUPPORTED, "%s: B*H*ceil(d/16) exceeds 2^21", fn);
   return RET_OK;
 }
@@ -263,7 +264,7 @@ extern "C" {
 
 size_t retention_gated_scan_workspace_bytes(int B, int H, int T, int d, ret_dtype dt) {
   if (check_sizes("retention_gated_scan_workspace_bytes", B, H, T, d, dt) != RET_OK) return kBad;
-  if (check_runs("retention_gated_scan_workspace_bytes", B, H, T, d) != RET_OK) return kBad;
+  if (check_runs("retention_gated_scan_workspace_bytes", B, H, T, d, false) != RET_OK) return kBad;
   return ret::gated_scan_chain_bytes(B, H, T, d);
 }
 
@@ -274,7 +275,7 @@ size_t retention_gated_scan_checkpoint_bytes(int B, int H, int T, int d) {
 
 size_t retention_gated_scan_bwd_workspace_bytes(int B, int H, int T, int d, ret_dtype dt, int have_checkpoints) {
   if (check_sizes("retention_gated_scan_bwd_workspace_bytes", B, H, T, d, dt) != RET_OK) return kBad;
-  if (check_runs("retention_gated_scan_bwd_workspace_bytes", B, H, T, d) != RET_OK) return kBad;
+  if (check_runs("retention_gated_scan_bwd_workspace_bytes", B, H, T, d, true) != RET_OK) return kBad;
   const size_t kept = have_checkpoints ? 0 : static_cast<size_t>(checkpoint_floats(B, H, T, d)) * 4;
   return own_offset(kept) + ret::gated_scan_chain_bytes(B, H, T, d);
 }
@@ -285,7 +286,7 @@ ret_status retention_gated_scan_fwd(const void* x, const void* f, const float* r
                                     size_t workspace_bytes, void* stream) {
   const char* fn = "retention_gated_scan_fwd";
   ret_status st = check_sizes(fn, B, H, T, d, dt);
-  if (st == RET_OK) st = check_runs(fn, B, H, T, d);
+  if (st == RET_OK) st = check_runs(fn, B, H, T, d, false);
   if (st == RET_OK) st = check_rates(fn, rate, H);
   if (st != RET_OK) return st;
   const Strides3 c = contiguous_bhtd(H, T, d);
@@ -316,7 +317,7 @@ ret_status retention_gated_scan_bwd(const void* x, const void* f, const float* r
                                     size_t workspace_bytes, void* stream) {
   const char* fn = "retention_gated_scan_bwd";
   ret_status st = check_sizes(fn, B, H, T, d, dt);
-  if (st == RET_OK) st = check_runs(fn, B, H, T, d);
+  if (st == RET_OK) st = check_runs(fn, B, H, T, d, true);
   if (st == RET_OK) st = check_rates(fn, rate, H);
   if (st != RET_OK) return st;
   const Strides3 c = contiguous_bhtd(H, T, d);
