@@ -317,8 +317,8 @@ typedef struct {
  *                 Calls that overlap in time need workspaces of their own.
  * T = 0 copies state_in (or zeros) to state_out.  Arithmetic, states and
  * checkpoints are fp32; y is rounded to dt.  Limits: T <= 2^30, every tensor's
- * element count below 2^31, B*H*ceil(d/16) <= 2^21 for T > 1.  Results do not depend on timing: the same call
- * gives the same bits.
+ * element count below 2^31, and for T > 1 at most 2^21 tiles of channels, B*H*ceil(d/w) with w = 64 for d > 32,
+ * 32 for d > 16, else 16.  Results do not depend on timing: the same call gives the same bits.
  */
 ret_status retention_gated_scan_fwd(const void* x, const void* f, const float* rate, const float* state_in,
                                     float* state_out, void* y, float* checkpoints, const ret_strides* strides,
@@ -347,7 +347,7 @@ size_t retention_gated_scan_checkpoint_bytes(int B, int H, int T, int d);
  *   grad_state_in  : nullable; written, fp32 [B,H,d]; may be grad_state_out exactly.
  *   strides        : x, f, grad_y, grad_x, grad_f.
  *   workspace      : retention_gated_scan_bwd_workspace_bytes() bytes, as above.
- * Limits as above, and B*H*ceil(d/16) <= 2^21 for one token too.
+ * Limits as above, that of the tiles for one token too.
  */
 ret_status retention_gated_scan_bwd(const void* x, const void* f, const float* rate, const float* state_in,
                                     const float* checkpoints, const void* grad_y, const float* grad_state_out,

@@ -189,8 +189,8 @@ constexpr int kMaxNormHeads = 65535;
 
 // A forward call of one token has no runs: its kernel goes by the element.
 ret_status check_runs(const char* fn, int B, int H, int T, int d, bool backward) {
-  if (T > (backward ? 0 : 1) && static_cast<long long>(B) * H * ((d + 15LL) / 16) > kMaxRuns)
-    return fail(RET_ERR_UNSUPPORTED, "%s: B*H*ceil(d/16) exceeds 2^21", fn);
+  if (T > (backward ? 0 : 1) && static_cast<long long>(B) * H * ret::gated_scan_tiles(d) > kMaxRuns)
+    return fail(RET_ERR_UNSUPPORTED, "%s: B*H*%d tiles of channels exceed 2^21", fn, ret::gated_scan_tiles(d));
   return RET_OK;
 }
 

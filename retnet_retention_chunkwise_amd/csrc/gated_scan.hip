@@ -1183,6 +1183,7 @@ hipError_t step_by_row(const GatedScanFwd& p, const HeadGroup& g, hipStream_t s)
 }  // namespace
 
 int gated_scan_block(int d) { return tile_tokens(d, kBlockElems); }
+int gated_scan_tiles(int d) { return static_cast<int>((d + static_cast<long>(tile_width(d)) - 1) / tile_width(d)); }
 
 size_t gated_scan_chain_bytes(int B, int H, int T, int d) {
   if (T <= 1 || !chained(B, H, T, d)) return 0;

@@ -188,6 +188,7 @@ struct GatedScanBwd {
   int dt;
 };
 int gated_scan_block(int d);  // tokens per checkpoint
+int gated_scan_tiles(int d);  // tiles of a row of d channels
 // Scratch of a launch that chains its tiles over workgroups (0: it needs none);
 // calls of more than kHeadsPerLaunch heads use it again for every head group.
 size_t gated_scan_chain_bytes(int B, int H, int T, int d);

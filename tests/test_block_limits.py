@@ -28,3 +28,18 @@ def test_backward_of_one_token_refuses_more_runs_than_a_launch_takes(B, H, d, wi
     assert "2^21" in _lib.last_error()
     # the forward of one token goes by the element
     assert lib.retention_gated_scan_workspace_bytes(B, H, 1, d, 0) == 0
+
+
+@pytest.mark.parametrize("B,H,d,most", [
+    (1 << 12, 32, 512, 1 << 20), (1 << 13, 32, 512, 1 << 21), (1 << 14, 64, 65, 1 << 21), (1 << 16, 32, 64, 1 << 21),
+    (1 << 16, 16, 48, 1 << 20), (1 << 15, 64, 32, 1 << 21), (1 << 16, 32, 16, 1 << 21), (1 << 21, 1, 3, 1 << 21)])
+def test_tiles_are_counted_as_wide_as_the_kernels_take_them(B, H, d, most):
+    """Rows of more than 32 channels are walked 64 channels at a time, of more than 16 32: at most 2^21 tiles."""
+    lib = _lib.load()
+    w = 64 if d > 32 else 32 if d > 16 else 16
+    assert B * H * -(-d // w) == most
+    for size in (lambda b: lib.retention_gated_scan_workspace_bytes(b, H, 2, d, 1),
+                 lambda b: lib.retention_gated_scan_bwd_workspace_bytes(b, H, 2, d, 1, 1)):
+        assert size(B) == 0  # so many runs are walked, without a workspace
+        if most == 1 << 21:
+            assert size(B + 1) == BAD and "2^21" in _lib.last_error()
