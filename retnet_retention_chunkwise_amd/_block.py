@@ -14,7 +14,7 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from ._lib import RET_BF16, RET_F32, RetentionError, _gamma_array, last_error, load
+from ._lib import RET_BF16, RET_F32, RetentionError, _gamma_array, _sizes, last_error, load
 
 _DT = {torch.float32: RET_F32, torch.bfloat16: RET_BF16}
 _BAD = ctypes.c_size_t(-1).value
@@ -114,6 +114,7 @@ def _out(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tens
 def _scan_inputs(x: torch.Tensor, f: torch.Tensor, dims: int):
     if x.dim() != dims:
         raise ValueError("expected x and f [B,H,T,d]" if dims == 4 else "expected x and f [B,H,d]")
+    _sizes(*x.shape)
     dt = _dtype(x)
     _rows(x, x.shape, x, "x")
     _rows(f, x.shape, x, "f")
@@ -122,7 +123,7 @@ def _scan_inputs(x: torch.Tensor, f: torch.Tensor, dims: int):
 
 def gated_scan_checkpoint_shape(B: int, H: int, T: int, d: int) -> Tuple[int, int, int, int]:
     """Shape of the fp32 checkpoints of a [B,H,T,d] call: the state before every block of tokens."""
-    n = int(load().retention_gated_scan_checkpoint_bytes(B, H, T, d))
+    n = int(load().retention_gated_scan_checkpoint_bytes(*_sizes(B, H, T, d)))
     if n == _BAD:
         raise RetentionError(1, last_error())
     return B, H, n // (4 * B * H * d), d
@@ -208,9 +209,9 @@ def gated_scan_step(x: torch.Tensor, f: torch.Tensor, rate, state: torch.Tensor,
 def _gate_norm_inputs(y, gate, weight, bias):
     if y.dim() != 4:
         raise ValueError("expected y [B,H,T,dv]")
+    B, H, T, dv = _sizes(*y.shape)
     dt = _dtype(y)
     _rows(y, y.shape, y, "y")
-    B, H, T, dv = y.shape
     token = (B, T, H, dv)
     if gate is not None:
         _rows(gate, token, y, "gate")
@@ -303,7 +304,7 @@ def _row_strides(**tensors):
 def _count(t: torch.Tensor) -> Tuple[int, int]:
     if t.dim() < 1 or t.shape[-1] < 1:
         raise ValueError("expected tensors [...,D] with D >= 1")
-    return t.numel() // t.shape[-1], t.shape[-1]
+    return _sizes(t.numel() // t.shape[-1], t.shape[-1])
 
 
 def residual_norm(x: torch.Tensor, f: torch.Tensor, weight: Optional[torch.Tensor] = None,

@@ -110,6 +110,13 @@ def _dt(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
 
 
+def _sizes(*n: int):
+    """Sizes as the C ABI takes them.  ctypes would pass the low 32 bits of a larger one."""
+    if max(n) > 0x7FFFFFFF or min(n) < -0x80000000:
+        raise ValueError(f"sizes must be below 2^31, got {tuple(n)}")
+    return n
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -158,7 +165,8 @@ def _qkv_shapes(q, k, v):
         raise ValueError("expected q, k [B,H,T,dk] and v [B,H,T,dv]")
     if not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k, v must share a dtype")
-    B, H, T, dk = q.shape
+    B, H, T, dk = _sizes(*q.shape)
+    _sizes(v.shape[-1])
     return B, H, T, dk, v.shape[-1], _dt(q)
 
 
@@ -177,6 +185,7 @@ def _qkv(q, k, v):
 
 def chunkwise_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int, C: int, dtype: torch.dtype) -> int:
     dt = RET_BF16 if dtype == torch.bfloat16 else RET_F32
+    _sizes(B, H, T, dk, dv, int(C))
     n = int(load().retention_chunkwise_workspace_bytes(B, H, T, dk, dv, C, dt))
     if n == ctypes.c_size_t(-1).value:
         raise RetentionError(RET_ERR_INVALID_ARG, "arguments rejected by retention_chunkwise_workspace_bytes")
@@ -197,6 +206,7 @@ def chunkwise_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma, C: i
     """
     lib = load()
     B, H, T, dk, dv, dt = _qkv_shapes(q, k, v)
+    _sizes(int(C))
     if y is not None:
         _out_check(y, (B, H, T, dv), q.dtype, q.device, "y")
     _qkv_devices(q, k, v)
@@ -240,6 +250,7 @@ def chunkwise_fwd_group_norm(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     check=True to wait for the call here and raise RuntimeError if it is set."""
     lib = load()
     B, H, T, dk, dv, dt = _qkv_shapes(q, k, v)
+    _sizes(int(C))
     if y is not None:
         _out_check(y, (B, H, T, dv), q.dtype, q.device, "y")
     _qkv_devices(q, k, v)
@@ -282,6 +293,7 @@ def fused_group_norm_failed(workspace: Optional[torch.Tensor], B: int, H: int, T
     Waits for the current stream (it reads the word back)."""
     lib = load()
     dt = RET_BF16 if dtype == torch.bfloat16 else RET_F32
+    _sizes(B, H, T, dk, dv, int(C))
     need = int(lib.retention_chunkwise_fwd_group_norm_workspace_bytes(B, H, T, dk, dv, int(C), dt))
     plain = int(lib.retention_chunkwise_workspace_bytes(B, H, T, dk, dv, int(C), dt))
     if workspace is None or need == plain or need == ctypes.c_size_t(-1).value:
@@ -305,6 +317,7 @@ def chunkwise_fwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gam
     Calls that overlap in time on one GPU race on that scratch.  Returns y."""
     lib = load()
     B, H, T, dk, dv, dt = _qkv_shapes(q, k, v)
+    _sizes(int(C))
     if y is not None:
         _out_check(y, (B, H, T, dv), q.dtype, q.device, "y")
     _qkv_devices(q, k, v)
@@ -334,6 +347,7 @@ def chunkwise_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma, C: i
     """
     lib = load()
     B, H, T, dk, dv, dt = _qkv(q, k, v)
+    _sizes(int(C))
     _dev(grad_y, "grad_y")
     if grad_y.shape != v.shape or grad_y.dtype != v.dtype or grad_y.device != v.device:
         raise ValueError("grad_y must match v in shape, dtype and device")
@@ -375,7 +389,7 @@ def group_norm(y: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     _dev(y, "y")
     if y.dim() != 4:
         raise ValueError("expected y [B,H,T,dv]")
-    B, H, T, dv = y.shape
+    B, H, T, dv = _sizes(*y.shape)
     dt = _dt(y)
     for t, n in ((weight, "weight"), (bias, "bias")):
         if t is not None:
@@ -417,8 +431,8 @@ def recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma, sta
     lib = load()
     if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[:2] != q.shape[:2]:
         raise ValueError("expected q, k [B,H,dk] and v [B,H,dv]")
-    B, H, dk = q.shape
-    dv = v.shape[-1]
+    B, H, dk = _sizes(*q.shape)
+    dv, = _sizes(v.shape[-1])
     dt = _dt(q)
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k, v must share a dtype")
