@@ -61,8 +61,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // t = e^-|f|.  log2(1+t) takes back the rounding of 1+t, and 1 - 2^z goes
 // through its Taylor series where 2^z is near 1, so c keeps its relative
 // precision down to the smallest decays.  f = -inf gives c = 1 and f = +inf
-// gives c = 0 exactly.  *t_out: t.
-__device__ __forceinline__ float decay_complement(float f, float rate, float* t_out) {
+// gives c = 0 exactly.  *t_out: t; *a_out: a = 2^z, which keeps its own digits
+// where c is rounded next to 1.
+__device__ __forceinline__ float decay_complement(float f, float rate, float* t_out, float* a_out) {
   const float af = fabsf(f);
   const float p = af * kLog2e;
   float t = __builtin_amdgcn_exp2f(-p);
@@ -76,9 +77,10 @@ __device__ __forceinline__ float decay_complement(float f, float rate, float* t_
   s = fmaf(z, s, 1.0f / 6.0f);
   s = fmaf(z, s, 0.5f);
   s = fmaf(z, s, 1.0f);
-  const float e = 1.0f - __builtin_amdgcn_exp2f(z2);
+  const float a = __builtin_amdgcn_exp2f(z2);
   *t_out = t;
-  return z > -0.25f ? -z * s : e;
+  *a_out = a;
+  return z > -0.25f ? -z * s : 1.0f - a;
 }
 
 // sigmoid(-f) from t = e^-|f|
@@ -116,13 +118,13 @@ __device__ __forceinline__ float gate_of_index(int i) {
 
 // One gate: c = 1 - a and, for the backward, k = rate a sigmoid(-f).
 __device__ __forceinline__ void gate_value(float f, float rate, float* out) {
-  float t;
-  *out = decay_complement(f, rate, &t);
+  float t, a;
+  *out = decay_complement(f, rate, &t, &a);
 }
 __device__ __forceinline__ void gate_value(float f, float rate, float2* out) {
-  float t;
-  const float c = decay_complement(f, rate, &t);
-  *out = make_float2(c, rate * (1.0f - c) * sigmoid_neg(f, t));
+  float t, a;
+  const float c = decay_complement(f, rate, &t, &a);
+  *out = make_float2(c, rate * a * sigmoid_neg(f, t));
 }
 
 template <typename Entry>
@@ -1010,8 +1012,8 @@ __global__ __launch_bounds__(256) void gated_scan_step_kernel(GatedScanFwd p, He
     for (int e = 0; e < VEC; ++e) p.checkpoints[row + e] = st[e];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    float t;
-    const float m = decay_complement(f[e], rates.r[hl], &t);
+    float t, a;
+    const float m = decay_complement(f[e], rates.r[hl], &t, &a);
     st[e] = kNorm ? fmaf(m, x[e] - st[e], st[e]) : fmaf(-m, st[e], st[e]) + x[e];
   }
   if (p.state_out != nullptr) VecIO<float, VEC>::store(p.state_out + row, st);
