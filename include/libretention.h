@@ -300,9 +300,12 @@ typedef struct {
  *   u_t = x_t (normalize = 0)  or  u_t = (1 - a_t) x_t (normalize = 1),
  * h_(-1) = state_in.  rate_h > 0 plays the part of retention's per-head decay:
  * a small one gives its head a long memory.  f_t = -inf gives a_t = 0 (the
- * token starts a new packed sequence), f_t = +inf gives a_t = 1; e^-|f| below
- * 2^-126 (|f| > 87.3) counts as 0.  After a NaN, or an infinity in x or in the
- * state, the later values of that channel are not finite; others are untouched.
+ * token starts a new packed sequence), f_t = +inf gives a_t = 1.  a_t below 1/2
+ * and 1 - a_t above it are held to their own relative precision, so long
+ * memories decay as they should and a forgotten past leaves no rounding behind
+ * (a_t = 0: y_t is x_t exactly).  e^-|f| (|f| > 87.3) or a_t below 2^-126 counts
+ * as 0.  After a NaN, or an infinity in x or in the state, the later values of
+ * that channel are not finite; others are untouched.
  *   x, f        : [B,H,T,d] in dt.
  *   rate        : HOST array of H floats, finite and > 0.
  *   state_in    : nullable (zeros); fp32 [B,H,d].

@@ -3,10 +3,17 @@
 // exponent rate > 0:
 //   a_t = sigmoid(f_t)^rate,  h_t = a_t h_(t-1) + u_t,  y_t = h_t,
 //   u_t = x_t, or u_t = (1 - a_t) x_t (normalize).
-// The recurrence is carried with c_t = 1 - a_t instead of a_t:
+// Where a_t >= 1/2 the recurrence is carried with c_t = 1 - a_t instead of a_t:
 //   h_t = h_(t-1) - c_t h_(t-1) + x_t,   normalize: h_t = h_(t-1) + c_t (x_t - h_(t-1)),
 // because a decay near 1 loses its distance to 1 when it is rounded (a memory
-// of n tokens would see n times that error), while c_t has 24 good bits.
+// of n tokens would see n times that error), while c_t has 24 good bits.  Below
+// 1/2 it is the other way round, c_t would lose a_t, and
+//   h_t = a_t h_(t-1) + x_t,   normalize: h_t = x_t + a_t (h_(t-1) - x_t),
+// so that what is forgotten leaves no rounding behind (a_t = 0: h_t = u_t).  A
+// decay is held in one number m_t that says which it is: c_t, or -a_t.  Choosing
+// by its sign costs where the vector unit is what bounds: B1 H8 T32768 d512
+// bf16, forward and backward, 520 us in place of 496 (two versions of every
+// product and a branch by the wave's signs: 529).
 //
 // A tile is CW channels by TT tokens.  Lanes run along channels (VEC per lane,
 // one access of up to 16 bytes) and then along time, so a wave reads whole
@@ -55,32 +62,44 @@ struct HeadRate {
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr double kLn2 = 0.69314718055994531;
 
-// c = 1 - sigmoid(f)^rate in fp32 from log2 sigmoid(f) = -(max(-f,0) log2e + log2(1+t)),
-// t = e^-|f|.  log2(1+t) takes back the rounding of 1+t, and 1 - 2^z goes
-// through its Taylor series where 2^z is near 1, so c keeps its relative
-// precision down to the smallest decays.  f = -inf gives c = 1 and f = +inf
-// gives c = 0 exactly.  *t_out: t; *a_out: a = 2^z, which keeps its own digits
-// where c is rounded next to 1.
-__device__ __forceinline__ float decay_complement(float f, float rate, float* t_out, float* a_out) {
-  const float af = fabsf(f);
-  const float p = af * kLog2e;
-  float t = __builtin_amdgcn_exp2f(-p);
+// a = sigmoid(f)^rate in fp32, as held (*a_out: as it is), from
+// z2 = rate log2 sigmoid(f) = -rate (max(-f,0) log2e + log2(1+t)), t = e^-|f|
+// (*t_out).  log2(1+t) takes back the rounding of 1+t, and c = 1 - 2^z2 goes
+// through its Taylor series where 2^z2 is near 1, so c keeps its relative
+// precision down to the smallest decays.  f = -inf gives a = 0 and f = +inf
+// gives c = 0 exactly.
+__device__ __forceinline__ float held_decay(float f, float rate, float* t_out, float* a_out) {
+  const float p = fabsf(f) * kLog2e;
+  const float t = __builtin_amdgcn_exp2f(-p);
   const float w = 1.0f + t;
   const float l = fmaf(t - (w - 1.0f), kLog2e, __builtin_amdgcn_logf(w));
-  const float z2 = -rate * fmaf(fmaxf(-f, 0.0f), kLog2e, l);
-  const float z = z2 * kLn2;
-  // relative error below -0.25: 2^-25 / 0.22; above it the series ends at z^6/5040 < 2^-24
-  float s = fmaf(z, 1.0f / 720.0f, 1.0f / 120.0f);
-  s = fmaf(z, s, 1.0f / 24.0f);
-  s = fmaf(z, s, 1.0f / 6.0f);
-  s = fmaf(z, s, 0.5f);
-  s = fmaf(z, s, 1.0f);
+  const float z2 = -rate * fmaf(__builtin_amdgcn_fmed3f(-f, 0.0f, __builtin_inff()), kLog2e, l);
+  // relative error below -0.36: 2^-25 / 0.22; above it the series ends at (z2 ln2)^6/5040 < 2^-24
+  constexpr double k2 = kLn2 * kLn2 / 2, k3 = k2 * kLn2 / 3, k4 = k3 * kLn2 / 4, k5 = k4 * kLn2 / 5, k6 = k5 * kLn2 / 6;
+  float s = fmaf(z2, static_cast<float>(k6), static_cast<float>(k5));
+  s = fmaf(z2, s, static_cast<float>(k4));
+  s = fmaf(z2, s, static_cast<float>(k3));
+  s = fmaf(z2, s, static_cast<float>(k2));
+  s = fmaf(z2, s, static_cast<float>(kLn2));
   const float a = __builtin_amdgcn_exp2f(z2);
   *t_out = t;
   *a_out = a;
-  return z > -0.25f ? -z * s : 1.0f - a;
+  // fabs: c is never -0 and never below 0, which a rounding of l could else make it
+  return z2 > -0.36f ? fabsf(z2 * s) : a < 0.5f ? -a : 1.0f - a;
+}
+
+// Whether a held decay is -a (-0 for a = 0) and not c >= 0.
+__device__ __forceinline__ bool holds_a(float m) { return __float_as_int(m) < 0; }
+// a h
+__device__ __forceinline__ float decayed(float m, float h) { return fmaf(-m, h, holds_a(m) ? 0.0f : h); }
+// (1 - a) h
+__device__ __forceinline__ float complement(float m, float h) { return fmaf(m, h, holds_a(m) ? h : 0.0f); }
+// a h + u
+template <bool kNorm>
+__device__ __forceinline__ float decay_step(float m, float x, float h) {
+  return kNorm ? fmaf(m, x - h, holds_a(m) ? x : h) : decayed(m, h) + x;
 }
 
 // sigmoid(-f) from t = e^-|f|
@@ -96,9 +115,10 @@ __device__ __forceinline__ float sigmoid_neg(float f, float t) {
 // instructions and an LDS read per element in place of about 35 (three of them
 // at a quarter of the rate), which bounded the kernel.  The entry of a value v
 // is at rotate_left(bits(v), 1), so that both signs of a magnitude lie side by
-// side.  Magnitudes below 2^-24 take the entry of 2^-24 (c moves by less than
-// 2^-24 of itself); a thread that meets 128 or more, an infinity or a NaN
-// evaluates its tokens directly.
+// side.  Magnitudes below 2^-24, of either sign, take the entry of +2^-24: f is
+// off by less than 2^-23 there, c by 1.45 x 2^-24 of itself, a by rate 2^-24.
+// A wave that meets 128 or more, an infinity or a NaN evaluates its tokens
+// directly.
 constexpr int kGateLow = 103 << 7, kGateHigh = 134 << 7;  // bf16 bits of 2^-24 and of 128
 constexpr int kGateN = 2 * (kGateHigh - kGateLow);
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -116,15 +136,15 @@ __device__ __forceinline__ float gate_of_index(int i) {
   return bf16_to_f32(static_cast<uint16_t>((kGateLow + (i >> 1)) | ((i & 1) << 15)));
 }
 
-// One gate: c = 1 - a and, for the backward, k = rate a sigmoid(-f).
+// One gate: a as held and, for the backward, k = rate a sigmoid(-f).
 __device__ __forceinline__ void gate_value(float f, float rate, float* out) {
   float t, a;
-  *out = decay_complement(f, rate, &t, &a);
+  *out = held_decay(f, rate, &t, &a);
 }
 __device__ __forceinline__ void gate_value(float f, float rate, float2* out) {
   float t, a;
-  const float c = decay_complement(f, rate, &t, &a);
-  *out = make_float2(c, rate * a * sigmoid_neg(f, t));
+  const float m = held_decay(f, rate, &t, &a);
+  *out = make_float2(m, rate * a * sigmoid_neg(f, t));
 }
 
 template <typename Entry>
@@ -468,19 +488,19 @@ struct FwdThread {
       for (int e = 0; e < VEC; ++e)
         if (t0 + s >= T) cm[s][e] = x[s][e] = 0.0f;
   }
-  __device__ __forceinline__ static float step(float c, float x, float h) {
-    return kNorm ? fmaf(c, x - h, h) : fmaf(-c, h, h) + x;
-  }
-  // the map of the thread's tokens
-  __device__ __forceinline__ void map(float (&A)[VEC], float (&H)[VEC]) const {
+  __device__ __forceinline__ static float step(float m, float x, float h) { return decay_step<kNorm>(m, x, h); }
+  // The map of the thread's tokens; cm and x become the maps up to each of
+  // them, which give the tokens' values in one operation.
+  __device__ __forceinline__ void map(float (&A)[VEC], float (&H)[VEC]) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       A[e] = 1.0f;
       H[e] = 0.0f;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        A[e] = fmaf(-cm[s][e], A[e], A[e]);
-        H[e] = step(cm[s][e], x[s][e], H[e]);
+        const float m = cm[s][e];
+        cm[s][e] = A[e] = decayed(m, A[e]);
+        x[s][e] = H[e] = step(m, x[s][e], H[e]);
       }
     }
   }
@@ -505,7 +525,7 @@ struct FwdThread {
       if (!whole && t0 + s >= T) continue;  // tokens past the end leave the state as it is
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        A[e] = fmaf(-c[0][e], A[e], A[e]);
+        A[e] = decayed(c[0][e], A[e]);
         H[e] = step(c[0][e], u[e], H[e]);
       }
     }
@@ -513,6 +533,7 @@ struct FwdThread {
   template <bool kTable>
   __device__ __forceinline__ void packed_replay(int chunk, const float* table, float (&h)[VEC]) {
     const int t0 = chunk * P::TT + seg * S;
+    E* py = yp + min(t0, T - 1) * sy;
     if constexpr (kTable) {
       // the compiler would otherwise keep the map's gates in registers, twice as many as the packed ones
 #pragma unroll
@@ -527,7 +548,8 @@ struct FwdThread {
       if (t0 + s >= T) continue;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) h[e] = step(c[0][e], u[e], h[e]);
-      if (store) cols.template store<E>(yp + (t0 + s) * sy, h);
+      if (store) cols.template store<E>(py, h);
+      py += sy;
     }
   }
   template <bool kTable>
@@ -541,15 +563,17 @@ struct FwdThread {
     }
     IO::unpack(rx[s], u);
   }
-  // a thread's tokens (c, u) from their incoming value
-  __device__ __forceinline__ void replay(int chunk, const float (&c)[S][VEC], const float (&u)[S][VEC],
-                                         float (&h)[VEC]) const {
+  // the thread's tokens from their incoming value, by the maps that map() left
+  __device__ __forceinline__ void replay(int chunk, const float (&in)[VEC]) const {
     const int t0 = chunk * P::TT + seg * S;
+    E* py = yp + min(t0, T - 1) * sy;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
+      float h[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) h[e] = step(c[s][e], u[s][e], h[e]);
-      if (store && t0 + s < T) cols.template store<E>(yp + (t0 + s) * sy, h);
+      for (int e = 0; e < VEC; ++e) h[e] = fmaf(cm[s][e], in[e], x[s][e]);
+      if (store && t0 + s < T) cols.template store<E>(py, h);
+      py += sy;
     }
   }
 };
@@ -611,7 +635,7 @@ __global__ __launch_bounds__(64 * NW) void gated_scan_fwd_walk_kernel(GatedScanF
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
       h[e] = fmaf(th.cols.get(segA[pl.seg], e), th.cols.get(waveH[q][pl.wave], e), th.cols.get(segH[pl.seg], e));
-    th.replay(chunk, th.cm, th.x, h);
+    th.replay(chunk, h);
   }
   if (kept && p.state_out != nullptr) p.state_out[bh * p.d + ch] = carry;
 }
@@ -738,12 +762,17 @@ struct BwdThread {
     store = pc.in;
   }
   __device__ __forceinline__ void load(int chunk) {
+    // one product of token and stride for the rows: products take a quarter of the rate
+    const int t0 = chunk * P::TT + seg * S;
+    const E* px = xp + min(t0, T - 1) * sx;
+    const E* pf = fp + min(t0, T - 1) * sf;
+    const E* pg = gyp + min(t0, T - 1) * sgy;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const long t = min(chunk * P::TT + seg * S + s, T - 1);
-      rx[s] = IO::load(xp + t * sx);
-      rf[s] = IO::load(fp + t * sf);
-      rg[s] = IO::load(gyp + t * sgy);
+      const bool on = t0 + s < T;  // else another token that exists, masked below
+      rx[s] = IO::load(px + (on ? s * sx : 0));
+      rf[s] = IO::load(pf + (on ? s * sf : 0));
+      rg[s] = IO::load(pg + (on ? s * sgy : 0));
     }
   }
   template <bool kTable>
@@ -768,19 +797,16 @@ struct BwdThread {
       for (int e = 0; e < VEC; ++e)
         if (t0 + s >= T) cm[s][e] = x[s][e] = dy[s][e] = 0.0f;
   }
-  // the maps of the thread's tokens: h -> A h + H forwards, G -> A G + R backwards
+  // the maps of the thread's tokens: h -> A h + H forwards, G -> A G + R
+  // backwards, where every token's dy has passed the decays up to its own
   __device__ __forceinline__ void map(int e, float& A, float& H, float& R) const {
     A = 1.0f;
     H = R = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      A = fmaf(-cm[s][e], A, A);
-      H = FwdThread<E, VEC, CW, NW, kPerThread, kNorm, kWhole>::step(cm[s][e], x[s][e], H);
-    }
-#pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-      const float g = dy[s][e] + R;
-      R = fmaf(-cm[s][e], g, g);
+      A = decayed(cm[s][e], A);
+      R = fmaf(A, dy[s][e], R);
+      H = decay_step<kNorm>(cm[s][e], x[s][e], H);
     }
   }
   // replays the tokens of element e forwards from h: kf becomes dy_t -> df_t, a_t h'_t with h'_t = dh_t / da_t
@@ -788,7 +814,7 @@ struct BwdThread {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       kf[s][e] *= kNorm ? h - x[s][e] : h;
-      h = FwdThread<E, VEC, CW, NW, kPerThread, kNorm, kWhole>::step(cm[s][e], x[s][e], h);
+      h = decay_step<kNorm>(cm[s][e], x[s][e], h);
     }
   }
   // and backwards from G behind them: g becomes dx, k becomes df
@@ -797,19 +823,24 @@ struct BwdThread {
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
       const float gs = g[s][e] + G;
-      G = fmaf(-c[s][e], gs, gs);
-      g[s][e] = kNorm ? gs * c[s][e] : gs;
+      G = decayed(c[s][e], gs);
+      g[s][e] = kNorm ? complement(c[s][e], gs) : gs;
       k[s][e] *= gs;
     }
   }
   __device__ __forceinline__ void write(int chunk, const float (&dx)[S][VEC], const float (&df)[S][VEC]) const {
     const int t0 = chunk * P::TT + seg * S;
+    E* px = gxp + min(t0, T - 1) * sgx;
+    E* pf = gfp + min(t0, T - 1) * sgf;
 #pragma unroll
-    for (int s = 0; s < S; ++s)
+    for (int s = 0; s < S; ++s) {
       if (store && t0 + s < T) {
-        cols.template store<E>(gxp + (t0 + s) * sgx, dx[s]);
-        cols.template store<E>(gfp + (t0 + s) * sgf, df[s]);
+        cols.template store<E>(px, dx[s]);
+        cols.template store<E>(pf, df[s]);
       }
+      px += sgx;
+      pf += sgf;
+    }
   }
 };
 
@@ -1013,8 +1044,7 @@ __global__ __launch_bounds__(256) void gated_scan_step_kernel(GatedScanFwd p, He
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
     float t, a;
-    const float m = decay_complement(f[e], rates.r[hl], &t, &a);
-    st[e] = kNorm ? fmaf(m, x[e] - st[e], st[e]) : fmaf(-m, st[e], st[e]) + x[e];
+    st[e] = decay_step<kNorm>(held_decay(f[e], rates.r[hl], &t, &a), x[e], st[e]);
   }
   if (p.state_out != nullptr) VecIO<float, VEC>::store(p.state_out + row, st);
   if (p.y != nullptr) IO::store(static_cast<E*>(p.y) + b * p.sy.b + h * p.sy.h + c, st);
