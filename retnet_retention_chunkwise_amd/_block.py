@@ -14,7 +14,7 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from ._lib import RET_BF16, RET_F32, RetentionError, _gamma_array, _sizes, last_error, load
+from ._lib import RET_BF16, RET_F32, RetentionError, _gamma_array, _shape, _sizes, last_error, load
 
 _DT = {torch.float32: RET_F32, torch.bfloat16: RET_BF16}
 _BAD = ctypes.c_size_t(-1).value
@@ -114,7 +114,8 @@ def _out(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tens
 def _scan_inputs(x: torch.Tensor, f: torch.Tensor, dims: int):
     if x.dim() != dims:
         raise ValueError("expected x and f [B,H,T,d]" if dims == 4 else "expected x and f [B,H,d]")
-    _sizes(*x.shape)
+    if not 0 < x.numel() <= 0x7FFFFFFF:
+        _sizes(*x.shape)
     dt = _dtype(x)
     _rows(x, x.shape, x, "x")
     _rows(f, x.shape, x, "f")
@@ -209,7 +210,7 @@ def gated_scan_step(x: torch.Tensor, f: torch.Tensor, rate, state: torch.Tensor,
 def _gate_norm_inputs(y, gate, weight, bias):
     if y.dim() != 4:
         raise ValueError("expected y [B,H,T,dv]")
-    B, H, T, dv = _sizes(*y.shape)
+    B, H, T, dv = _shape(y)
     dt = _dtype(y)
     _rows(y, y.shape, y, "y")
     token = (B, T, H, dv)
@@ -304,7 +305,8 @@ def _row_strides(**tensors):
 def _count(t: torch.Tensor) -> Tuple[int, int]:
     if t.dim() < 1 or t.shape[-1] < 1:
         raise ValueError("expected tensors [...,D] with D >= 1")
-    return _sizes(t.numel() // t.shape[-1], t.shape[-1])
+    n, D = t.numel(), t.shape[-1]
+    return (n // D, D) if n <= 0x7FFFFFFF else _sizes(n // D, D)
 
 
 def residual_norm(x: torch.Tensor, f: torch.Tensor, weight: Optional[torch.Tensor] = None,

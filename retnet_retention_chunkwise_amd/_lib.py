@@ -117,6 +117,12 @@ def _sizes(*n: int):
     return n
 
 
+def _shape(t: torch.Tensor):
+    """t.shape as the C ABI takes it; the element count tells most tensors fit, and is quicker."""
+    n = t.numel()
+    return t.shape if 0 < n <= 0x7FFFFFFF else _sizes(*t.shape)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -165,9 +171,8 @@ def _qkv_shapes(q, k, v):
         raise ValueError("expected q, k [B,H,T,dk] and v [B,H,T,dv]")
     if not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k, v must share a dtype")
-    B, H, T, dk = _sizes(*q.shape)
-    _sizes(v.shape[-1])
-    return B, H, T, dk, v.shape[-1], _dt(q)
+    B, H, T, dk = _shape(q)
+    return B, H, T, dk, _shape(v)[-1], _dt(q)
 
 
 def _qkv_devices(q, k, v):
@@ -389,7 +394,7 @@ def group_norm(y: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     _dev(y, "y")
     if y.dim() != 4:
         raise ValueError("expected y [B,H,T,dv]")
-    B, H, T, dv = _sizes(*y.shape)
+    B, H, T, dv = _shape(y)
     dt = _dt(y)
     for t, n in ((weight, "weight"), (bias, "bias")):
         if t is not None:
@@ -431,8 +436,8 @@ def recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma, sta
     lib = load()
     if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[:2] != q.shape[:2]:
         raise ValueError("expected q, k [B,H,dk] and v [B,H,dv]")
-    B, H, dk = _sizes(*q.shape)
-    dv, = _sizes(v.shape[-1])
+    B, H, dk = _shape(q)
+    dv = _shape(v)[-1]
     dt = _dt(q)
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k, v must share a dtype")
