@@ -321,8 +321,9 @@ ret_status retention_gated_scan_bwd(const void* x, const void* f, const float* r
   if (st == RET_OK) st = check_rates(fn, rate, H);
   if (st != RET_OK) return st;
   const Strides3 c = contiguous_bhtd(H, T, d);
-  const Strides3 sx = given(strides, 0, c), sf = given(strides, 1, c), sgy = given(strides, 2, c),
-                 sgx = given(strides, 3, c), sgf = given(strides, 4, c);
+  Strides3 sx = given(strides, 0, c), sf = given(strides, 1, c), sgy = given(strides, 2, c),
+           sgx = given(strides, 3, c), sgf = given(strides, 4, c);
+  if (T == 1) sx.t = sf.t = sgy.t = sgx.t = sgf.t = d;  // not followed, but multiplied
   const long long ns = static_cast<long long>(B) * H * d;
   const size_t need = retention_gated_scan_bwd_workspace_bytes(B, H, T, d, dt, checkpoints != nullptr);
   st = check_args(fn,

@@ -24,3 +24,22 @@ def test_many_runs(B, H, T, d, dtype):
     x, f, dy, s, ds = (v[pick].cpu() for v in (x, f, dy, s, ds))
     check_forward(f"many runs {B}", x, f, rate, s, True, y[pick], last[pick])
     check_backward(f"many runs {B}", x, f, rate, dy, s, ds, True, [v[pick] for v in got])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_one_token_has_no_stride_to_follow(dtype):
+    """A dimension of one may have any stride; the backward of one token multiplies none of them."""
+    B, H, d = 3, 2, 36
+    g = torch.Generator().manual_seed(77)
+    x, f, dy = (torch.randn(B, H, 1, d, generator=g).to(dtype) for _ in range(3))
+    s, ds = torch.randn(B, H, d, generator=g), torch.randn(B, H, d, generator=g)
+
+    def far(t):
+        wide = torch.nn.functional.pad(t, (0, 4)).to(DEV)
+        return wide.as_strided((B, H, 1, d), (H * (d + 4), d + 4, 2 ** 61, 1))
+
+    out = lambda: far(torch.full((B, H, 1, d), float("nan"), dtype=dtype))  # noqa: E731
+    got = ret.gated_scan_bwd(far(x), far(f), rates(H), far(dy), s.to(DEV), ds.to(DEV), None, True, grad_x=out(), grad_f=out())
+    want = ret.gated_scan_bwd(*(t.to(DEV) for t in (x, f)), rates(H), dy.to(DEV), s.to(DEV), ds.to(DEV), None, True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    check_backward("one token", x, f, rates(H), dy, s, ds, True, got)
