@@ -23,9 +23,10 @@
 // (within a wave, then over the waves), and every thread replays its tokens
 // from its incoming value.  x and f are read once and y is written once.
 // Measured, bf16:
-// B4 H8 T2048 d512 forward 41 us (4.9 TB/s), B2 H16 T8192 d512 forward 160 us
-// and backward 284 us (5.0 and 4.7 TB/s), B1 H8 T65536 d512 forward 333 us with
-// the workspace's fill (4.8 TB/s).
+// B4 H8 T2048 d512 forward 40 us (5.0 TB/s), B2 H16 T8192 d512 forward and
+// backward 432 to 445 us (4.9 TB/s), B1 H8 T65536 d512 forward 334 to 340 us with
+// the workspace's fill (4.8 TB/s): the means of passes one after the other;
+// single launches vary more, by up to a fifth.
 #include "common.h"
 #include "gfx950.h"
 #include "kernels.h"
@@ -44,15 +45,17 @@ constexpr int kBlockElems = 128;  // a checkpoint's block: as many elements per 
 // than kWalkTiles and have kChainSteps blocks of tokens or more; else one
 // workgroup walks each run.  Measured in us, walking / chaining, d 64, bf16
 // forward (and backward), runs x tokens:
-//     32 x 512   13 / 17 (16 / 20)      32 x 1024    17 / 17 (27 / 20)
-//     32 x 4096  59 / 24 (101 / 34)    128 x 4096    62 / 53 (109 / 93)
-//    192 x 4096  68 / 74 (118 / 131)   256 x 16384  286 / 318 (504 / 668)
-// and in fp32 128 x 4096 83 / 76 (140 / 118), 256 x 4096 140 / 144 (199 / 229).
+//     32 x 512   13 / 17 (17 / 20)      32 x 1024    16 / 17 (24 / 21)
+//     32 x 4096  51 / 25 (85 / 32)     128 x 4096    55 / 54 (92 / 88)
+//    192 x 4096  63 / 74 (107 / 130)   256 x 16384  284 / 314 (456 / 639)
+//    384 x 4096 124 / 129 (194 / 241)  512 x 4096   145 / 171 (233 / 322)
+// and in fp32 128 x 4096 83 / 77 (137 / 117), 256 x 4096 139 / 147 (202 / 230),
+// 384 x 4096 214 / 218 (329 / 342).
 constexpr int kWalkTiles = 160, kChainSteps = 8;
 constexpr int kTableTiles = 4;  // tiles of a workgroup from which on its gate table pays
 // A workgroup that walks a run uses a table, and 16 waves, where the run is
 // longer than so many blocks of tokens.  With / without, us, 1280 runs of d 64:
-//   T 128   28 / 17 (backward 40 / 31)    T 256   32 / 29 (45 / 53)    T 512   52 / 54 (76 / 104)
+//   T 128   29 / 17 (backward 41 / 31)    T 256   32 / 30 (46 / 53)    T 512   51 / 53 (78 / 105)
 constexpr int kTableStepsFwd = 2, kTableStepsBwd = 1;
 
 typedef unsigned long long u64;

@@ -286,7 +286,8 @@ hipError_t launch_gate_norm_fwd(const GateNormFwd& a, hipStream_t s) {
 
 int gate_norm_bwd_slabs(int B, int H, int T, int dv) {
   const long groups = static_cast<long>(B) * T;  // rows of one head
-  const long per = kThreads / lanes_for(dv);     // rows in a workgroup at once (twice that with 4 lanes)
+  // rows in a workgroup at once (twice that with 4 lanes to a row: of short narrow heads half then get no row)
+  const long per = kThreads / lanes_for(dv);
   const long most = (groups + per - 1) / per;
   const long want = (1024 + H - 1) / H;  // about four workgroups on each of 256 compute units
   return static_cast<int>(want < most ? want : most);
