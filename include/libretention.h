@@ -445,6 +445,119 @@ ret_status retention_residual_norm_bwd(const void* r, const void* grad_n, const 
                                        ret_dtype dt, void* workspace, size_t workspace_bytes, void* stream);
 size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D);
 
+/*
+ * ---- Softmax attention beside retention in a hybrid stack ----
+ *
+ * An exact memory where retention keeps a summary, in the same three forms:
+ * whole sequence, gradients, one token in place on the memory (a paged cache).
+ * Per batch b and query head h (H a multiple of Hk; query head h reads key and
+ * value head h / (H / Hk)), one map or two:
+ *   A_m[t,s] = softmax over the visible s of scale q_m[t] . k_m[s],
+ *   o[t] = sum_s A_1[t,s] v[s]                        (lam NULL: one map)
+ *   o[t] = sum_s (A_1[t,s] - lam_h A_2[t,s]) v[s]     (differential attention)
+ * The two maps take the two halves of the dk channels of a row of q and k.
+ * Strides are those of ret_strides.  scale is finite and > 0 (1 / sqrt of a
+ * map's channels is usual).  Products are of the tensors' type (bf16 or fp32
+ * MFMA) with fp32 accumulators; scores, softmax statistics and sums are fp32;
+ * probabilities are rounded to the tensors' type before they meet the values;
+ * outputs are rounded once.  lam and its gradient are fp32 [H]; lam, lse and
+ * int arrays need the alignment of their elements only.
+ * Limits: dk, dv <= 256; every tensor (a cache aside) below 2^31 elements,
+ * B*H*T <= 2^25, T and S <= 2^30, B*H*ceil(T/64) and B*Hk*ceil(S/64) <= 2^23.
+ * No sum depends on timing: the same call gives the same bits.
+ */
+
+/*
+ * A whole sequence.  Row t sees the keys s < lens[b] (lens NULL: S) and, when
+ * causal, s <= t + offset (offset S - T aligns the last row with the last key).
+ * A row that sees no key is 0, and its lse -inf.  Keys and values from lens[b]
+ * on are not used, whatever they hold.
+ *   q [B,H,T,dk], k [B,Hk,S,dk], v [B,Hk,S,dv] in dt.
+ *   lam     : nullable; device fp32 [H].    lens : nullable; device int [B], taken into 0..S.
+ *   o       : written, [B,H,T,dv] in dt.
+ *   lse     : nullable; written, contiguous fp32 [B,H,maps,T], the log of the
+ *             sum of exp(score) of every row and map (maps = 1, or 2 with lam).
+ *   second  : nullable; written, contiguous [B,H,T,dv] in dt, sum_s A_2 v (lam
+ *             only).  lse and second are what the backward needs.
+ *   strides : q, k, v, o.
+ *   workspace : retention_attention_workspace_bytes() bytes (may be NULL when
+ *             that is 0), 16-byte aligned, owned by the caller, overlapping no
+ *             other argument; contents ignored on entry.  Calls that overlap in
+ *             time need workspaces of their own.
+ * Inputs that are not finite reach the rows that see them as the formula says;
+ * a value row that is not finite may also reach rows before it.
+ */
+ret_status retention_attention_fwd(const void* q, const void* k, const void* v, const float* lam, const int* lens,
+                                   void* o, float* lse, void* second, const ret_strides* strides, int B, int H, int Hk,
+                                   int T, int S, int dk, int dv, float scale, int causal, int offset, ret_dtype dt,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+/* Functions of the sizes alone ((size_t)-1 for arguments the calls would reject). */
+size_t retention_attention_workspace_bytes(int B, int H, int Hk, int T, int S, int dk, int dv, int maps, ret_dtype dt);
+
+/*
+ * Gradients of retention_attention_fwd for L = sum <grad_o, o>.
+ *   q, k, v, lam, lens, scale, causal, offset, sizes : the forward call's.
+ *   o, lse, second : what it wrote (second NULL with one map).
+ *   grad_o  : [B,H,T,dv] in dt.
+ *   grad_q [B,H,T,dk], grad_k [B,Hk,S,dk], grad_v [B,Hk,S,dv] : written in dt,
+ *             summed over the query heads that share a key head; 0 for rows that
+ *             see no key and for keys and values from lens[b] on.
+ *   grad_lam : written, fp32 [H]; NULL exactly when lam is NULL.
+ *   strides : q, k, v, o, grad_o, grad_q, grad_k, grad_v.
+ *   workspace : retention_attention_bwd_workspace_bytes() bytes, as above.
+ */
+ret_status retention_attention_bwd(const void* q, const void* k, const void* v, const float* lam, const int* lens,
+                                   const void* o, const float* lse, const void* second, const void* grad_o,
+                                   void* grad_q, void* grad_k, void* grad_v, float* grad_lam,
+                                   const ret_strides* strides, int B, int H, int Hk, int T, int S, int dk, int dv,
+                                   float scale, int causal, int offset, ret_dtype dt, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+size_t retention_attention_bwd_workspace_bytes(int B, int H, int Hk, int T, int S, int dk, int dv, int maps,
+                                               ret_dtype dt);
+
+/*
+ * One new token of every sequence, in place on a paged cache: its k and v are
+ * stored as token lens[b] of sequence b, and its q sees the lens[b] tokens before
+ * it and itself.
+ *   q [B,H,dk], k [B,Hk,dk], v [B,Hk,dv] in dt.     o : written, [B,H,dv] in dt.
+ *   k_cache, v_cache : in/out, [pages,Hk,page,dk] and [pages,Hk,page,dv] in dt
+ *             (any strides between pages, heads and tokens); any element count.
+ *   table   : device int [B,max_pages]; token s of sequence b is row s % page
+ *             of page table[b][s / page].  A number outside 0..pages-1 is a page
+ *             that is not there: its tokens are not seen, and none is stored.
+ *   lens    : device int [B], tokens in the cache before the call; a negative
+ *             one marks an idle sequence (o is 0, nothing is stored).  A sequence
+ *             of max_pages * page tokens is full: the new token is seen, not stored.
+ *   lam     : as above.
+ *   strides : q, k, v, k_cache, v_cache, o (t unused but in the caches; b of a
+ *             cache is the distance between pages).
+ *   workspace : retention_attention_step_workspace_bytes() bytes, as above.
+ * Pages may be shared by sequences, but not the places the call stores to.
+ * max_pages * page <= 2^30, B*H <= 2^23.
+ */
+ret_status retention_attention_step(const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
+                                    const int* table, const int* lens, const float* lam, void* o,
+                                    const ret_strides* strides, int B, int H, int Hk, int dk, int dv, int pages,
+                                    int page, int max_pages, float scale, ret_dtype dt, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+size_t retention_attention_step_workspace_bytes(int B, int H, int Hk, int dk, int dv, int page, int max_pages, int maps,
+                                                ret_dtype dt);
+
+/*
+ * Stores the keys and values of T tokens of every sequence (a prompt) in the
+ * cache: token t < counts[b] of sequence b as its token start[b] + t.
+ *   k [B,Hk,T,dk], v [B,Hk,T,dv] in dt.     k_cache, v_cache, table : as above.
+ *   start   : device int [B]; a negative one marks an idle sequence.
+ *   counts  : nullable (T); device int [B], tokens to store.
+ *   strides : k, v, k_cache, v_cache.
+ * Tokens whose page is not there, and those behind max_pages * page, are left
+ * out; all else in the cache stays as it was.  Limits as above with T for S.
+ */
+ret_status retention_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, const int* table,
+                                  const int* start, const int* counts, const ret_strides* strides, int B, int Hk,
+                                  int T, int dk, int dv, int pages, int page, int max_pages, ret_dtype dt,
+                                  void* stream);
+
 /* Text of the last error on this host thread ("" after a successful call).
  * Valid until the next libretention call on the same thread. */
 const char* retention_last_error(void);

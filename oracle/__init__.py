@@ -10,3 +10,4 @@ __all__ = ["recurrent", "recurrent_step", "parallel", "chunkwise", "chunk_state_
            "recurrent_backward", "group_norm"]
 from .block_oracle import (gated_scan, gated_scan_backward, group_norm_gated, group_norm_gated_backward,  # noqa: F401
                            residual, residual_norm_backward, stream_norm)
+from .attention_oracle import attention, attention_backward, attention_step, cache_append  # noqa: F401

@@ -32,8 +32,24 @@ Around retention in a block (strided tensors: any layout with contiguous rows):
     residual_norm_bwd(r, grad_n, grad_r=None, weight=None, f=None, scale=None, ...)
         -> (grad_x, grad_f, grad_weight, grad_bias, grad_scale)
 
+Softmax attention beside retention in a hybrid stack (one map, or the difference of two with lam):
+
+    attention_fwd(q, k, v, lam=None, causal=True, scale=None, offset=None, lens=None, keep=False)
+        -> o  or  (o, kept)     (query heads may share key heads; kept is for the backward)
+    attention_bwd(q, k, v, o, grad_o, kept, lam=None, causal=True, scale=None, offset=None, lens=None)
+        -> (grad_q, grad_k, grad_v, grad_lam)
+    attention_step(q, k, v, k_cache, v_cache, table, lens, lam=None, scale=None) -> o
+        (one new token of every sequence, in place on a paged cache)
+    cache_append(k, v, k_cache, v_cache, table, start, counts=None)   (a prompt's keys and values into the cache)
+
 Build the library with ``python -m retnet_retention_chunkwise_amd.build``.
 """
+from ._attention import (  # noqa: F401
+    attention_bwd,
+    attention_fwd,
+    attention_step,
+    cache_append,
+)
 from ._block import (  # noqa: F401
     gated_scan_bwd,
     gated_scan_checkpoint_shape,

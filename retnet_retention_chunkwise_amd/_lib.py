@@ -54,6 +54,16 @@ SIGNATURES = {
     "retention_residual_norm_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _i, _vp, _vp,
                                          _vp, _vp, _vp, _sp, _i, _i, _i, _vp, _sz, _vp]),
     "retention_residual_norm_bwd_workspace_bytes": (_sz, [_i, _i]),
+    "retention_attention_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sp, _i, _i, _i, _i, _i, _i, _i,
+                                     ctypes.c_float, _i, _i, _i, _vp, _sz, _vp]),
+    "retention_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "retention_attention_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sp, _i, _i, _i,
+                                     _i, _i, _i, _i, ctypes.c_float, _i, _i, _i, _vp, _sz, _vp]),
+    "retention_attention_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "retention_attention_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sp, _i, _i, _i, _i, _i, _i, _i, _i,
+                                      ctypes.c_float, _i, _vp, _sz, _vp]),
+    "retention_attention_step_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "retention_cache_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "retention_last_error": (ctypes.c_char_p, []),
     "retention_version": (_i, []),
 }

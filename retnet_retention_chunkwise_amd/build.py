@@ -41,6 +41,13 @@ SOURCES = [
     "residual_norm.hip",
     "column_sums.hip",
     "block_api.cpp",
+    "attention_fwd_bf16.hip",
+    "attention_fwd_f32.hip",
+    "attention_bwd_bf16.hip",
+    "attention_bwd_f32.hip",
+    "attention_step.hip",
+    "attention_rows.hip",
+    "attention_api.cpp",
 ]
 
 ARCH = "gfx950"

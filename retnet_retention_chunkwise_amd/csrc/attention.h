@@ -1,0 +1,129 @@
+// Launch interface of the attention kernels (attention_*.hip); arguments are
+// validated by the caller.
+#pragma once
+
+#include <type_traits>
+
+#include "kernels.h"
+
+namespace ret {
+
+constexpr int kAttnMaxDk = 256;  // channels of q and k, all maps together
+constexpr int kAttnMaxDv = 256;
+
+struct AttnFwd {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* lam;  // [H]; null: one map
+  const int* lens;   // [B] or null
+  void* o;
+  void* second;      // nullable: [B,H,T,dv], the second map's output
+  float* lse;        // nullable: [B,H,M,T]
+  Strides3 sq, sk, sv, so;
+  int B, H, Hk, T, S;
+  int d, dv;         // channels of one map; of a value
+  float scale;       // of the scores, > 0
+  bool causal;
+  int offset;        // causal: row t sees the keys up to t + offset
+  int dt;
+  int maps() const { return lam != nullptr ? 2 : 1; }
+};
+struct AttnBwd {
+  AttnFwd f;         // the forward's, o, second and lse as it wrote them
+  const void* grad_o;
+  void* grad_q;
+  void* grad_k;
+  void* grad_v;
+  float* grad_lam;   // null with one map
+  Strides3 sdo, sdq, sdk, sdv;
+};
+
+// One new token of every sequence over a paged cache of keys and values.
+// Strides of a cache: between pages (b), heads (h) and tokens of a page (t).
+struct AttnStep {
+  const void* q;     // [B,H,M d]
+  const void* k;     // [B,Hk,M d], the new token's
+  const void* v;     // [B,Hk,dv]
+  void* k_cache;     // [pages,Hk,page,M d]
+  void* v_cache;     // [pages,Hk,page,dv]
+  const int* table;  // [B,max_pages]
+  const int* lens;   // [B], keys in the cache
+  const float* lam;  // [H]; null: one map
+  void* o;           // [B,H,dv]
+  Strides3 sq, sk, sv, skc, svc, so;
+  int B, H, Hk, d, dv, pages, page, max_pages;
+  float scale;
+  int dt;
+  int maps() const { return lam != nullptr ? 2 : 1; }
+};
+// T tokens of every sequence into the cache.
+struct CacheAppend {
+  const void* k;     // [B,Hk,T,dk]
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  const int* table;
+  const int* start;   // [B], position of token 0
+  const int* counts;  // [B] or null: T
+  Strides3 sk, sv, skc, svc;
+  int B, Hk, T, dk, dv, pages, page, max_pages, dt;
+};
+
+// Scratch of the calls in bytes, functions of the sizes alone.
+size_t attention_fwd_workspace(const AttnFwd& a);
+size_t attention_bwd_workspace(const AttnFwd& a);
+hipError_t launch_attention_fwd(const AttnFwd& a, void* ws, hipStream_t s);
+hipError_t launch_attention_bwd(const AttnBwd& a, void* ws, hipStream_t s);
+size_t attention_step_workspace(const AttnStep& a);
+hipError_t launch_attention_step(const AttnStep& a, void* ws, hipStream_t s);
+hipError_t launch_cache_append(const CacheAppend& a, hipStream_t s);
+
+namespace attn {
+
+// Shares of the keys of a call whose keys are split: outputs not yet divided,
+// [split][row][M][dv4] with dv4 = dv rounded up to 4, and their {maximum of
+// scale score log2 e, sum}, [split][row][M].
+struct Partial {
+  float* out;
+  float* ml;
+  int nsplit;
+};
+inline size_t partial_floats(long rows, int maps, int dv, int nsplit) {
+  return nsplit > 1 ? static_cast<size_t>(nsplit) * rows * maps * (((dv + 3) & ~3) + 4) : 0;  // ml in 16 bytes
+}
+inline Partial partial_at(void* ws, long rows, int maps, int dv, int nsplit) {
+  float* out = static_cast<float*>(ws);
+  return {out, out + static_cast<size_t>(nsplit) * rows * maps * ((dv + 3) & ~3), nsplit};
+}
+// Joins the shares into o, second and lse (T rows of every batch element and head).
+hipError_t launch_join(const AttnFwd& a, const Partial& p, hipStream_t s);
+
+// The kernels of one type (E: uint16_t, bf16 bits, or float).
+template <typename E>
+int fwd_rows(const AttnFwd& a);  // rows of a workgroup
+template <typename E>
+hipError_t launch_fwd(const AttnFwd& a, const Partial& part, hipStream_t s);
+template <typename E>
+hipError_t launch_bwd_q(const AttnBwd& a, const float* stats, float* lam_part, hipStream_t s);
+template <typename E>
+int bwd_q_rows(const AttnFwd& a);
+template <typename E>
+hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, hipStream_t s);
+
+// f(maps, channels of all maps, channels of a value), as types, for the
+// smallest sizes built that hold the call's.
+template <typename A, typename F>
+auto with_sizes(const A& a, F&& f) {
+  auto pick = [&](auto maps) {
+    const int dk = a.d * decltype(maps)::value;
+    if (dk <= 64 && a.dv <= 64) return f(maps, std::integral_constant<int, 64>(), std::integral_constant<int, 64>());
+    if (dk <= 128 && a.dv <= 128)
+      return f(maps, std::integral_constant<int, 128>(), std::integral_constant<int, 128>());
+    return f(maps, std::integral_constant<int, 256>(), std::integral_constant<int, 256>());
+  };
+  return a.maps() > 1 ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 1>());
+}
+
+}  // namespace attn
+}  // namespace ret

@@ -1,0 +1,374 @@
+// Gradients of softmax attention (attention_fwd.h).  With dP = dO V^T and
+// D_m[t] = sum_s A_m dP:
+//   dV = (A_1 - lam A_2)^T dO,
+//   dS_1 = A_1 (dP - D_1),  dS_2 = -lam A_2 (dP - D_2),
+//   dq_m = scale dS_m k_m,  dk_m = scale dS_m^T q_m,  dlam = -sum A_2 dP,
+// A_m = exp(scale q_m . k_m - lse_m) from the forward's lse.  Three launches:
+//   rows    D_2 = dO . second and D_1 = dO . o + lam D_2 of every row, with
+//           lse log2 e beside them;
+//   q pass  a wave owns 16 NB rows as columns and streams keys and values
+//           through LDS, as the forward does: S^T, dP^T and then
+//           dQ^T[chan][row] += K^T dS^T;
+//   kv pass a wave owns 16 NB keys as columns and streams q and dO of every
+//           head that shares them: S, dP, then dV^T += dO^T P and
+//           dK^T += Q^T dS.
+// The scores are computed twice (7 products in place of 5) so that every
+// gradient is summed by one wave in a fixed order: no atomics, the same bits
+// every time.  P and dS are rounded to the tensors' type as operands, all else
+// is fp32.
+#pragma once
+
+#include "attention.h"
+#include "attention_tiles.h"
+#include "row_sum.h"
+
+namespace ret {
+namespace attn {
+
+// stats: [M][B*H*T] of {lse log2 e, D}: first all of map 1.
+template <typename E, int MAPS, int DK, int DV, int NB, int NW, int KT>
+__global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, const float2* __restrict__ stats,
+                                                                  float* __restrict__ lam_part, int tiles) {
+  typedef Mma<E> X;
+  typedef typename X::Frag Frag;
+  constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
+  constexpr int KB = KT / 16, KS = D / 32, VS = DV / 32, CB = D / 16;
+  constexpr int KLD = kTileLd<E, DK>, VLD = kTileLd<E, DV>;
+  __shared__ __attribute__((aligned(16))) E Ks[KT * KLD];
+  __shared__ __attribute__((aligned(16))) E Vs[KT * VLD];
+  __shared__ float wave_lam[NW];
+
+  const AttnFwd& a = g.f;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
+  const int id = blockIdx.x;
+  const int tile = tiles - 1 - id % tiles;  // the longest rows first
+  const int bh = id / tiles, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
+  const int len = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
+  auto seen = [&](int t) { return a.causal ? min(max(t + a.offset + 1, 0), len) : len; };
+  const int q0 = tile * QT, w0 = q0 + wave * 16 * NB;
+  const int last = (seen(min(q0 + QT, a.T) - 1) + KT - 1) / KT;
+  const int wmax = w0 < a.T ? seen(min(w0 + 16 * NB, a.T) - 1) : 0, wall = seen(w0);
+
+  const E* q = static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h;
+  const E* dout = static_cast<const E*>(g.grad_o) + b * g.sdo.b + h * g.sdo.h;
+  const E* k = static_cast<const E*>(a.k) + b * a.sk.b + hk * a.sk.h;
+  const E* v = static_cast<const E*>(a.v) + b * a.sv.b + hk * a.sv.h;
+  const long rows = static_cast<long>(a.B) * a.H * a.T;
+  Frag qf[NB][MAPS * KS], gf[NB][VS];
+  int lim[NB];
+  float2 st[MAPS][NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int t = w0 + 16 * n + col;
+    const int row = min(t, a.T - 1);
+    load_columns<E, MAPS, D>(q + row * a.sq.t, t < a.T, a.d, lane, qf[n]);
+    load_columns<E, 1, DV>(dout + row * g.sdo.t, t < a.T, a.dv, lane, gf[n]);
+    lim[n] = seen(t);
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m)
+      st[m][n] = t < a.T ? stats[m * rows + static_cast<long>(bh) * a.T + t] : make_float2(INFINITY, 0.0f);
+  }
+  const float c = a.scale * kLog2e;
+  f32x4 dq[MAPS][CB][NB];
+#pragma unroll
+  for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) dq[m][i][n] = f32x4{0, 0, 0, 0};
+  float lam_sum = 0.0f;
+
+  Stage<E, KT, MAPS, D, THREADS> ks(a.d, tid);
+  Stage<E, KT, 1, DV, THREADS> vs(a.dv, tid);
+  if (last > 0) {
+    ks.load(k, a.sk.t, 0, len, a.d);
+    vs.load(v, a.sv.t, 0, len, a.dv);
+  }
+  for (int i = 0; i < last; ++i) {
+    const int k0 = i * KT;
+    __syncthreads();
+    ks.store(Ks, KLD, k0, len, a.d);
+    vs.store(Vs, VLD, k0, len, a.dv);
+    __syncthreads();
+    if (i + 1 < last) {
+      ks.load(k, a.sk.t, k0 + KT, len, a.d);
+      vs.load(v, a.sv.t, k0 + KT, len, a.dv);
+    }
+    if (k0 >= wmax) continue;
+    f32x4 dp[KB][NB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) dp[kb][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < VS; ++e) {
+        const Frag vf = rows_frag<E>(Vs, VLD, 16 * kb, 32 * e, lane);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) dp[kb][n] = X::mma(vf, gf[n][e], dp[kb][n]);
+      }
+    }
+    const bool edge = k0 + KT > wall;
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+      f32x4 s[KB][NB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) s[kb][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < KS; ++e) {
+          const Frag kf = rows_frag<E>(Ks, KLD, 16 * kb, m * D + 32 * e, lane);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) s[kb][n] = X::mma(kf, qf[n][m * KS + e], s[kb][n]);
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float p = fast_exp2(fmaf(s[kb][n][r], c, -st[m][n].x));
+            if (edge && k0 + 16 * kb + 4 * grp + r >= lim[n]) p = 0.0f;
+            if (m == 1) lam_sum = fmaf(p, dp[kb][n][r], lam_sum);
+            s[kb][n][r] = p * (dp[kb][n][r] - st[m][n].y);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < KT / 32; ++j) {
+        Frag ds[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[2 * j][n], s[2 * j + 1][n]);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          const Frag kt = cols_frag<E>(Ks, KLD, 32 * j, m * D + 16 * cb, lane);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) dq[m][cb][n] = X::mma(kt, ds[n], dq[m][cb][n]);
+        }
+      }
+    }
+  }
+
+  if constexpr (MAPS > 1) {  // this tile's share of the weight's gradient, in a fixed order
+    const float w = lanes_sum<64>(lam_sum);
+    if (lane == 0) wave_lam[wave] = w;
+    __syncthreads();
+    if (tid == 0) {
+      float x = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) x += wave_lam[i];
+      lam_part[(static_cast<long>(b) * tiles + tile) * a.H + h] = -x;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int t = w0 + 16 * n + col;
+    if (t >= a.T) continue;
+    E* out = static_cast<E*>(g.grad_q) + b * g.sdq.b + h * g.sdq.h + t * g.sdq.t;
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+      const float f = m == 0 ? a.scale : -a.lam[h] * a.scale;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) store4<E>(out + m * a.d, 16 * cb + 4 * grp, a.d, dq[m][cb][n] * f);
+    }
+  }
+}
+
+template <typename E, int MAPS, int DK, int DV, int NB, int NW, int QT>
+__global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, const float2* __restrict__ stats,
+                                                                   int tiles) {
+  typedef Mma<E> X;
+  typedef typename X::Frag Frag;
+  constexpr int D = DK / MAPS, THREADS = 64 * NW, KT = 16 * NB * NW;
+  constexpr int QB = QT / 16, KS = D / 32, VS = DV / 32, CB = D / 16, VB = DV / 16;
+  constexpr int QLD = kTileLd<E, DK>, GLD = kTileLd<E, DV>;
+  __shared__ __attribute__((aligned(16))) E Qs[QT * QLD];
+  __shared__ __attribute__((aligned(16))) E Gs[QT * GLD];
+  __shared__ __attribute__((aligned(16))) float Ls[MAPS][QT], Ds[MAPS][QT];
+  static_assert(MAPS * QT <= THREADS, "a thread per row's statistics");
+
+  const AttnFwd& a = g.f;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
+  const int id = blockIdx.x;
+  const int tile = id % tiles;  // the keys that most rows see first
+  const int bh = id / tiles, b = bh / a.Hk, hk = bh % a.Hk, G = a.H / a.Hk;
+  const int len = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
+  const int k0 = tile * KT, w0 = k0 + wave * 16 * NB;
+  // the first row that sees a key
+  auto from = [&](int key) { return a.causal ? min(max(key - a.offset, 0), a.T) : 0; };
+  const int t0 = from(k0) / QT * QT, n_tiles = k0 < len ? (a.T - t0 + QT - 1) / QT : 0;
+  // rows that see some key, and every key, of this wave
+  const int wfirst = w0 < len ? from(w0) : a.T, wall = from(w0 + 16 * NB - 1);
+
+  const E* k = static_cast<const E*>(a.k) + b * a.sk.b + hk * a.sk.h;
+  const E* v = static_cast<const E*>(a.v) + b * a.sv.b + hk * a.sv.h;
+  const long rows = static_cast<long>(a.B) * a.H * a.T;
+  Frag kf[NB][MAPS * KS], vf[NB][VS];
+  int lim[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int key = w0 + 16 * n + col;
+    const int row = min(key, a.S - 1);
+    load_columns<E, MAPS, D>(k + row * a.sk.t, key < len, a.d, lane, kf[n]);
+    load_columns<E, 1, DV>(v + row * a.sv.t, key < len, a.dv, lane, vf[n]);
+    lim[n] = from(key);
+  }
+  const float c = a.scale * kLog2e;
+  f32x4 dk[MAPS][CB][NB], dv[VB][NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+      for (int i = 0; i < CB; ++i) dk[m][i][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < VB; ++i) dv[i][n] = f32x4{0, 0, 0, 0};
+  }
+
+  Stage<E, QT, MAPS, D, THREADS> qs(a.d, tid);
+  Stage<E, QT, 1, DV, THREADS> gs(a.dv, tid);
+  float2 st;
+  auto load = [&](int i) {
+    const int h = hk * G + i / n_tiles, row0 = t0 + i % n_tiles * QT;
+    qs.load(static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h, a.sq.t, row0, a.T, a.d);
+    gs.load(static_cast<const E*>(g.grad_o) + b * g.sdo.b + h * g.sdo.h, g.sdo.t, row0, a.T, a.dv);
+    if (tid < MAPS * QT) {
+      const int t = row0 + tid % QT;
+      st = t < a.T ? stats[tid / QT * rows + (static_cast<long>(b) * a.H + h) * a.T + t] : make_float2(INFINITY, 0.0f);
+    }
+  };
+  const int n_all = G * n_tiles;
+  if (n_all > 0) load(0);
+  for (int i = 0; i < n_all; ++i) {
+    const int row0 = t0 + i % n_tiles * QT;
+    __syncthreads();
+    qs.store(Qs, QLD, row0, a.T, a.d);
+    gs.store(Gs, GLD, row0, a.T, a.dv);
+    if (tid < MAPS * QT) {
+      Ls[tid / QT][tid % QT] = st.x;
+      Ds[tid / QT][tid % QT] = st.y;
+    }
+    __syncthreads();
+    if (i + 1 < n_all) load(i + 1);
+    if (row0 + QT <= wfirst) continue;
+    const float lam = MAPS > 1 ? a.lam[hk * G + i / n_tiles] : 0.0f;
+    const bool edge = row0 < wall;
+    f32x4 dp[QB][NB], pv[QB][NB];
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) dp[qb][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < VS; ++e) {
+        const Frag x = rows_frag<E>(Gs, GLD, 16 * qb, 32 * e, lane);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) dp[qb][n] = X::mma(x, vf[n][e], dp[qb][n]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+      f32x4 s[QB][NB];
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) s[qb][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < KS; ++e) {
+          const Frag x = rows_frag<E>(Qs, QLD, 16 * qb, m * D + 32 * e, lane);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) s[qb][n] = X::mma(x, kf[n][m * KS + e], s[qb][n]);
+        }
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(&Ls[m][16 * qb + 4 * grp]);
+        const f32x4 d4 = *reinterpret_cast<const f32x4*>(&Ds[m][16 * qb + 4 * grp]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float p = fast_exp2(fmaf(s[qb][n][r], c, -l4[r]));
+            if (edge && row0 + 16 * qb + 4 * grp + r < lim[n]) p = 0.0f;
+            if (m == 1) p *= -lam;
+            pv[qb][n][r] = m == 0 ? p : pv[qb][n][r] + p;
+            s[qb][n][r] = p * (dp[qb][n][r] - d4[r]);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < QT / 32; ++j) {
+        Frag ds[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[2 * j][n], s[2 * j + 1][n]);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          const Frag x = cols_frag<E>(Qs, QLD, 32 * j, m * D + 16 * cb, lane);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) dk[m][cb][n] = X::mma(x, ds[n], dk[m][cb][n]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < QT / 32; ++j) {
+      Frag p[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) p[n] = X::pack(pv[2 * j][n], pv[2 * j + 1][n]);
+#pragma unroll
+      for (int vb = 0; vb < VB; ++vb) {
+        const Frag x = cols_frag<E>(Gs, GLD, 32 * j, 16 * vb, lane);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) dv[vb][n] = X::mma(x, p[n], dv[vb][n]);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int key = w0 + 16 * n + col;
+    if (key >= a.S) continue;
+    const bool in = key < len;  // keys behind the sequence have no gradient
+    E* ok = static_cast<E*>(g.grad_k) + b * g.sdk.b + hk * g.sdk.h + key * g.sdk.t;
+    E* ov = static_cast<E*>(g.grad_v) + b * g.sdv.b + hk * g.sdv.h + key * g.sdv.t;
+    const f32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+        store4<E>(ok + m * a.d, 16 * cb + 4 * grp, a.d, in ? dk[m][cb][n] * a.scale : zero);
+#pragma unroll
+    for (int vb = 0; vb < VB; ++vb) store4<E>(ov, 16 * vb + 4 * grp, a.dv, in ? dv[vb][n] : zero);
+  }
+}
+
+template <typename E, int DK>
+struct BwdShape {
+  static constexpr int NB = sizeof(E) == 2 && DK <= 128 ? 2 : 1;
+  static constexpr int NW = 4, TILE = 16 * NB * NW, STREAM = 32;
+};
+
+template <typename E>
+int bwd_q_rows(const AttnFwd& a) {
+  return with_sizes(a, [](auto, auto dk, auto) { return BwdShape<E, decltype(dk)::value>::TILE; });
+}
+
+template <typename E>
+hipError_t launch_bwd_q(const AttnBwd& a, const float* stats, float* lam_part, hipStream_t s) {
+  return with_sizes(a.f, [&](auto m, auto dk, auto dv) {
+    constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
+    typedef BwdShape<E, DK> C;
+    const int tiles = (a.f.T + C::TILE - 1) / C::TILE;
+    hipLaunchKernelGGL((attention_bwd_q_kernel<E, M, DK, DV, C::NB, C::NW, C::STREAM>),
+                       dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.H), dim3(64 * C::NW), 0, s, a,
+                       reinterpret_cast<const float2*>(stats), lam_part, tiles);
+    return hipGetLastError();
+  });
+}
+
+template <typename E>
+hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, hipStream_t s) {
+  return with_sizes(a.f, [&](auto m, auto dk, auto dv) {
+    constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
+    typedef BwdShape<E, DK> C;
+    const int tiles = (a.f.S + C::TILE - 1) / C::TILE;
+    hipLaunchKernelGGL((attention_bwd_kv_kernel<E, M, DK, DV, C::NB, C::NW, C::STREAM>),
+                       dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.Hk), dim3(64 * C::NW), 0, s, a,
+                       reinterpret_cast<const float2*>(stats), tiles);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace attn
+}  // namespace ret

@@ -1,0 +1,247 @@
+// Softmax attention over a whole sequence, ordinary (M = 1 map) or differential
+// (M = 2):  o[t] = sum_s (A_1 - lam_h A_2)[t,s] v[s],  A_m = softmax over the
+// visible s of scale q_m[t] . k_m[s].
+//
+// A workgroup holds QT rows of q for one query head and streams the keys and
+// values through LDS, KT at a time; each wave owns 16 NB rows as the columns of
+// its products:
+//   S^T[key][row]  = K Q^T    (K from LDS along its rows, Q in registers)
+//   O^T[chan][row] += V^T P^T (V from LDS across its rows; P^T is S^T's own
+//                              registers, rounded to the tensors' type)
+// so a row's scores lie in one lane group's registers and its maximum takes
+// two lane swaps.  One pass with a running maximum and sum; the maximum is only
+// moved (and O scaled) when a score exceeds it by 2^kSlack, which no bf16 or
+// fp32 value notices: p is then at most 2^kSlack instead of 1.  Both maps read
+// the same value tile once and keep an output each, because they are divided by
+// different sums.  Products are bf16 MFMA (fp32: fp32 MFMA); scores, maxima,
+// sums and outputs are fp32; p is rounded to bf16 as an operand.
+#pragma once
+
+#include "attention.h"
+#include "attention_tiles.h"
+
+namespace ret {
+namespace attn {
+
+constexpr float kSlack = 8.0f;
+
+template <typename E, int MAPS, int DK, int DV, int NB, int NW, int KT>
+__global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Partial part, int tiles) {
+  typedef Mma<E> X;
+  typedef typename X::Frag Frag;
+  constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
+  constexpr int KB = KT / 16, KS = D / 32, VB = DV / 16;
+  constexpr int KLD = kTileLd<E, DK>, VLD = kTileLd<E, DV>;
+  __shared__ __attribute__((aligned(16))) E Ks[KT * KLD];
+  __shared__ __attribute__((aligned(16))) E Vs[KT * VLD];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
+  const int id = blockIdx.x;
+  const int tile = tiles - 1 - id % tiles;  // the longest rows first
+  const int bh = id / tiles, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
+  const int split = blockIdx.y;
+  const int len = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
+  // keys that a row t sees
+  auto seen = [&](int t) { return a.causal ? min(max(t + a.offset + 1, 0), len) : len; };
+  const int q0 = tile * QT, w0 = q0 + wave * 16 * NB;
+  const int kmax = seen(min(q0 + QT, a.T) - 1);
+  const int all = (kmax + KT - 1) / KT;
+  const int first = static_cast<int>(static_cast<long>(all) * split / part.nsplit);
+  const int last = static_cast<int>(static_cast<long>(all) * (split + 1) / part.nsplit);
+  // keys that some row, and that every row, of this wave sees
+  const int wmax = w0 < a.T ? seen(min(w0 + 16 * NB, a.T) - 1) : 0, wall = seen(w0);
+
+  const E* q = static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h;
+  const E* k = static_cast<const E*>(a.k) + b * a.sk.b + hk * a.sk.h;
+  const E* v = static_cast<const E*>(a.v) + b * a.sv.b + hk * a.sv.h;
+  Frag qf[NB][MAPS * KS];
+  int lim[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int t = w0 + 16 * n + col;
+    load_columns<E, MAPS, D>(q + min(t, a.T - 1) * a.sq.t, t < a.T, a.d, lane, qf[n]);
+    lim[n] = seen(t);
+  }
+
+  const float c = a.scale * kLog2e, slack = kSlack / c;
+  f32x4 o[MAPS][VB][NB];
+  float mx[MAPS][NB], sum[MAPS][NB];
+#pragma unroll
+  for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mx[m][n] = -INFINITY;
+      sum[m][n] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VB; ++i) o[m][i][n] = f32x4{0, 0, 0, 0};
+    }
+
+  Stage<E, KT, MAPS, D, THREADS> ks(a.d, tid);
+  Stage<E, KT, 1, DV, THREADS> vs(a.dv, tid);
+  if (first < last) {
+    ks.load(k, a.sk.t, first * KT, len, a.d);
+    vs.load(v, a.sv.t, first * KT, len, a.dv);
+  }
+  for (int i = first; i < last; ++i) {
+    const int k0 = i * KT;
+    __syncthreads();
+    ks.store(Ks, KLD, k0, len, a.d);
+    vs.store(Vs, VLD, k0, len, a.dv);
+    __syncthreads();
+    if (i + 1 < last) {
+      ks.load(k, a.sk.t, k0 + KT, len, a.d);
+      vs.load(v, a.sv.t, k0 + KT, len, a.dv);
+    }
+    if (k0 >= wmax) continue;
+    Frag pf[MAPS][NB][KT / 32];
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+      f32x4 s[KB][NB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) s[kb][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < KS; ++e) {
+          const Frag kf = rows_frag<E>(Ks, KLD, 16 * kb, m * D + 32 * e, lane);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) s[kb][n] = X::mma(kf, qf[n][m * KS + e], s[kb][n]);
+        }
+      }
+      if (k0 + KT > wall) {  // some row does not see some key
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (k0 + 16 * kb + 4 * grp + r >= lim[n]) s[kb][n][r] = -INFINITY;
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = fmaxf(top, s[kb][n][r]);
+        if (__any(top > mx[m][n] + slack)) {
+          const float next = fmaxf(mx[m][n], row4_max(top));
+          const float f = next == -INFINITY ? 1.0f : fast_exp2((mx[m][n] - next) * c);
+          mx[m][n] = next;
+          sum[m][n] *= f;
+#pragma unroll
+          for (int j = 0; j < VB; ++j) o[m][j][n] *= f;
+        }
+        const float mc = mx[m][n] == -INFINITY ? 0.0f : mx[m][n] * c;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float p = fast_exp2(fmaf(s[kb][n][r], c, -mc));
+            s[kb][n][r] = p;
+            sum[m][n] += p;
+          }
+#pragma unroll
+        for (int j = 0; j < KT / 32; ++j) pf[m][n][j] = X::pack(s[2 * j][n], s[2 * j + 1][n]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < KT / 32; ++j)
+#pragma unroll
+      for (int vb = 0; vb < VB; ++vb) {
+        const Frag vf = cols_frag<E>(Vs, VLD, 32 * j, 16 * vb, lane);
+#pragma unroll
+        for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) o[m][vb][n] = X::mma(vf, pf[m][n][j], o[m][vb][n]);
+      }
+  }
+
+  const float lam = MAPS > 1 ? a.lam[h] : 0.0f;
+  const long rows = static_cast<long>(a.B) * a.H * a.T;
+#pragma unroll
+  for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) sum[m][n] = row4_sum(sum[m][n]);
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int t = w0 + 16 * n + col;
+    if (t >= a.T) continue;
+    const long row = static_cast<long>(bh) * a.T + t;
+    if (part.nsplit > 1) {
+      const int dv4 = (a.dv + 3) & ~3;
+#pragma unroll
+      for (int m = 0; m < MAPS; ++m) {
+        const long at = (split * rows + row) * MAPS + m;
+        if (grp == 0) reinterpret_cast<float2*>(part.ml)[at] = make_float2(mx[m][n] * c, sum[m][n]);
+#pragma unroll
+        for (int vb = 0; vb < VB; ++vb) {
+          const int ch = 16 * vb + 4 * grp;
+          if (ch < dv4) *reinterpret_cast<f32x4*>(part.out + at * dv4 + ch) = o[m][vb][n];
+        }
+      }
+      continue;
+    }
+    float inv[MAPS];
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+      const float l = sum[m][n];
+      inv[m] = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees no key is zero
+      if (a.lse != nullptr && grp == 0)
+        a.lse[(static_cast<long>(bh) * MAPS + m) * a.T + t] =
+            l == 0.0f ? -INFINITY : mx[m][n] * a.scale + logf(l);
+    }
+    E* out = static_cast<E*>(a.o) + b * a.so.b + h * a.so.h + t * a.so.t;
+    E* two = static_cast<E*>(a.second) + row * a.dv;
+#pragma unroll
+    for (int vb = 0; vb < VB; ++vb) {
+      f32x4 y = o[0][vb][n] * inv[0];
+      if constexpr (MAPS > 1) {
+        const f32x4 z = o[1][vb][n] * inv[1];
+        y -= lam * z;
+        if (a.second != nullptr) store4<E>(two, 16 * vb + 4 * grp, a.dv, z);
+      }
+      store4<E>(out, 16 * vb + 4 * grp, a.dv, y);
+    }
+  }
+}
+
+// Keys are split where the rows alone give fewer workgroups than the device has
+// compute units, into ranges of at least kSplitKeys keys.
+constexpr int kSplitKeys = 256, kSplitTarget = 512;
+
+inline int splits(long workgroups, int keys) {
+  if (workgroups >= kSplitTarget / 2 || keys < 2 * kSplitKeys) return 1;
+  const long want = kSplitTarget / workgroups, most = keys / kSplitKeys;
+  return static_cast<int>(want < most ? want : most);
+}
+
+template <typename E, int MAPS, int DK, int DV>
+struct FwdShape {
+  static constexpr int NB = sizeof(E) == 2 && DV * MAPS <= 256 ? 2 : 1;
+  static constexpr int NW = 4, KT = 32, QT = 16 * NB * NW;
+};
+
+// Rows of a tile, for the sizes that hold the call's.
+template <typename E>
+int fwd_rows(const AttnFwd& a) {
+  return with_sizes(a, [](auto m, auto dk, auto dv) {
+    return FwdShape<E, decltype(m)::value, decltype(dk)::value, decltype(dv)::value>::QT;
+  });
+}
+
+template <typename E>
+hipError_t launch_fwd(const AttnFwd& a, const Partial& part, hipStream_t s) {
+  return with_sizes(a, [&](auto m, auto dk, auto dv) {
+    constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
+    typedef FwdShape<E, M, DK, DV> C;
+    const int tiles = (a.T + C::QT - 1) / C::QT;
+    hipLaunchKernelGGL((attention_fwd_kernel<E, M, DK, DV, C::NB, C::NW, C::KT>),
+                       dim3(static_cast<unsigned>(tiles) * a.B * a.H, part.nsplit), dim3(64 * C::NW), 0, s, a, part,
+                       tiles);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace attn
+}  // namespace ret

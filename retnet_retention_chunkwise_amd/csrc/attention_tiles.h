@@ -1,0 +1,219 @@
+// Building blocks of the attention kernels: tiles of rows staged from strided
+// tensors into LDS, and the 16x16 matrix products on them, for bf16 and fp32
+// alike.
+//
+// Every product is C[r][c] += sum_k A[r][k] B[k][c] on 16x16 accumulators: lane
+// l holds C[4 (l / 16) + i][l % 16], i = 0..3.  Operands are eight values per
+// lane, A[l % 16][k] and B[k][l % 16] for the lane's eight k.  Which k belong to
+// which lane is free as long as A and B agree, and two ways are used:
+//   along a row (rows_frag): k = 8 (l / 16) + 0..7, consecutive channels;
+//   along tile rows (cols_frag): k = 4 (l / 16) + 0..3 and 16 + the same, which
+//   is what two accumulators of a former product hold, so that probabilities
+//   become operands without leaving their lane.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+#include "gfx950.h"
+#include "vec_io.h"
+
+namespace ret {
+
+template <typename E>
+struct Mma;
+template <>
+struct Mma<uint16_t> {
+  typedef bf16x8 Frag;
+  __device__ __forceinline__ static f32x4 mma(Frag a, Frag b, f32x4 c) { return mfma(a, b, c); }
+  // Two accumulators as an operand along their rows (round to nearest even).
+  __device__ __forceinline__ static Frag pack(f32x4 lo, f32x4 hi) { return pack_bf16x8(lo, hi); }
+};
+template <>
+struct Mma<float> {
+  typedef f32x8 Frag;
+  __device__ __forceinline__ static f32x4 mma(Frag a, Frag b, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+  }
+  __device__ __forceinline__ static Frag pack(f32x4 lo, f32x4 hi) {
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+// Rows of DIM elements in LDS, LD apart: 16 bytes more than the row, so that 16
+// rows read at one channel lie in different banks.
+template <typename E, int DIM>
+constexpr int kTileLd = DIM + 16 / static_cast<int>(sizeof(E));
+
+// A[row][channels]: eight consecutive channels from c0 + 8 (lane / 16) of row lane % 16.
+template <typename E>
+__device__ __forceinline__ typename Mma<E>::Frag rows_frag(const E* tile, int ld, int row0, int c0, int lane) {
+  const E* p = tile + (row0 + (lane & 15)) * ld + c0 + 8 * (lane >> 4);
+  if constexpr (sizeof(E) == 2) {
+    return *reinterpret_cast<const bf16x8*>(p);
+  } else {
+    return Mma<float>::pack(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4));
+  }
+}
+
+// A[channel][rows]: of channel c0 + lane % 16, the rows row0 + 4 (lane / 16) + 0..3 and those 16 further.
+template <typename E>
+__device__ __forceinline__ typename Mma<E>::Frag cols_frag(const E* tile, int ld, int row0, int c0, int lane) {
+  const int j = lane & 15, g = lane >> 4;
+  if constexpr (sizeof(E) == 2) {
+    const uint16_t* p = tile + (row0 + 4 * g + j / 4) * ld + c0 + 4 * (j % 4);
+    return join(lds_read_tr(p), lds_read_tr(p + 16 * ld));
+  } else {
+    const float* p = tile + (row0 + 4 * g) * ld + c0 + j;
+    f32x8 f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = p[e * ld];
+      f[4 + e] = p[(16 + e) * ld];
+    }
+    return f;
+  }
+}
+
+// A lane's 16 bytes of a row of n elements, nominally from element c on.  No lane
+// leaves the others: where the row ends inside the piece it is read so far back
+// that it ends with the row, and shifted when it is used; a piece behind the row
+// reads the row's end.  What lies behind the row is zero if n is no multiple of
+// a piece, and otherwise left: it meets zeros in the other operand or fills
+// outputs that are not stored.
+template <typename E>
+struct Piece16 {
+  static constexpr int CE = 16 / static_cast<int>(sizeof(E));
+  int at, by;
+  __device__ __forceinline__ Piece16(int c, int n) : at(min(c, max(n - CE, 0))), by(c - at) {}
+  __device__ __forceinline__ u32x4 load(const E* row, int n) const {
+    typedef typename RawOf<16, static_cast<int>(sizeof(E))>::at At;
+    if (n >= CE) return *reinterpret_cast<const At*>(row + at);
+    E e[CE];
+#pragma unroll
+    for (int i = 0; i < CE; ++i) {
+      const E y = row[i < n ? i : 0];
+      e[i] = i < n ? y : E(0);
+    }
+    u32x4 x;
+    __builtin_memcpy(&x, e, 16);
+    return x;
+  }
+  __device__ __forceinline__ u32x4 finish(u32x4 x, int n) const {
+    if (n % CE != 0) {
+      if constexpr (sizeof(E) == 2) {
+        const u32x4 y = {x[0] >> 16 | x[1] << 16, x[1] >> 16 | x[2] << 16, x[2] >> 16 | x[3] << 16, x[3] >> 16};
+        if (by & 1) x = y;
+      }
+      const int words = by * static_cast<int>(sizeof(E)) / 4;
+      if (words & 1) x = u32x4{x[1], x[2], x[3], 0};
+      if (words & 2) x = u32x4{x[2], x[3], 0, 0};
+      if (words & ~3) x = u32x4{0, 0, 0, 0};
+    }
+    return x;
+  }
+  __device__ __forceinline__ u32x4 zero_behind(u32x4 x) const { return by >= CE ? u32x4{0, 0, 0, 0} : x; }
+};
+
+// ROWS rows of MAPS parts of d elements, each part padded to D, on their way
+// from memory to LDS: THREADS threads, 16 bytes a piece.  load() only requests;
+// store() waits, and puts zeros for the rows from n on (which load the last row).
+template <typename E, int ROWS, int MAPS, int D, int THREADS>
+struct Stage {
+  static constexpr int CE = 16 / static_cast<int>(sizeof(E));
+  static constexpr int CH = MAPS * D / CE;               // pieces of a row
+  static constexpr int STEP = THREADS / CH;              // rows of one round
+  static constexpr int N = ROWS / STEP;                  // rounds
+  static_assert(THREADS % CH == 0 && ROWS % STEP == 0, "a thread stays in its columns, every round is full");
+  u32x4 r[N];
+  Piece16<E> piece;
+  int row, col;  // of the thread's first piece in the tile
+  int part;      // elements in front of its part of a row
+  __device__ __forceinline__ Stage(int d, int tid)
+      : piece((tid % CH - (MAPS > 1 ? tid % CH / (D / CE) : 0) * (D / CE)) * CE, d),
+        row(tid / CH),
+        col(tid % CH * CE),
+        part(MAPS > 1 ? tid % CH / (D / CE) * d : 0) {}
+
+  // Rows row0.. of base, stride apart; n > 0 rows are readable.
+  __device__ __forceinline__ void load(const E* base, long stride, int row0, int n, int d) {
+    const E* p = base + part;
+    if (row0 + ROWS <= n) {
+      p += (row0 + row) * stride;
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = piece.load(p + i * STEP * stride, d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = piece.load(p + min(row0 + row + i * STEP, n - 1) * stride, d);
+    }
+  }
+  __device__ __forceinline__ void store(E* tile, int ld, int row0, int n, int d) {
+    if (row0 + ROWS > n) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (row0 + row + i * STEP >= n) r[i] = u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      *reinterpret_cast<u32x4*>(tile + (row + i * STEP) * ld + col) = piece.finish(r[i], d);
+  }
+};
+
+// B[channels][column]: column col's row of MAPS parts of d elements, padded with
+// zeros to D each, channels along a row; zeros where the column is not in (row
+// is readable all the same).
+template <typename E, int MAPS, int D>
+__device__ __forceinline__ void load_columns(const E* row, bool in, int d, int lane,
+                                             typename Mma<E>::Frag (&f)[MAPS * D / 32]) {
+  constexpr int CE = 16 / static_cast<int>(sizeof(E));
+#pragma unroll
+  for (int k = 0; k < MAPS * D / 32; ++k) {
+    const int map = k / (D / 32), c = (k - map * (D / 32)) * 32 + 8 * (lane >> 4);
+    u32x4 x[8 / CE];
+#pragma unroll
+    for (int i = 0; i < 8 / CE; ++i) {
+      const Piece16<E> piece(c + i * CE, d);
+      x[i] = piece.zero_behind(piece.finish(piece.load(row + map * d, d), d));
+      if (!in) x[i] = u32x4{0, 0, 0, 0};
+    }
+    __builtin_memcpy(&f[k], x, sizeof(f[k]));
+  }
+}
+
+// Four consecutive elements of a row of n from element c on; c is a multiple of
+// 4, elements from n on are left out.
+template <typename E>
+__device__ __forceinline__ void store4(E* row, int c, int n, f32x4 x) {
+  if (n % 4 == 0) {
+    typename RawOf<4 * sizeof(E), sizeof(E)>::type r;
+    if constexpr (sizeof(E) == 4) {
+      r = __builtin_bit_cast(u32x4, x);
+    } else {
+      r[0] = static_cast<uint32_t>(f32_to_bf16(x[0])) | (static_cast<uint32_t>(f32_to_bf16(x[1])) << 16);
+      r[1] = static_cast<uint32_t>(f32_to_bf16(x[2])) | (static_cast<uint32_t>(f32_to_bf16(x[3])) << 16);
+    }
+    if (c < n) *reinterpret_cast<typename RawOf<4 * sizeof(E), sizeof(E)>::at*>(row + c) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < n) Elem<E>::store(row, c + i, x[i]);
+  }
+}
+
+// The largest of x over lanes l, l^16, l^32, l^48, in each of them.
+__device__ __forceinline__ float row4_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  const float y = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(y), __float_as_uint(y), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+}  // namespace ret
