@@ -107,20 +107,31 @@ hipError_t launch_fwd(const AttnFwd& a, const Partial& part, hipStream_t s);
 template <typename E>
 hipError_t launch_bwd_q(const AttnBwd& a, const float* stats, float* lam_part, hipStream_t s);
 template <typename E>
-int bwd_q_rows(const AttnFwd& a);
+int bwd_rows(const AttnFwd& a);  // rows of a workgroup
 template <typename E>
-hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, hipStream_t s);
+int bwd_keys(const AttnFwd& a);  // keys of a workgroup
+// shares > 1: every share of the rows leaves its sums in part
+template <typename E>
+hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, float* part, int shares, hipStream_t s);
 
-// f(maps, channels of all maps, channels of a value), as types, for the
-// smallest sizes built that hold the call's.
+// f(maps, channels of all maps, channels of a value, whole), as types, for the
+// smallest sizes built that hold the call's.  whole: the rows of a map and of a
+// value are whole pieces of 16 bytes; rows that are not take code that shifts
+// their ends, built for two sizes.
 template <typename A, typename F>
 auto with_sizes(const A& a, F&& f) {
+  typedef std::integral_constant<int, 64> N64;
+  typedef std::integral_constant<int, 128> N128;
+  typedef std::integral_constant<int, 256> N256;
   auto pick = [&](auto maps) {
-    const int dk = a.d * decltype(maps)::value;
-    if (dk <= 64 && a.dv <= 64) return f(maps, std::integral_constant<int, 64>(), std::integral_constant<int, 64>());
-    if (dk <= 128 && a.dv <= 128)
-      return f(maps, std::integral_constant<int, 128>(), std::integral_constant<int, 128>());
-    return f(maps, std::integral_constant<int, 256>(), std::integral_constant<int, 256>());
+    const int dk = a.d * decltype(maps)::value, piece = a.dt ? 8 : 4;
+    if (a.d % piece != 0 || a.dv % piece != 0) {
+      if (dk <= 128 && a.dv <= 128) return f(maps, N128(), N128(), std::false_type());
+      return f(maps, N256(), N256(), std::false_type());
+    }
+    if (dk <= 64 && a.dv <= 64) return f(maps, N64(), N64(), std::true_type());
+    if (dk <= 128 && a.dv <= 128) return f(maps, N128(), N128(), std::true_type());
+    return f(maps, N256(), N256(), std::true_type());
   };
   return a.maps() > 1 ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 1>());
 }

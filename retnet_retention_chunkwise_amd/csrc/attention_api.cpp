@@ -8,6 +8,7 @@ namespace {
 
 constexpr int kMaxLen = 1 << 30;               // tokens, and the offset's magnitude
 constexpr long long kMaxAttnRows = 1LL << 25;  // rows of q: a wave each, below 2^32 threads in all
+constexpr long kMaxTokenStride = 1L << 24;
 constexpr long long kMaxTiles = 1LL << 23;     // workgroups of 256 threads
 
 struct Sizes {
@@ -53,6 +54,14 @@ ret_status check_scores(const char* fn, float scale, int offset) {
     return fail(RET_ERR_INVALID_ARG, "%s: scale=%g must be finite and > 0", fn, static_cast<double>(scale));
   if (offset < -kMaxLen || offset > kMaxLen)
     return fail(RET_ERR_INVALID_ARG, "%s: offset=%d is beyond 2^30", fn, offset);
+  return RET_OK;
+}
+
+// Distances between tokens: a tile of 64 rows is addressed in 32 bits.
+ret_status check_token_strides(const char* fn, std::initializer_list<std::pair<const Strides3*, int>> all) {
+  for (const auto& x : all)
+    if (x.second > 1 && x.first->t > kMaxTokenStride)
+      return fail(RET_ERR_UNSUPPORTED, "%s: a distance of %ld elements between tokens exceeds 2^24", fn, x.first->t);
   return RET_OK;
 }
 
@@ -127,6 +136,9 @@ ret_status retention_attention_fwd(const void* q, const void* k, const void* v, 
   a.sk = given(strides, 1, contiguous_bhtd(Hk, S, dk));
   a.sv = given(strides, 2, contiguous_bhtd(Hk, S, dv));
   a.so = given(strides, 3, contiguous_bhtd(H, T, dv));
+  st = check_token_strides(fn, {{&a.sk, S}, {&a.sv, S}});
+  if (st != RET_OK) return st;
+  if (S <= 1) a.sk.t = a.sv.t = 0;  // not followed, but multiplied
   const size_t need = T == 0 ? 0 : ret::attention_fwd_workspace(a);
   const long long rows = static_cast<long long>(B) * H * T;
   st = check_args(fn, {seq("q", q, false, B, H, T, dk, a.sq, dt), seq("k", k, false, B, Hk, S, dk, a.sk, dt),
@@ -178,6 +190,10 @@ ret_status retention_attention_bwd(const void* q, const void* k, const void* v, 
   g.sdq = given(strides, 5, cq);
   g.sdk = given(strides, 6, ck);
   g.sdv = given(strides, 7, cv);
+  st = check_token_strides(fn, {{&a.sq, T}, {&g.sdo, T}, {&a.sk, S}, {&a.sv, S}});
+  if (st != RET_OK) return st;
+  if (T <= 1) a.sq.t = g.sdo.t = 0;  // not followed, but multiplied
+  if (S <= 1) a.sk.t = a.sv.t = 0;
   const size_t need = ret::attention_bwd_workspace(a);
   const long long rows = static_cast<long long>(B) * H * T;
   Arg two = seq("second", second, false, B, H, T, dv, co, dt);

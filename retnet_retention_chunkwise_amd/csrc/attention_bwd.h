@@ -26,7 +26,7 @@ namespace ret {
 namespace attn {
 
 // stats: [M][B*H*T] of {lse log2 e, D}: first all of map 1.
-template <typename E, int MAPS, int DK, int DV, int NB, int NW, int KT>
+template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int KT>
 __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, const float2* __restrict__ stats,
                                                                   float* __restrict__ lam_part, int tiles) {
   typedef Mma<E> X;
@@ -34,15 +34,15 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
   constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
   constexpr int KB = KT / 16, KS = D / 32, VS = DV / 32, CB = D / 16;
   constexpr int KLD = kTileLd<E, DK>, VLD = kTileLd<E, DV>;
-  __shared__ __attribute__((aligned(16))) E Ks[KT * KLD];
-  __shared__ __attribute__((aligned(16))) E Vs[KT * VLD];
+  __shared__ __attribute__((aligned(16))) E Kt[2][KT * KLD];
+  __shared__ __attribute__((aligned(16))) E Vt[2][KT * VLD];
   __shared__ float wave_lam[NW];
 
   const AttnFwd& a = g.f;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
-  const int id = blockIdx.x;
-  const int tile = tiles - 1 - id % tiles;  // the longest rows first
-  const int bh = id / tiles, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), col = lane & 15, grp = lane >> 4;
+  // the longest rows of all heads first, so that the last workgroups are short
+  const int heads = a.B * a.H, bh = blockIdx.x % heads, tile = tiles - 1 - blockIdx.x / heads;
+  const int b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
   const int len = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
   auto seen = [&](int t) { return a.causal ? min(max(t + a.offset + 1, 0), len) : len; };
   const int q0 = tile * QT, w0 = q0 + wave * 16 * NB;
@@ -61,8 +61,8 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
   for (int n = 0; n < NB; ++n) {
     const int t = w0 + 16 * n + col;
     const int row = min(t, a.T - 1);
-    load_columns<E, MAPS, D>(q + row * a.sq.t, t < a.T, a.d, lane, qf[n]);
-    load_columns<E, 1, DV>(dout + row * g.sdo.t, t < a.T, a.dv, lane, gf[n]);
+    load_columns<E, MAPS, D, kWhole>(q + row * a.sq.t, t < a.T, a.d, lane, qf[n]);
+    load_columns<E, 1, DV, kWhole>(dout + row * g.sdo.t, t < a.T, a.dv, lane, gf[n]);
     lim[n] = seen(t);
 #pragma unroll
     for (int m = 0; m < MAPS; ++m)
@@ -78,21 +78,30 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
       for (int n = 0; n < NB; ++n) dq[m][i][n] = f32x4{0, 0, 0, 0};
   float lam_sum = 0.0f;
 
-  Stage<E, KT, MAPS, D, THREADS> ks(a.d, tid);
-  Stage<E, KT, 1, DV, THREADS> vs(a.dv, tid);
+  Stage<E, KT, MAPS, D, THREADS, kWhole> ks(a.d, tid);
+  Stage<E, KT, 1, DV, THREADS, kWhole> vs(a.dv, tid);
+  // two tiles in LDS, as in the forward
   if (last > 0) {
     ks.load(k, a.sk.t, 0, len, a.d);
     vs.load(v, a.sv.t, 0, len, a.dv);
+    ks.store(Kt[0], KLD, 0, len);
+    vs.store(Vt[0], VLD, 0, len);
+    if (last > 1) {
+      ks.load(k, a.sk.t, KT, len, a.d);
+      vs.load(v, a.sv.t, KT, len, a.dv);
+    }
   }
   for (int i = 0; i < last; ++i) {
-    const int k0 = i * KT;
-    __syncthreads();
-    ks.store(Ks, KLD, k0, len, a.d);
-    vs.store(Vs, VLD, k0, len, a.dv);
-    __syncthreads();
+    const int k0 = i * KT, slot = i & 1;
+    const E *Ks = Kt[slot], *Vs = Vt[slot];
+    lds_barrier();
     if (i + 1 < last) {
-      ks.load(k, a.sk.t, k0 + KT, len, a.d);
-      vs.load(v, a.sv.t, k0 + KT, len, a.dv);
+      ks.store(Kt[slot ^ 1], KLD, k0 + KT, len);
+      vs.store(Vt[slot ^ 1], VLD, k0 + KT, len);
+      if (i + 2 < last) {
+        ks.load(k, a.sk.t, k0 + 2 * KT, len, a.d);
+        vs.load(v, a.sv.t, k0 + 2 * KT, len, a.dv);
+      }
     }
     if (k0 >= wmax) continue;
     f32x4 dp[KB][NB];
@@ -166,29 +175,30 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
     for (int m = 0; m < MAPS; ++m) {
       const float f = m == 0 ? a.scale : -a.lam[h] * a.scale;
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) store4<E>(out + m * a.d, 16 * cb + 4 * grp, a.d, dq[m][cb][n] * f);
+      for (int cb = 0; cb < CB; ++cb) store4<E, kWhole>(out + m * a.d, 16 * cb + 4 * grp, a.d, dq[m][cb][n] * f);
     }
   }
 }
 
-template <typename E, int MAPS, int DK, int DV, int NB, int NW, int QT>
+template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int QT>
 __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, const float2* __restrict__ stats,
-                                                                   int tiles) {
+                                                                      float* __restrict__ part, int shares) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
   constexpr int D = DK / MAPS, THREADS = 64 * NW, KT = 16 * NB * NW;
   constexpr int QB = QT / 16, KS = D / 32, VS = DV / 32, CB = D / 16, VB = DV / 16;
   constexpr int QLD = kTileLd<E, DK>, GLD = kTileLd<E, DV>;
-  __shared__ __attribute__((aligned(16))) E Qs[QT * QLD];
-  __shared__ __attribute__((aligned(16))) E Gs[QT * GLD];
-  __shared__ __attribute__((aligned(16))) float Ls[MAPS][QT], Ds[MAPS][QT];
+  constexpr bool kAhead = sizeof(E) == 2;
+  __shared__ __attribute__((aligned(16))) E Qt[2][QT * QLD];
+  __shared__ __attribute__((aligned(16))) E Gt[2][QT * GLD];
+  __shared__ __attribute__((aligned(16))) float Lt[2][MAPS][QT], Dt[2][MAPS][QT];
   static_assert(MAPS * QT <= THREADS, "a thread per row's statistics");
 
   const AttnFwd& a = g.f;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
-  const int id = blockIdx.x;
-  const int tile = id % tiles;  // the keys that most rows see first
-  const int bh = id / tiles, b = bh / a.Hk, hk = bh % a.Hk, G = a.H / a.Hk;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), col = lane & 15, grp = lane >> 4;
+  // the keys that most rows see first, of all heads and shares
+  const int heads = a.B * a.Hk, bh = blockIdx.x % heads, share = blockIdx.x / heads % shares, tile = blockIdx.x / heads / shares;
+  const int b = bh / a.Hk, hk = bh % a.Hk, G = a.H / a.Hk;
   const int len = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
   const int k0 = tile * KT, w0 = k0 + wave * 16 * NB;
   // the first row that sees a key
@@ -204,10 +214,9 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
   int lim[NB];
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    const int key = w0 + 16 * n + col;
-    const int row = min(key, a.S - 1);
-    load_columns<E, MAPS, D>(k + row * a.sk.t, key < len, a.d, lane, kf[n]);
-    load_columns<E, 1, DV>(v + row * a.sv.t, key < len, a.dv, lane, vf[n]);
+    const int key = w0 + 16 * n + col, row = min(key, a.S - 1);
+    load_columns<E, MAPS, D, kWhole>(k + row * a.sk.t, key < len, a.d, lane, kf[n]);
+    load_columns<E, 1, DV, kWhole>(v + row * a.sv.t, key < len, a.dv, lane, vf[n]);
     lim[n] = from(key);
   }
   const float c = a.scale * kLog2e;
@@ -222,8 +231,8 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
     for (int i = 0; i < VB; ++i) dv[i][n] = f32x4{0, 0, 0, 0};
   }
 
-  Stage<E, QT, MAPS, D, THREADS> qs(a.d, tid);
-  Stage<E, QT, 1, DV, THREADS> gs(a.dv, tid);
+  Stage<E, QT, MAPS, D, THREADS, kWhole> qs(a.d, tid);
+  Stage<E, QT, 1, DV, THREADS, kWhole> gs(a.dv, tid);
   float2 st;
   auto load = [&](int i) {
     const int h = hk * G + i / n_tiles, row0 = t0 + i % n_tiles * QT;
@@ -234,85 +243,194 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
       st = t < a.T ? stats[tid / QT * rows + (static_cast<long>(b) * a.H + h) * a.T + t] : make_float2(INFINITY, 0.0f);
     }
   };
-  const int n_all = G * n_tiles;
-  if (n_all > 0) load(0);
-  for (int i = 0; i < n_all; ++i) {
-    const int row0 = t0 + i % n_tiles * QT;
-    __syncthreads();
-    qs.store(Qs, QLD, row0, a.T, a.d);
-    gs.store(Gs, GLD, row0, a.T, a.dv);
+  auto store = [&](int i) {
+    const int row0 = t0 + i % n_tiles * QT, slot = i & 1;
+    qs.store(Qt[slot], QLD, row0, a.T);
+    gs.store(Gt[slot], GLD, row0, a.T);
     if (tid < MAPS * QT) {
-      Ls[tid / QT][tid % QT] = st.x;
-      Ds[tid / QT][tid % QT] = st.y;
+      Lt[slot][tid / QT][tid % QT] = st.x;
+      Dt[slot][tid / QT][tid % QT] = st.y;
     }
-    __syncthreads();
-    if (i + 1 < n_all) load(i + 1);
+  };
+  // this workgroup's share of the heads' tiles
+  const int n_all = G * n_tiles;
+  const int first = static_cast<int>(static_cast<long>(n_all) * share / shares);
+  const int last = static_cast<int>(static_cast<long>(n_all) * (share + 1) / shares);
+  if (first < last) {
+    load(first);
+    store(first);
+    if (first + 1 < last) load(first + 1);
+  }
+  for (int i = first; i < last; ++i) {
+    const int row0 = t0 + i % n_tiles * QT, slot = i & 1;
+    const E *Qs = Qt[slot], *Gs = Gt[slot];
+    const float(*Ls)[QT] = Lt[slot], (*Ds)[QT] = Dt[slot];
+    lds_barrier();
+    if (i + 1 < last) {
+      store(i + 1);
+      if (i + 2 < last) load(i + 2);
+    }
     if (row0 + QT <= wfirst) continue;
     const float lam = MAPS > 1 ? a.lam[hk * G + i / n_tiles] : 0.0f;
-    const bool edge = row0 < wall;
-    f32x4 dp[QB][NB], pv[QB][NB];
+    Frag ga[QB][VS], qa[MAPS][QB][KS], qc[MAPS][QT / 32][CB];
+    f32x4 dp[QB][NB], s[MAPS][QB][NB], pv[QB][NB];
+    // an operand that was read a stage ahead; fp32 ones, twice as large, are read when they are used
+    auto get = [](const Frag& ahead, auto&& now) {
+      if constexpr (kAhead) return ahead;
+      else return now();
+    };
+    auto read_q = [&](int m) {
+      if constexpr (!kAhead) return;
 #pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
+      for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-      for (int n = 0; n < NB; ++n) dp[qb][n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < VS; ++e) {
-        const Frag x = rows_frag<E>(Gs, GLD, 16 * qb, 32 * e, lane);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) dp[qb][n] = X::mma(x, vf[n][e], dp[qb][n]);
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < MAPS; ++m) {
-      f32x4 s[QB][NB];
+        for (int e = 0; e < KS; ++e) qa[m][qb][e] = rows_frag<E>(Qs, QLD, 16 * qb, m * D + 32 * e, lane);
+    };
+    auto scores = [&](int m) {
 #pragma unroll
       for (int qb = 0; qb < QB; ++qb) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n) s[qb][n] = f32x4{0, 0, 0, 0};
+        for (int n = 0; n < NB; ++n) s[m][qb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < KS; ++e) {
-          const Frag x = rows_frag<E>(Qs, QLD, 16 * qb, m * D + 32 * e, lane);
+        for (int e = 0; e < KS; ++e)
 #pragma unroll
-          for (int n = 0; n < NB; ++n) s[qb][n] = X::mma(x, kf[n][m * KS + e], s[qb][n]);
-        }
+          for (int n = 0; n < NB; ++n)
+            s[m][qb][n] = X::mma(get(qa[m][qb][e], [&] { return rows_frag<E>(Qs, QLD, 16 * qb, m * D + 32 * e, lane); }),
+                                 kf[n][m * KS + e], s[m][qb][n]);
+      }
+    };
+    auto mask = [&]() {
+      if (row0 < wall) {  // some row does not see some key
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const bool out = row0 + 16 * qb + 4 * grp + r < lim[n];
+#pragma unroll
+              for (int m = 0; m < MAPS; ++m)
+                if (out) s[m][qb][n][r] = -INFINITY;
+            }
+      }
+    };
+    auto read_qt = [&](int m) {
+      if constexpr (!kAhead) return;
+#pragma unroll
+      for (int j = 0; j < QT / 32; ++j)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) qc[m][j][cb] = cols_frag<E>(Qs, QLD, 32 * j, m * D + 16 * cb, lane);
+    };
+    // p and ds of a map in place of its scores; pv collects p_1 - lam p_2
+    auto weigh = [&](int m) {
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb) {
         const f32x4 l4 = *reinterpret_cast<const f32x4*>(&Ls[m][16 * qb + 4 * grp]);
         const f32x4 d4 = *reinterpret_cast<const f32x4*>(&Ds[m][16 * qb + 4 * grp]);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            float p = fast_exp2(fmaf(s[qb][n][r], c, -l4[r]));
-            if (edge && row0 + 16 * qb + 4 * grp + r < lim[n]) p = 0.0f;
+            float p = fast_exp2(fmaf(s[m][qb][n][r], c, -l4[r]));
             if (m == 1) p *= -lam;
             pv[qb][n][r] = m == 0 ? p : pv[qb][n][r] + p;
-            s[qb][n][r] = p * (dp[qb][n][r] - d4[r]);
+            s[m][qb][n][r] = p * (dp[qb][n][r] - d4[r]);
           }
       }
+    };
+    auto add_k = [&](int m) {
 #pragma unroll
       for (int j = 0; j < QT / 32; ++j) {
         Frag ds[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[2 * j][n], s[2 * j + 1][n]);
+        for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[m][2 * j][n], s[m][2 * j + 1][n]);
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          const Frag x = cols_frag<E>(Qs, QLD, 32 * j, m * D + 16 * cb, lane);
+        for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-          for (int n = 0; n < NB; ++n) dk[m][cb][n] = X::mma(x, ds[n], dk[m][cb][n]);
-        }
+          for (int n = 0; n < NB; ++n) 
+            dk[m][cb][n] = X::mma(get(qc[m][j][cb], [&] { return cols_frag<E>(Qs, QLD, 32 * j, m * D + 16 * cb, lane); }),
+                                  ds[n], dk[m][cb][n]);
       }
+    };
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+        for (int e = 0; e < VS; ++e) ga[qb][e] = rows_frag<E>(Gs, GLD, 16 * qb, 32 * e, lane);
     }
+    read_q(0);
+    stage_border<E>();
+    products_first();
 #pragma unroll
-    for (int j = 0; j < QT / 32; ++j) {
-      Frag p[NB];
+    for (int qb = 0; qb < QB; ++qb) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) p[n] = X::pack(pv[2 * j][n], pv[2 * j + 1][n]);
+      for (int n = 0; n < NB; ++n) dp[qb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int vb = 0; vb < VB; ++vb) {
-        const Frag x = cols_frag<E>(Gs, GLD, 32 * j, 16 * vb, lane);
+      for (int e = 0; e < VS; ++e)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) dv[vb][n] = X::mma(x, p[n], dv[vb][n]);
-      }
+        for (int n = 0; n < NB; ++n)
+          dp[qb][n] = X::mma(get(ga[qb][e], [&] { return rows_frag<E>(Gs, GLD, 16 * qb, 32 * e, lane); }), vf[n][e], dp[qb][n]);
     }
+    stage_border<E>();
+    if constexpr (MAPS > 1) read_q(1);
+    else read_qt(0);
+    stage_border<E>();
+    scores(0);
+    stage_border<E>();
+    if constexpr (MAPS > 1) {
+      read_qt(0);
+      stage_border<E>();
+      scores(1);
+      products_done();
+      mask();
+      weigh(0);
+      stage_border<E>();
+      read_qt(1);
+      stage_border<E>();
+      products_first();
+      add_k(0);
+      products_done();
+      weigh(1);
+    } else {
+      products_done();
+      mask();
+      weigh(0);
+    }
+    stage_border<E>();
+    constexpr int VG = VB < 4 ? VB : 4;  // blocks of values of a stage
+    Frag gc[2][QT / 32][VG];
+    auto read_gt = [&](int v0) {
+      if constexpr (!kAhead) return;
+#pragma unroll
+      for (int j = 0; j < QT / 32; ++j)
+#pragma unroll
+        for (int vb = 0; vb < VG; ++vb) gc[v0 / VG & 1][j][vb] = cols_frag<E>(Gs, GLD, 32 * j, 16 * (v0 + vb), lane);
+    };
+    read_gt(0);
+    stage_border<E>();
+    products_first();
+    add_k(MAPS - 1);
+    Frag pf[QT / 32][NB];
+#pragma unroll
+    for (int j = 0; j < QT / 32; ++j)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) pf[j][n] = X::pack(pv[2 * j][n], pv[2 * j + 1][n]);
+#pragma unroll
+    for (int v0 = 0; v0 < VB; v0 += VG) {
+      stage_border<E>();
+      if (v0 + VG < VB) read_gt(v0 + VG);
+      stage_border<E>();
+#pragma unroll
+      for (int j = 0; j < QT / 32; ++j)
+#pragma unroll
+        for (int vb = 0; vb < VG; ++vb)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+            dv[v0 + vb][n] = X::mma(
+                get(gc[v0 / VG & 1][j][vb], [&] { return cols_frag<E>(Gs, GLD, 32 * j, 16 * (v0 + vb), lane); }), pf[j][n],
+                dv[v0 + vb][n]);
+    }
+    products_done();
   }
 
 #pragma unroll
@@ -320,19 +438,35 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
     const int key = w0 + 16 * n + col;
     if (key >= a.S) continue;
     const bool in = key < len;  // keys behind the sequence have no gradient
+    const f32x4 zero = {0, 0, 0, 0};
+    if (shares > 1) {  // fp32 sums of the share, [share][b, hk, key][dk4 + dv4]
+      const int d4 = (a.d + 3) & ~3, dv4 = (a.dv + 3) & ~3;
+      float* to = part + (share * static_cast<long>(heads) * a.S + static_cast<long>(bh) * a.S + key) * (MAPS * d4 + dv4);
+#pragma unroll
+      for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          store4<float, true>(to + m * d4, 16 * cb + 4 * grp, d4, in ? dk[m][cb][n] : zero);
+#pragma unroll
+      for (int vb = 0; vb < VB; ++vb) store4<float, true>(to + MAPS * d4, 16 * vb + 4 * grp, dv4, in ? dv[vb][n] : zero);
+      continue;
+    }
     E* ok = static_cast<E*>(g.grad_k) + b * g.sdk.b + hk * g.sdk.h + key * g.sdk.t;
     E* ov = static_cast<E*>(g.grad_v) + b * g.sdv.b + hk * g.sdv.h + key * g.sdv.t;
-    const f32x4 zero = {0, 0, 0, 0};
 #pragma unroll
     for (int m = 0; m < MAPS; ++m)
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb)
-        store4<E>(ok + m * a.d, 16 * cb + 4 * grp, a.d, in ? dk[m][cb][n] * a.scale : zero);
+        store4<E, kWhole>(ok + m * a.d, 16 * cb + 4 * grp, a.d, in ? dk[m][cb][n] * a.scale : zero);
 #pragma unroll
-    for (int vb = 0; vb < VB; ++vb) store4<E>(ov, 16 * vb + 4 * grp, a.dv, in ? dv[vb][n] : zero);
+    for (int vb = 0; vb < VB; ++vb) store4<E, kWhole>(ov, 16 * vb + 4 * grp, a.dv, in ? dv[vb][n] : zero);
   }
 }
 
+template <typename E, int DK>
+struct KvShape {
+  static constexpr int NB = 1, NW = 4, TILE = 16 * NB * NW, STREAM = 32;
+};
 template <typename E, int DK>
 struct BwdShape {
   static constexpr int NB = sizeof(E) == 2 && DK <= 128 ? 2 : 1;
@@ -340,17 +474,22 @@ struct BwdShape {
 };
 
 template <typename E>
-int bwd_q_rows(const AttnFwd& a) {
-  return with_sizes(a, [](auto, auto dk, auto) { return BwdShape<E, decltype(dk)::value>::TILE; });
+int bwd_keys(const AttnFwd& a) {
+  return with_sizes(a, [](auto, auto dk, auto, auto) { return KvShape<E, decltype(dk)::value>::TILE; });
+}
+template <typename E>
+int bwd_rows(const AttnFwd& a) {
+  return with_sizes(a, [](auto, auto dk, auto, auto) { return BwdShape<E, decltype(dk)::value>::TILE; });
 }
 
 template <typename E>
 hipError_t launch_bwd_q(const AttnBwd& a, const float* stats, float* lam_part, hipStream_t s) {
-  return with_sizes(a.f, [&](auto m, auto dk, auto dv) {
+  return with_sizes(a.f, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
+    constexpr bool W = decltype(whole)::value;
     typedef BwdShape<E, DK> C;
     const int tiles = (a.f.T + C::TILE - 1) / C::TILE;
-    hipLaunchKernelGGL((attention_bwd_q_kernel<E, M, DK, DV, C::NB, C::NW, C::STREAM>),
+    hipLaunchKernelGGL((attention_bwd_q_kernel<E, M, DK, DV, W, C::NB, C::NW, C::STREAM>),
                        dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.H), dim3(64 * C::NW), 0, s, a,
                        reinterpret_cast<const float2*>(stats), lam_part, tiles);
     return hipGetLastError();
@@ -358,14 +497,15 @@ hipError_t launch_bwd_q(const AttnBwd& a, const float* stats, float* lam_part, h
 }
 
 template <typename E>
-hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, hipStream_t s) {
-  return with_sizes(a.f, [&](auto m, auto dk, auto dv) {
+hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, float* part, int shares, hipStream_t s) {
+  return with_sizes(a.f, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
-    typedef BwdShape<E, DK> C;
+    constexpr bool W = decltype(whole)::value;
+    typedef KvShape<E, DK> C;
     const int tiles = (a.f.S + C::TILE - 1) / C::TILE;
-    hipLaunchKernelGGL((attention_bwd_kv_kernel<E, M, DK, DV, C::NB, C::NW, C::STREAM>),
-                       dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.Hk), dim3(64 * C::NW), 0, s, a,
-                       reinterpret_cast<const float2*>(stats), tiles);
+    hipLaunchKernelGGL((attention_bwd_kv_kernel<E, M, DK, DV, W, C::NB, C::NW, C::STREAM>),
+                       dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.Hk * shares), dim3(64 * C::NW), 0, s, a,
+                       reinterpret_cast<const float2*>(stats), part, shares);
     return hipGetLastError();
   });
 }

@@ -25,20 +25,20 @@ namespace attn {
 
 constexpr float kSlack = 8.0f;
 
-template <typename E, int MAPS, int DK, int DV, int NB, int NW, int KT>
+template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int KT>
 __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Partial part, int tiles) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
   constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
   constexpr int KB = KT / 16, KS = D / 32, VB = DV / 16;
   constexpr int KLD = kTileLd<E, DK>, VLD = kTileLd<E, DV>;
-  __shared__ __attribute__((aligned(16))) E Ks[KT * KLD];
-  __shared__ __attribute__((aligned(16))) E Vs[KT * VLD];
+  __shared__ __attribute__((aligned(16))) E Kt[2][KT * KLD];
+  __shared__ __attribute__((aligned(16))) E Vt[2][KT * VLD];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
-  const int id = blockIdx.x;
-  const int tile = tiles - 1 - id % tiles;  // the longest rows first
-  const int bh = id / tiles, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), col = lane & 15, grp = lane >> 4;
+  // the longest rows of all heads first, so that the last workgroups are short
+  const int heads = a.B * a.H, bh = blockIdx.x % heads, tile = tiles - 1 - blockIdx.x / heads;
+  const int b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
   const int split = blockIdx.y;
   const int len = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
   // keys that a row t sees
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Parti
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const int t = w0 + 16 * n + col;
-    load_columns<E, MAPS, D>(q + min(t, a.T - 1) * a.sq.t, t < a.T, a.d, lane, qf[n]);
+    load_columns<E, MAPS, D, kWhole>(q + min(t, a.T - 1) * a.sq.t, t < a.T, a.d, lane, qf[n]);
     lim[n] = seen(t);
   }
 
@@ -76,75 +76,107 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Parti
       for (int i = 0; i < VB; ++i) o[m][i][n] = f32x4{0, 0, 0, 0};
     }
 
-  Stage<E, KT, MAPS, D, THREADS> ks(a.d, tid);
-  Stage<E, KT, 1, DV, THREADS> vs(a.dv, tid);
+  Stage<E, KT, MAPS, D, THREADS, kWhole> ks(a.d, tid);
+  Stage<E, KT, 1, DV, THREADS, kWhole> vs(a.dv, tid);
+  // Two tiles in LDS: while one is used the next is written (its loads were sent
+  // a tile earlier) and the one after is on its way; one barrier a tile.
   if (first < last) {
     ks.load(k, a.sk.t, first * KT, len, a.d);
     vs.load(v, a.sv.t, first * KT, len, a.dv);
+    ks.store(Kt[0], KLD, first * KT, len);
+    vs.store(Vt[0], VLD, first * KT, len);
+    if (first + 1 < last) {
+      ks.load(k, a.sk.t, (first + 1) * KT, len, a.d);
+      vs.load(v, a.sv.t, (first + 1) * KT, len, a.dv);
+    }
   }
   for (int i = first; i < last; ++i) {
-    const int k0 = i * KT;
-    __syncthreads();
-    ks.store(Ks, KLD, k0, len, a.d);
-    vs.store(Vs, VLD, k0, len, a.dv);
-    __syncthreads();
+    const int k0 = i * KT, slot = (i - first) & 1;
+    const E *Ks = Kt[slot], *Vs = Vt[slot];
+    lds_barrier();
     if (i + 1 < last) {
-      ks.load(k, a.sk.t, k0 + KT, len, a.d);
-      vs.load(v, a.sv.t, k0 + KT, len, a.dv);
+      ks.store(Kt[slot ^ 1], KLD, k0 + KT, len);
+      vs.store(Vt[slot ^ 1], VLD, k0 + KT, len);
+      if (i + 2 < last) {
+        ks.load(k, a.sk.t, k0 + 2 * KT, len, a.d);
+        vs.load(v, a.sv.t, k0 + 2 * KT, len, a.dv);
+      }
     }
     if (k0 >= wmax) continue;
-    Frag pf[MAPS][NB][KT / 32];
+    products_first();
+    f32x4 s[MAPS][KB][NB];
 #pragma unroll
-    for (int m = 0; m < MAPS; ++m) {
-      f32x4 s[KB][NB];
+    for (int m = 0; m < MAPS; ++m)
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
+        Frag kf[KS];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) s[kb][n] = f32x4{0, 0, 0, 0};
+        for (int e = 0; e < KS; ++e) kf[e] = rows_frag<E>(Ks, KLD, 16 * kb, m * D + 32 * e, lane);
 #pragma unroll
-        for (int e = 0; e < KS; ++e) {
-          const Frag kf = rows_frag<E>(Ks, KLD, 16 * kb, m * D + 32 * e, lane);
+        for (int n = 0; n < NB; ++n) s[m][kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int n = 0; n < NB; ++n) s[kb][n] = X::mma(kf, qf[n][m * KS + e], s[kb][n]);
-        }
+        for (int e = 0; e < KS; ++e)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) s[m][kb][n] = X::mma(kf[e], qf[n][m * KS + e], s[m][kb][n]);
       }
-      if (k0 + KT > wall) {  // some row does not see some key
+    products_done();
+    if (k0 + KT > wall) {  // some row does not see some key
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (k0 + 16 * kb + 4 * grp + r >= lim[n]) s[kb][n][r] = -INFINITY;
-      }
+          for (int r = 0; r < 4; ++r) {
+            const bool out = k0 + 16 * kb + 4 * grp + r >= lim[n];
+#pragma unroll
+            for (int m = 0; m < MAPS; ++m)
+              if (out) s[m][kb][n][r] = -INFINITY;
+          }
+    }
+    float top[MAPS][NB];
+    bool over = false;
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m)
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        float top = -INFINITY;
+        top[m][n] = -INFINITY;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) top = fmaxf(top, s[kb][n][r]);
-        if (__any(top > mx[m][n] + slack)) {
-          const float next = fmaxf(mx[m][n], row4_max(top));
+          for (int r = 0; r < 4; ++r) top[m][n] = fmaxf(top[m][n], s[m][kb][n][r]);
+        over = over || top[m][n] > mx[m][n] + slack;
+      }
+    if (__any(over)) {
+#pragma unroll
+      for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const float next = fmaxf(mx[m][n], row4_max(top[m][n]));
           const float f = next == -INFINITY ? 1.0f : fast_exp2((mx[m][n] - next) * c);
           mx[m][n] = next;
           sum[m][n] *= f;
 #pragma unroll
           for (int j = 0; j < VB; ++j) o[m][j][n] *= f;
         }
+    }
+    Frag pf[MAPS][NB][KT / 32];
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
         const float mc = mx[m][n] == -INFINITY ? 0.0f : mx[m][n] * c;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float p = fast_exp2(fmaf(s[kb][n][r], c, -mc));
-            s[kb][n][r] = p;
+            const float p = fast_exp2(fmaf(s[m][kb][n][r], c, -mc));
+            s[m][kb][n][r] = p;
             sum[m][n] += p;
           }
 #pragma unroll
-        for (int j = 0; j < KT / 32; ++j) pf[m][n][j] = X::pack(s[2 * j][n], s[2 * j + 1][n]);
+        for (int j = 0; j < KT / 32; ++j) pf[m][n][j] = X::pack(s[m][2 * j][n], s[m][2 * j + 1][n]);
       }
-    }
+    products_first();
 #pragma unroll
     for (int j = 0; j < KT / 32; ++j)
 #pragma unroll
@@ -155,6 +187,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Parti
 #pragma unroll
           for (int n = 0; n < NB; ++n) o[m][vb][n] = X::mma(vf, pf[m][n][j], o[m][vb][n]);
       }
+    products_done();
   }
 
   const float lam = MAPS > 1 ? a.lam[h] : 0.0f;
@@ -199,9 +232,9 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Parti
       if constexpr (MAPS > 1) {
         const f32x4 z = o[1][vb][n] * inv[1];
         y -= lam * z;
-        if (a.second != nullptr) store4<E>(two, 16 * vb + 4 * grp, a.dv, z);
+        if (a.second != nullptr) store4<E, kWhole>(two, 16 * vb + 4 * grp, a.dv, z);
       }
-      store4<E>(out, 16 * vb + 4 * grp, a.dv, y);
+      store4<E, kWhole>(out, 16 * vb + 4 * grp, a.dv, y);
     }
   }
 }
@@ -225,18 +258,19 @@ struct FwdShape {
 // Rows of a tile, for the sizes that hold the call's.
 template <typename E>
 int fwd_rows(const AttnFwd& a) {
-  return with_sizes(a, [](auto m, auto dk, auto dv) {
+  return with_sizes(a, [](auto m, auto dk, auto dv, auto) {
     return FwdShape<E, decltype(m)::value, decltype(dk)::value, decltype(dv)::value>::QT;
   });
 }
 
 template <typename E>
 hipError_t launch_fwd(const AttnFwd& a, const Partial& part, hipStream_t s) {
-  return with_sizes(a, [&](auto m, auto dk, auto dv) {
+  return with_sizes(a, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
+    constexpr bool W = decltype(whole)::value;
     typedef FwdShape<E, M, DK, DV> C;
     const int tiles = (a.T + C::QT - 1) / C::QT;
-    hipLaunchKernelGGL((attention_fwd_kernel<E, M, DK, DV, C::NB, C::NW, C::KT>),
+    hipLaunchKernelGGL((attention_fwd_kernel<E, M, DK, DV, W, C::NB, C::NW, C::KT>),
                        dim3(static_cast<unsigned>(tiles) * a.B * a.H, part.nsplit), dim3(64 * C::NW), 0, s, a, part,
                        tiles);
     return hipGetLastError();

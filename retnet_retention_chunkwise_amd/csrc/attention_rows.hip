@@ -11,92 +11,179 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// One wave per row, four channels a lane.  The shares' outputs o_i with maxima
-// m_i and sums l_i join as sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.
+// Four elements of a row from c on, zeros from n on.
+template <typename E>
+__device__ __forceinline__ f32x4 load4(const E* row, int c, int n) {
+  f32x4 x = {0, 0, 0, 0};
+  if (n % 4 == 0) {
+    if (c < n) {
+      float y[4];
+      VecIO<E, 4>::unpack(VecIO<E, 4>::load(row + c), y);
+      x = f32x4{y[0], y[1], y[2], y[3]};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < n) x[i] = Elem<E>::load(row, c + i);
+  }
+  return x;
+}
+template <typename E>
+__device__ __forceinline__ void put4(E* row, int c, int n, f32x4 x) {
+  if (n % 4 == 0)
+    store4<E, true>(row, c, n, x);
+  else
+    store4<E, false>(row, c, n, x);
+}
+
+// A workgroup per row; lanes along the channels, four each, and waves along the
+// shares.  The shares' outputs o_i with maxima m_i and sums l_i join as
+// sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i, the waves' sums in wave order.
 template <typename E, int MAPS>
 __global__ __launch_bounds__(64 * kWaves) void attention_join_kernel(AttnFwd a, Partial p, long rows) {
-  const int lane = threadIdx.x & 63, ch = 4 * lane;
-  const long row = static_cast<long>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
-  if (row >= rows) return;
+  __shared__ float tops[kWaves][MAPS], sums[kWaves][MAPS];
+  __shared__ f32x4 outs[kWaves][MAPS][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = 4 * lane;
+  const long row = blockIdx.x;
   const int t = static_cast<int>(row % a.T), dv4 = (a.dv + 3) & ~3;
   const long bh = row / a.T;
   const int h = static_cast<int>(bh % a.H), b = static_cast<int>(bh / a.H);
   const float2* ml = reinterpret_cast<const float2*>(p.ml);
-  f32x4 y[MAPS];
+  // this wave's shares: wave, wave + kWaves, ..., one maximum a lane to begin with
 #pragma unroll
   for (int m = 0; m < MAPS; ++m) {
     float top = -INFINITY;
-    for (int i = 0; i < p.nsplit; ++i) top = fmaxf(top, ml[(i * rows + row) * MAPS + m].x);
+    for (int i = wave + kWaves * lane; i < p.nsplit; i += kWaves * 64) top = fmaxf(top, ml[(i * rows + row) * MAPS + m].x);
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
     const float at = top == -INFINITY ? 0.0f : top;
     float l = 0.0f;
     f32x4 x = {0, 0, 0, 0};
-    for (int i = 0; i < p.nsplit; ++i) {
+#pragma unroll 4
+    for (int i = wave; i < p.nsplit; i += kWaves) {
       const long j = (i * rows + row) * MAPS + m;
       const float2 s = ml[j];
-      if (s.x == -INFINITY) continue;  // a share without keys wrote no outputs
+      f32x4 y = {0, 0, 0, 0};
+      if (ch < dv4) y = *reinterpret_cast<const f32x4*>(p.out + j * dv4 + ch);
       const float f = fast_exp2(s.x - at);
       l = fmaf(s.y, f, l);
-      if (ch < dv4) x += *reinterpret_cast<const f32x4*>(p.out + j * dv4 + ch) * f;
+      x += y * f;
     }
-    y[m] = x * (l == 0.0f ? 0.0f : 1.0f / l);
+    if (lane == 0) {
+      tops[wave][m] = top;
+      sums[wave][m] = l;
+    }
+    outs[wave][m][lane] = x;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  f32x4 y[MAPS];
+#pragma unroll
+  for (int m = 0; m < MAPS; ++m) {
+    float top = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][m]);
+    y[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = tops[w][m] == -INFINITY ? 0.0f : fast_exp2(tops[w][m] - top);
+      l = fmaf(sums[w][m], f, l);
+      y[m] += outs[w][m][lane] * f;
+    }
+    y[m] *= l == 0.0f ? 0.0f : 1.0f / l;
     if (a.lse != nullptr && lane == 0)
       a.lse[(bh * MAPS + m) * a.T + t] = l == 0.0f ? -INFINITY : top * kLn2 + logf(l);
   }
   if constexpr (MAPS > 1) {
-    if (a.second != nullptr) store4<E>(static_cast<E*>(a.second) + row * a.dv, ch, a.dv, y[1]);
+    if (a.second != nullptr) put4<E>(static_cast<E*>(a.second) + row * a.dv, ch, a.dv, y[1]);
     y[0] -= a.lam[h] * y[1];
   }
-  store4<E>(static_cast<E*>(a.o) + b * a.so.b + h * a.so.h + t * a.so.t, ch, a.dv, y[0]);
+  put4<E>(static_cast<E*>(a.o) + b * a.so.b + h * a.so.h + t * a.so.t, ch, a.dv, y[0]);
 }
 
-// {lse log2 e, D} of every row and map, one wave per row.  A row that saw no key
-// gets +inf, so that exp2(score - lse) is zero there.
-template <typename E, int MAPS>
+// {lse log2 e, D} of every row and map, LPR lanes per row, four channels a lane.
+// A row that saw no key gets +inf, so that exp2(score - lse) is zero there.
+template <typename E, int MAPS, int LPR>
 __global__ __launch_bounds__(64 * kWaves) void attention_stats_kernel(AttnBwd g, float2* stats, long rows) {
   const AttnFwd& a = g.f;
-  const int lane = threadIdx.x & 63, ch = 4 * lane;
-  const long row = static_cast<long>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
-  if (row >= rows) return;
+  const int lane = threadIdx.x % LPR, ch = 4 * lane;
+  const long at = (static_cast<long>(blockIdx.x) * kWaves * 64 + threadIdx.x) / LPR;
+  const long row = at < rows ? at : rows - 1;
   const int t = static_cast<int>(row % a.T);
   const long bh = row / a.T;
   const int h = static_cast<int>(bh % a.H), b = static_cast<int>(bh / a.H);
-  const E* o = static_cast<const E*>(a.o) + b * a.so.b + h * a.so.h + t * a.so.t;
-  const E* d = static_cast<const E*>(g.grad_o) + b * g.sdo.b + h * g.sdo.h + t * g.sdo.t;
-  const E* z = static_cast<const E*>(a.second) + row * a.dv;
-  float s[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (ch + i < a.dv) {
-      const float x = Elem<E>::load(d, ch + i);
-      s[0] = fmaf(x, Elem<E>::load(o, ch + i), s[0]);
-      if constexpr (MAPS > 1) s[1] = fmaf(x, Elem<E>::load(z, ch + i), s[1]);
-    }
-  s[0] = lanes_sum<64>(s[0]);
+  const f32x4 d = load4<E>(static_cast<const E*>(g.grad_o) + b * g.sdo.b + h * g.sdo.h + t * g.sdo.t, ch, a.dv);
+  const f32x4 o = load4<E>(static_cast<const E*>(a.o) + b * a.so.b + h * a.so.h + t * a.so.t, ch, a.dv);
+  float s[2];
+  s[0] = d[0] * o[0] + d[1] * o[1] + d[2] * o[2] + d[3] * o[3];
+  s[0] = lanes_sum<LPR>(s[0]);
   if constexpr (MAPS > 1) {
-    s[1] = lanes_sum<64>(s[1]);
+    const f32x4 z = load4<E>(static_cast<const E*>(a.second) + row * a.dv, ch, a.dv);
+    s[1] = d[0] * z[0] + d[1] * z[1] + d[2] * z[2] + d[3] * z[3];
+    s[1] = lanes_sum<LPR>(s[1]);
     s[0] = fmaf(a.lam[h], s[1], s[0]);
   }
-  if (lane < MAPS) {
+  if (lane < MAPS && at < rows) {
     const float l = a.lse[(bh * MAPS + lane) * a.T + t];
     stats[lane * rows + row] = make_float2(l == -INFINITY ? INFINITY : l * kLog2e, lane == 0 ? s[0] : s[1]);
   }
 }
 
-unsigned row_blocks(long rows) { return static_cast<unsigned>((rows + kWaves - 1) / kWaves); }
+// grad_k and grad_v from the shares' sums [share][row][MAPS d4 + dv4], added in
+// share order: a thread per four channels of a row (b, hk, key).
+template <typename E, int MAPS>
+__global__ __launch_bounds__(64 * kWaves) void attention_add_kernel(AttnBwd g, const float* __restrict__ part, int shares,
+                                                                    long rows) {
+  const AttnFwd& a = g.f;
+  const int d4 = (a.d + 3) & ~3, dv4 = (a.dv + 3) & ~3, width = MAPS * d4 + dv4, per = width / 4;
+  const long at = static_cast<long>(blockIdx.x) * (64 * kWaves) + threadIdx.x, row = at / per;
+  if (row >= rows) return;
+  const int c = 4 * static_cast<int>(at % per);
+  f32x4 x = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int i = 0; i < shares; ++i) x += *reinterpret_cast<const f32x4*>(part + (i * rows + row) * width + c);
+  const int key = static_cast<int>(row % a.S);
+  const long bh = row / a.S;
+  const int hk = static_cast<int>(bh % a.Hk), b = static_cast<int>(bh / a.Hk);
+  if (c < MAPS * d4) {
+    const int m = MAPS > 1 && c >= d4;
+    put4<E>(static_cast<E*>(g.grad_k) + b * g.sdk.b + hk * g.sdk.h + key * g.sdk.t + m * a.d, c - m * d4, a.d, x * a.scale);
+  } else {
+    put4<E>(static_cast<E*>(g.grad_v) + b * g.sdv.b + hk * g.sdv.h + key * g.sdv.t, c - MAPS * d4, a.dv, x);
+  }
+}
+
+int kv_width(const AttnFwd& a) { return a.maps() * ((a.d + 3) & ~3) + ((a.dv + 3) & ~3); }
 
 template <typename E>
-hipError_t stats(const AttnBwd& g, float* to, hipStream_t s) {
-  const long rows = static_cast<long>(g.f.B) * g.f.H * g.f.T;
-  auto* kern = g.f.maps() > 1 ? attention_stats_kernel<E, 2> : attention_stats_kernel<E, 1>;
-  hipLaunchKernelGGL(kern, dim3(row_blocks(rows)), dim3(64 * kWaves), 0, s, g, reinterpret_cast<float2*>(to), rows);
+hipError_t add(const AttnBwd& g, const float* part, int shares, hipStream_t s) {
+  const long rows = static_cast<long>(g.f.B) * g.f.Hk * g.f.S, n = rows * (kv_width(g.f) / 4);
+  auto* kern = g.f.maps() > 1 ? attention_add_kernel<E, 2> : attention_add_kernel<E, 1>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((n + 64 * kWaves - 1) / (64 * kWaves))), dim3(64 * kWaves), 0, s, g,
+                     part, shares, rows);
   return hipGetLastError();
+}
+
+template <typename E, int LPR>
+hipError_t stats_by_width(const AttnBwd& g, float* to, hipStream_t s) {
+  const long rows = static_cast<long>(g.f.B) * g.f.H * g.f.T, per = 64 * kWaves / LPR;
+  auto* kern = g.f.maps() > 1 ? attention_stats_kernel<E, 2, LPR> : attention_stats_kernel<E, 1, LPR>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(64 * kWaves), 0, s, g,
+                     reinterpret_cast<float2*>(to), rows);
+  return hipGetLastError();
+}
+template <typename E>
+hipError_t stats(const AttnBwd& g, float* to, hipStream_t s) {
+  if (g.f.dv <= 64) return stats_by_width<E, 16>(g, to, s);
+  if (g.f.dv <= 128) return stats_by_width<E, 32>(g, to, s);
+  return stats_by_width<E, 64>(g, to, s);
 }
 
 template <typename E>
 hipError_t join(const AttnFwd& a, const Partial& p, hipStream_t s) {
   const long rows = static_cast<long>(a.B) * a.H * a.T;
   auto* kern = a.maps() > 1 ? attention_join_kernel<E, 2> : attention_join_kernel<E, 1>;
-  hipLaunchKernelGGL(kern, dim3(row_blocks(rows)), dim3(64 * kWaves), 0, s, a, p, rows);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(rows)), dim3(64 * kWaves), 0, s, a, p, rows);
   return hipGetLastError();
 }
 
@@ -115,8 +202,26 @@ int fwd_splits(const AttnFwd& a) {
 }
 
 int lam_rows(const AttnFwd& a) {  // tiles of the q pass
-  const int rows = a.dt ? bwd_q_rows<uint16_t>(a) : bwd_q_rows<float>(a);
+  const int rows = a.dt ? bwd_rows<uint16_t>(a) : bwd_rows<float>(a);
   return a.B * ((a.T + rows - 1) / rows);
+}
+
+// The kv pass gives every tile of keys to one workgroup, or to several that share
+// the rows where the tiles are fewer than kShareTarget workgroups: two of them
+// fit on a compute unit, and twice as many even out the tiles' lengths.  A share
+// has at least kShareRows rows.
+constexpr int kShareTarget = 1024, kShareRows = 256;
+
+int kv_shares(const AttnFwd& a) {
+  const int keys = a.dt ? bwd_keys<uint16_t>(a) : bwd_keys<float>(a);
+  const long wgs = static_cast<long>((a.S + keys - 1) / keys) * a.B * a.Hk, rows = static_cast<long>(a.H / a.Hk) * a.T;
+  if (wgs == 0 || wgs >= kShareTarget || rows < 2 * kShareRows) return 1;
+  const long want = (kShareTarget + wgs - 1) / wgs, most = rows / kShareRows;
+  return static_cast<int>(want < most ? want : most);
+}
+size_t kv_floats(const AttnFwd& a) {
+  const int n = kv_shares(a);
+  return n > 1 ? static_cast<size_t>(n) * a.B * a.Hk * a.S * kv_width(a) : 0;
 }
 
 size_t stats_floats(const AttnFwd& a) { return (static_cast<size_t>(rows_of(a)) * a.maps() * 2 + 3) & ~static_cast<size_t>(3); }
@@ -134,7 +239,7 @@ size_t attention_fwd_workspace(const AttnFwd& a) {
 }
 
 size_t attention_bwd_workspace(const AttnFwd& a) {
-  return 4 * (attn::stats_floats(a) + (a.maps() > 1 ? static_cast<size_t>(attn::lam_rows(a)) * a.H : 0));
+  return 4 * (attn::stats_floats(a) + attn::kv_floats(a) + (a.maps() > 1 ? static_cast<size_t>(attn::lam_rows(a)) * a.H : 0));
 }
 
 hipError_t launch_attention_fwd(const AttnFwd& a, void* ws, hipStream_t s) {
@@ -147,7 +252,8 @@ hipError_t launch_attention_fwd(const AttnFwd& a, void* ws, hipStream_t s) {
 hipError_t launch_attention_bwd(const AttnBwd& g, void* ws, hipStream_t s) {
   const AttnFwd& a = g.f;
   float* stats = static_cast<float*>(ws);
-  float* lam_part = stats + attn::stats_floats(a);
+  float* part = stats + attn::stats_floats(a);
+  float* lam_part = part + attn::kv_floats(a);
   hipError_t e = hipSuccess;
   if (a.T > 0) {
     e = a.dt ? attn::stats<uint16_t>(g, stats, s) : attn::stats<float>(g, stats, s);
@@ -156,7 +262,9 @@ hipError_t launch_attention_bwd(const AttnBwd& g, void* ws, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (a.S > 0) {
-    e = a.dt ? attn::launch_bwd_kv<uint16_t>(g, stats, s) : attn::launch_bwd_kv<float>(g, stats, s);
+    const int n = attn::kv_shares(a);
+    e = a.dt ? attn::launch_bwd_kv<uint16_t>(g, stats, part, n, s) : attn::launch_bwd_kv<float>(g, stats, part, n, s);
+    if (e == hipSuccess && n > 1) e = a.dt ? attn::add<uint16_t>(g, part, n, s) : attn::add<float>(g, part, n, s);
     if (e != hipSuccess) return e;
   }
   if (a.maps() > 1) {

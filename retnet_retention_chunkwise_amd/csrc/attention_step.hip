@@ -22,7 +22,7 @@ namespace {
 constexpr int kWaves = 4, kKeys = 32;
 constexpr float kSlack = 8.0f;  // see attention_fwd.h
 
-template <typename E, int MAPS, int DK, int DV>
+template <typename E, int MAPS, int DK, int DV, bool kWhole>
 __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a, Partial part) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
@@ -40,7 +40,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), col = lane & 15, grp = lane >> 4;
   const int G = a.H / a.Hk, blocks = (G + 15) / 16;
   const int gb = blockIdx.x % blocks, bk = blockIdx.x / blocks, b = bk / a.Hk, hk = bk % a.Hk;
   const int split = blockIdx.y;
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   const int* table = a.table + static_cast<long>(b) * a.max_pages;
 
   Frag qf[MAPS * KS];
-  load_columns<E, MAPS, D>(static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h, live, a.d, lane, qf);
+  load_columns<E, MAPS, D, kWhole>(static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h, live, a.d, lane, qf);
   const float c = a.scale * kLog2e, slack = kSlack / c;
   f32x4 o[MAPS][VB];
   float mx[MAPS], sum[MAPS];
@@ -79,8 +79,8 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   u32x4 kr[2][MAPS * KS][KP], vr[VN];
   unsigned ok = 0;
   const int vrow = lane / CH, vchunk = (lane % CH) * CE;
-  const Piece16<E> vpiece(vchunk, a.dv);
-  auto kpiece = [&](int e, int i) { return Piece16<E>(32 * (e % KS) + 8 * grp + i * CE, a.d); };
+  const Piece16<E, kWhole> vpiece(vchunk, a.dv);
+  auto kpiece = [&](int e, int i) { return Piece16<E, kWhole>(32 * (e % KS) + 8 * grp + i * CE, a.d); };
   auto load = [&](int tile) {
     // lane j finds key j's rows; a key without a page (or behind the last) is
     // masked, and the new token's rows are read in its place
@@ -107,10 +107,10 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
 #pragma unroll
       for (int e = 0; e < MAPS * KS; ++e)
 #pragma unroll
-        for (int i = 0; i < KP; ++i) kr[kb][e][i] = kpiece(e, i).load(p + e / KS * a.d, a.d);
+        for (int i = 0; i < KP; ++i) kr[kb][e][i] = kpiece(e, i).load(reinterpret_cast<const char*>(p + e / KS * a.d), 0, a.d);
     }
 #pragma unroll
-    for (int i = 0; i < VN; ++i) vr[i] = vpiece.load(from(vp, i * VR + vrow), a.dv);
+    for (int i = 0; i < VN; ++i) vr[i] = vpiece.load(reinterpret_cast<const char*>(from(vp, i * VR + vrow)), 0, a.dv);
   };
 
   E* vs = lds.v[wave];
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   for (; i < last; i += kWaves) {
 #pragma unroll
     for (int j = 0; j < VN; ++j)
-      *reinterpret_cast<u32x4*>(vs + (j * VR + vrow) * VLD + vchunk) = vpiece.finish(vr[j], a.dv);
+      *reinterpret_cast<u32x4*>(vs + (j * VR + vrow) * VLD + vchunk) = vpiece.finish(vr[j]);
     f32x4 s[MAPS][2];
 #pragma unroll
     for (int m = 0; m < MAPS; ++m)
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
         for (int e = m * KS; e < (m + 1) * KS; ++e) {
           u32x4 x[KP];
 #pragma unroll
-          for (int j = 0; j < KP; ++j) x[j] = kpiece(e, j).finish(kr[kb][e][j], a.d);
+          for (int j = 0; j < KP; ++j) x[j] = kpiece(e, j).finish(kr[kb][e][j]);
           Frag kf;
           __builtin_memcpy(&kf, x, sizeof(kf));
           s[m][kb] = X::mma(kf, qf[e], s[m][kb]);
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
     const int ch = 16 * vb + 4 * grp;
     f32x4 y = *reinterpret_cast<const f32x4*>(&lds.j.out[0][col][ch]) * inv[0];
     if constexpr (MAPS > 1) y -= *reinterpret_cast<const f32x4*>(&lds.j.out[1][col][ch]) * (inv[1] * lam);
-    store4<E>(out, ch, a.dv, y);
+    store4<E, kWhole>(out, ch, a.dv, y);
   }
 }
 
@@ -338,10 +338,10 @@ int step_splits(const AttnStep& a) {
 
 template <typename E>
 hipError_t step(const AttnStep& a, const Partial& p, hipStream_t s) {
-  return with_sizes(a, [&](auto m, auto dk, auto dv) {
+  return with_sizes(a, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
     const int blocks = (a.H / a.Hk + 15) / 16;
-    hipLaunchKernelGGL((attention_step_kernel<E, M, DK, DV>),
+    hipLaunchKernelGGL((attention_step_kernel<E, M, DK, DV, decltype(whole)::value>),
                        dim3(static_cast<unsigned>(a.B) * a.Hk * blocks, p.nsplit), dim3(64 * kWaves), 0, s, a, p);
     return hipGetLastError();
   });

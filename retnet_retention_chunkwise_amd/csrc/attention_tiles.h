@@ -43,10 +43,12 @@ struct Mma<float> {
   }
 };
 
-// Rows of DIM elements in LDS, LD apart: 16 bytes more than the row, so that 16
-// rows read at one channel lie in different banks.
+// Rows of DIM elements in LDS, kTileLd apart.  32 bytes (fp32: 16) more than the
+// row: with bf16 the 16-byte reads of 16 rows and the transposing reads then both
+// run at 210-220 bytes a clock and compute unit; with 16 bytes more at 120, with
+// none at 32 and 64.
 template <typename E, int DIM>
-constexpr int kTileLd = DIM + 16 / static_cast<int>(sizeof(E));
+constexpr int kTileLd = DIM + (sizeof(E) == 2 ? 16 : 4);
 
 // A[row][channels]: eight consecutive channels from c0 + 8 (lane / 16) of row lane % 16.
 template <typename E>
@@ -78,20 +80,22 @@ __device__ __forceinline__ typename Mma<E>::Frag cols_frag(const E* tile, int ld
   }
 }
 
-// A lane's 16 bytes of a row of n elements, nominally from element c on.  No lane
-// leaves the others: where the row ends inside the piece it is read so far back
-// that it ends with the row, and shifted when it is used; a piece behind the row
-// reads the row's end.  What lies behind the row is zero if n is no multiple of
-// a piece, and otherwise left: it meets zeros in the other operand or fills
-// outputs that are not stored.
-template <typename E>
+// A lane's 16 bytes of a row of n elements, nominally from element c on.
+// kWhole: rows end with a piece (n a multiple of CE); a piece behind the row
+// reads the row's last.  Otherwise a piece that the row ends in is read so far
+// back that it ends with the row, and shifted when it is used, with zeros behind
+// the row.  No lane leaves the others.  What a whole row's padding holds is
+// left: it meets zeros in the other operand or fills outputs that are not stored.
+template <typename E, bool kWhole>
 struct Piece16 {
   static constexpr int CE = 16 / static_cast<int>(sizeof(E));
   int at, by;
-  __device__ __forceinline__ Piece16(int c, int n) : at(min(c, max(n - CE, 0))), by(c - at) {}
-  __device__ __forceinline__ u32x4 load(const E* row, int n) const {
+  __device__ __forceinline__ Piece16(int c, int n) : at(min(c, kWhole ? n - CE : max(n - CE, 0))), by(c - at) {}
+  // of the row that starts off bytes behind p
+  __device__ __forceinline__ u32x4 load(const char* p, unsigned off, int n) const {
     typedef typename RawOf<16, static_cast<int>(sizeof(E))>::at At;
-    if (n >= CE) return *reinterpret_cast<const At*>(row + at);
+    if (kWhole || n >= CE) return *reinterpret_cast<const At*>(p + (off + at * static_cast<unsigned>(sizeof(E))));
+    const E* row = reinterpret_cast<const E*>(p + off);
     E e[CE];
 #pragma unroll
     for (int i = 0; i < CE; ++i) {
@@ -102,8 +106,8 @@ struct Piece16 {
     __builtin_memcpy(&x, e, 16);
     return x;
   }
-  __device__ __forceinline__ u32x4 finish(u32x4 x, int n) const {
-    if (n % CE != 0) {
+  __device__ __forceinline__ u32x4 finish(u32x4 x) const {
+    if constexpr (!kWhole) {
       if constexpr (sizeof(E) == 2) {
         const u32x4 y = {x[0] >> 16 | x[1] << 16, x[1] >> 16 | x[2] << 16, x[2] >> 16 | x[3] << 16, x[3] >> 16};
         if (by & 1) x = y;
@@ -111,7 +115,7 @@ struct Piece16 {
       const int words = by * static_cast<int>(sizeof(E)) / 4;
       if (words & 1) x = u32x4{x[1], x[2], x[3], 0};
       if (words & 2) x = u32x4{x[2], x[3], 0, 0};
-      if (words & ~3) x = u32x4{0, 0, 0, 0};
+      x = zero_behind(x);
     }
     return x;
   }
@@ -121,15 +125,16 @@ struct Piece16 {
 // ROWS rows of MAPS parts of d elements, each part padded to D, on their way
 // from memory to LDS: THREADS threads, 16 bytes a piece.  load() only requests;
 // store() waits, and puts zeros for the rows from n on (which load the last row).
-template <typename E, int ROWS, int MAPS, int D, int THREADS>
+template <typename E, int ROWS, int MAPS, int D, int THREADS, bool kWhole>
 struct Stage {
   static constexpr int CE = 16 / static_cast<int>(sizeof(E));
   static constexpr int CH = MAPS * D / CE;               // pieces of a row
   static constexpr int STEP = THREADS / CH;              // rows of one round
-  static constexpr int N = ROWS / STEP;                  // rounds
-  static_assert(THREADS % CH == 0 && ROWS % STEP == 0, "a thread stays in its columns, every round is full");
+  static constexpr int N = STEP > ROWS ? 1 : ROWS / STEP;  // rounds
+  static_assert(THREADS % CH == 0 && (STEP > ROWS || ROWS % STEP == 0),
+                "a thread stays in its columns, rounds are full or one round has threads to spare");
   u32x4 r[N];
-  Piece16<E> piece;
+  Piece16<E, kWhole> piece;
   int row, col;  // of the thread's first piece in the tile
   int part;      // elements in front of its part of a row
   __device__ __forceinline__ Stage(int d, int tid)
@@ -138,34 +143,41 @@ struct Stage {
         col(tid % CH * CE),
         part(MAPS > 1 ? tid % CH / (D / CE) * d : 0) {}
 
-  // Rows row0.. of base, stride apart; n > 0 rows are readable.
+  // Rows row0.. of base, stride (below 2^24 elements) apart; n > 0 rows are
+  // readable.  A tile's address is uniform, a thread's place in it 32 bits.
   __device__ __forceinline__ void load(const E* base, long stride, int row0, int n, int d) {
-    const E* p = base + part;
-    if (row0 + ROWS <= n) {
-      p += (row0 + row) * stride;
+    const char* p = reinterpret_cast<const char*>(base + row0 * stride);
+    const unsigned step = static_cast<unsigned>(stride) * sizeof(E);
+    unsigned at[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = piece.load(p + i * STEP * stride, d);
-    } else {
+    for (int i = 0; i < N; ++i) at[i] = (STEP > ROWS ? min(row, ROWS - 1) : row + i * STEP) * step;
+    if (row0 + ROWS > n) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = piece.load(p + min(row0 + row + i * STEP, n - 1) * stride, d);
+      for (int i = 0; i < N; ++i) at[i] = min(row + i * STEP, n - 1 - row0) * step;
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = piece.load(p, at[i] + part * static_cast<unsigned>(sizeof(E)), d);
   }
-  __device__ __forceinline__ void store(E* tile, int ld, int row0, int n, int d) {
+  __device__ __forceinline__ void store(E* tile, int ld, int row0, int n) {
     if (row0 + ROWS > n) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (row0 + row + i * STEP >= n) r[i] = u32x4{0, 0, 0, 0};
     }
+    if (STEP > ROWS && row >= ROWS) return;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      *reinterpret_cast<u32x4*>(tile + (row + i * STEP) * ld + col) = piece.finish(r[i], d);
+      *reinterpret_cast<u32x4*>(tile + (row + i * STEP) * ld + col) = piece.finish(r[i]);
   }
 };
+
+// This wave's number in its workgroup, known to be the same in all its lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
 
 // B[channels][column]: column col's row of MAPS parts of d elements, padded with
 // zeros to D each, channels along a row; zeros where the column is not in (row
 // is readable all the same).
-template <typename E, int MAPS, int D>
+template <typename E, int MAPS, int D, bool kWhole>
 __device__ __forceinline__ void load_columns(const E* row, bool in, int d, int lane,
                                              typename Mma<E>::Frag (&f)[MAPS * D / 32]) {
   constexpr int CE = 16 / static_cast<int>(sizeof(E));
@@ -175,8 +187,8 @@ __device__ __forceinline__ void load_columns(const E* row, bool in, int d, int l
     u32x4 x[8 / CE];
 #pragma unroll
     for (int i = 0; i < 8 / CE; ++i) {
-      const Piece16<E> piece(c + i * CE, d);
-      x[i] = piece.zero_behind(piece.finish(piece.load(row + map * d, d), d));
+      const Piece16<E, kWhole> piece(c + i * CE, d);
+      x[i] = piece.zero_behind(piece.finish(piece.load(reinterpret_cast<const char*>(row + map * d), 0, d)));
       if (!in) x[i] = u32x4{0, 0, 0, 0};
     }
     __builtin_memcpy(&f[k], x, sizeof(f[k]));
@@ -185,9 +197,9 @@ __device__ __forceinline__ void load_columns(const E* row, bool in, int d, int l
 
 // Four consecutive elements of a row of n from element c on; c is a multiple of
 // 4, elements from n on are left out.
-template <typename E>
+template <typename E, bool kWhole>
 __device__ __forceinline__ void store4(E* row, int c, int n, f32x4 x) {
-  if (n % 4 == 0) {
+  if constexpr (kWhole) {
     typename RawOf<4 * sizeof(E), sizeof(E)>::type r;
     if constexpr (sizeof(E) == 4) {
       r = __builtin_bit_cast(u32x4, x);
@@ -210,6 +222,20 @@ __device__ __forceinline__ float row4_max(float x) {
   const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(y), __float_as_uint(y), false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
+
+// A border the compiler moves no instruction over.  The loops read the operands of
+// a stage from LDS one stage ahead of their products; left alone, the compiler
+// moves the reads down to their uses to save registers, and every two products
+// then wait for an LDS access.  (fp32 products are slow enough without.)
+template <typename E>
+__device__ __forceinline__ void stage_border() {
+  if constexpr (sizeof(E) == 2) __builtin_amdgcn_sched_barrier(0);
+}
+
+// Products go before the other wave's exponentials on a SIMD: a product occupies
+// the issue for a quarter of its time, the rest is the other wave's.
+__device__ __forceinline__ void products_first() { __builtin_amdgcn_s_setprio(1); }
+__device__ __forceinline__ void products_done() { __builtin_amdgcn_s_setprio(0); }
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
