@@ -104,47 +104,66 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
       }
     }
     if (k0 >= wmax) continue;
-    f32x4 dp[KB][NB];
+    products_first();
+    f32x4 dp[KB][NB], s[MAPS][KB][NB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
+      Frag vf[VS];
+#pragma unroll
+      for (int e = 0; e < VS; ++e) vf[e] = rows_frag<E>(Vs, VLD, 16 * kb, 32 * e, lane);
 #pragma unroll
       for (int n = 0; n < NB; ++n) dp[kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int e = 0; e < VS; ++e) {
-        const Frag vf = rows_frag<E>(Vs, VLD, 16 * kb, 32 * e, lane);
+      for (int e = 0; e < VS; ++e)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) dp[kb][n] = X::mma(vf, gf[n][e], dp[kb][n]);
-      }
+        for (int n = 0; n < NB; ++n) dp[kb][n] = X::mma(vf[e], gf[n][e], dp[kb][n]);
     }
-    const bool edge = k0 + KT > wall;
 #pragma unroll
-    for (int m = 0; m < MAPS; ++m) {
-      f32x4 s[KB][NB];
+    for (int m = 0; m < MAPS; ++m)
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
+        Frag kf[KS];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) s[kb][n] = f32x4{0, 0, 0, 0};
+        for (int e = 0; e < KS; ++e) kf[e] = rows_frag<E>(Ks, KLD, 16 * kb, m * D + 32 * e, lane);
 #pragma unroll
-        for (int e = 0; e < KS; ++e) {
-          const Frag kf = rows_frag<E>(Ks, KLD, 16 * kb, m * D + 32 * e, lane);
+        for (int n = 0; n < NB; ++n) s[m][kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int n = 0; n < NB; ++n) s[kb][n] = X::mma(kf, qf[n][m * KS + e], s[kb][n]);
-        }
+        for (int e = 0; e < KS; ++e)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) s[m][kb][n] = X::mma(kf[e], qf[n][m * KS + e], s[m][kb][n]);
+      }
+    products_done();
+    if (k0 + KT > wall) {  // some row does not see some key
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            float p = fast_exp2(fmaf(s[kb][n][r], c, -st[m][n].x));
-            if (edge && k0 + 16 * kb + 4 * grp + r >= lim[n]) p = 0.0f;
-            if (m == 1) lam_sum = fmaf(p, dp[kb][n][r], lam_sum);
-            s[kb][n][r] = p * (dp[kb][n][r] - st[m][n].y);
+            const bool out = k0 + 16 * kb + 4 * grp + r >= lim[n];
+#pragma unroll
+            for (int m = 0; m < MAPS; ++m)
+              if (out) s[m][kb][n][r] = -INFINITY;
           }
-      }
+    }
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float p = fast_exp2(fmaf(s[m][kb][n][r], c, -st[m][n].x));
+            if (m == 1) lam_sum = fmaf(p, dp[kb][n][r], lam_sum);
+            s[m][kb][n][r] = p * (dp[kb][n][r] - st[m][n].y);
+          }
+      products_first();
 #pragma unroll
       for (int j = 0; j < KT / 32; ++j) {
         Frag ds[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[2 * j][n], s[2 * j + 1][n]);
+        for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[m][2 * j][n], s[m][2 * j + 1][n]);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
           const Frag kt = cols_frag<E>(Ks, KLD, 32 * j, m * D + 16 * cb, lane);
@@ -152,6 +171,7 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
           for (int n = 0; n < NB; ++n) dq[m][cb][n] = X::mma(kt, ds[n], dq[m][cb][n]);
         }
       }
+      products_done();
     }
   }
 
