@@ -27,6 +27,7 @@ struct AttnFwd {
   bool causal;
   int offset;        // causal: row t sees the keys up to t + offset
   int dt;
+  bool whole;        // rows of whole 16-byte pieces; bf16: also at 16-byte addresses
   int maps() const { return lam != nullptr ? 2 : 1; }
 };
 struct AttnBwd {
@@ -55,6 +56,7 @@ struct AttnStep {
   int B, H, Hk, d, dv, pages, page, max_pages;
   float scale;
   int dt;
+  bool whole;        // rows of whole 16-byte pieces
   int maps() const { return lam != nullptr ? 2 : 1; }
 };
 // T tokens of every sequence into the cache.
@@ -115,17 +117,17 @@ template <typename E>
 hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, float* part, int shares, hipStream_t s);
 
 // f(maps, channels of all maps, channels of a value, whole), as types, for the
-// smallest sizes built that hold the call's.  whole: the rows of a map and of a
-// value are whole pieces of 16 bytes; rows that are not take code that shifts
-// their ends, built for two sizes.
+// smallest sizes built that hold the call's.  Rows that are not whole take code
+// that shifts their ends, built for two sizes; a workgroup's rows do not depend
+// on it.
 template <typename A, typename F>
 auto with_sizes(const A& a, F&& f) {
   typedef std::integral_constant<int, 64> N64;
   typedef std::integral_constant<int, 128> N128;
   typedef std::integral_constant<int, 256> N256;
   auto pick = [&](auto maps) {
-    const int dk = a.d * decltype(maps)::value, piece = a.dt ? 8 : 4;
-    if (a.d % piece != 0 || a.dv % piece != 0) {
+    const int dk = a.d * decltype(maps)::value;
+    if (!a.whole) {
       if (dk <= 128 && a.dv <= 128) return f(maps, N128(), N128(), std::false_type());
       return f(maps, N256(), N256(), std::false_type());
     }

@@ -100,7 +100,18 @@ ret::AttnFwd sizes_only(const Sizes& z, ret_dtype dt) {
   a.d = z.dk / z.maps;
   a.dv = z.dv;
   a.dt = dt == RET_BF16 ? 1 : 0;
+  a.whole = true;
   return a;
+}
+
+// Whether maps of d and values of dv elements are whole pieces of 16 bytes.
+bool whole_rows(int d, int dv, ret_dtype dt) {
+  const int piece = dt == RET_BF16 ? 8 : 4;
+  return d % piece == 0 && dv % piece == 0;
+}
+// Whether every row of a tensor starts at a multiple of 16 bytes.
+bool rows_aligned(const void* p, const Strides3& s, size_t es) {
+  return (reinterpret_cast<uintptr_t>(p) | s.b * es | s.h * es | s.t * es) % 16 == 0;
 }
 
 }  // namespace
@@ -161,6 +172,8 @@ ret_status retention_attention_fwd(const void* q, const void* k, const void* v, 
   a.scale = scale;
   a.causal = causal != 0;
   a.offset = offset;
+  a.whole = whole_rows(a.d, dv, dt) &&
+            (dt == RET_F32 || (rows_aligned(k, a.sk, dsize(dt)) && rows_aligned(v, a.sv, dsize(dt))));
   return done(fn, ret::launch_attention_fwd(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
@@ -219,6 +232,9 @@ ret_status retention_attention_bwd(const void* q, const void* k, const void* v, 
   a.scale = scale;
   a.causal = causal != 0;
   a.offset = offset;
+  a.whole = whole_rows(a.d, dv, dt) &&
+            (dt == RET_F32 || (rows_aligned(k, a.sk, dsize(dt)) && rows_aligned(v, a.sv, dsize(dt)) &&
+                               rows_aligned(q, a.sq, dsize(dt)) && rows_aligned(grad_o, g.sdo, dsize(dt))));
   g.grad_o = grad_o;
   g.grad_q = grad_q;
   g.grad_k = grad_k;
@@ -298,6 +314,7 @@ ret_status retention_attention_step(const void* q, const void* k, const void* v,
   a.max_pages = max_pages;
   a.scale = scale;
   a.dt = dt == RET_BF16 ? 1 : 0;
+  a.whole = whole_rows(a.d, dv, dt);
   return done(fn, ret::launch_attention_step(a, workspace, static_cast<hipStream_t>(stream)));
 }
 

@@ -27,15 +27,18 @@ namespace attn {
 
 // stats: [M][B*H*T] of {lse log2 e, D}: first all of map 1.
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int KT>
-__global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, const float2* __restrict__ stats,
+__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) void attention_bwd_q_kernel(AttnBwd g, const float2* __restrict__ stats,
                                                                   float* __restrict__ lam_part, int tiles) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
   constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
   constexpr int KB = KT / 16, KS = D / 32, VS = DV / 32, CB = D / 16;
-  constexpr int KLD = kTileLd<E, DK>, VLD = kTileLd<E, DV>;
-  __shared__ __attribute__((aligned(16))) E Kt[2][KT * KLD];
-  __shared__ __attribute__((aligned(16))) E Vt[2][KT * VLD];
+  constexpr bool kDma = kWhole && sizeof(E) == 2;
+  constexpr int SLOTS = DK + DV <= 256 ? 3 : 2;
+  typedef Tile<E, DK, kDma> KTile;
+  typedef Tile<E, DV, kDma> VTile;
+  __shared__ __attribute__((aligned(16))) E K0[KT * KTile::LD], K1[KT * KTile::LD], K2[kDma && SLOTS == 3 ? KT * DK : 16];
+  __shared__ __attribute__((aligned(16))) E V0[KT * VTile::LD], V1[KT * VTile::LD], V2[kDma && SLOTS == 3 ? KT * DV : 16];
   __shared__ float wave_lam[NW];
 
   const AttnFwd& a = g.f;
@@ -78,39 +81,16 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
       for (int n = 0; n < NB; ++n) dq[m][i][n] = f32x4{0, 0, 0, 0};
   float lam_sum = 0.0f;
 
-  Stage<E, KT, MAPS, D, THREADS, kWhole> ks(a.d, tid);
-  Stage<E, KT, 1, DV, THREADS, kWhole> vs(a.dv, tid);
-  // two tiles in LDS, as in the forward
-  if (last > 0) {
-    ks.load(k, a.sk.t, 0, len, a.d);
-    vs.load(v, a.sv.t, 0, len, a.dv);
-    ks.store(Kt[0], KLD, 0, len);
-    vs.store(Vt[0], VLD, 0, len);
-    if (last > 1) {
-      ks.load(k, a.sk.t, KT, len, a.d);
-      vs.load(v, a.sv.t, KT, len, a.dv);
-    }
-  }
-  for (int i = 0; i < last; ++i) {
-    const int k0 = i * KT, slot = i & 1;
-    const E *Ks = Kt[slot], *Vs = Vt[slot];
-    lds_barrier();
-    if (i + 1 < last) {
-      ks.store(Kt[slot ^ 1], KLD, k0 + KT, len);
-      vs.store(Vt[slot ^ 1], VLD, k0 + KT, len);
-      if (i + 2 < last) {
-        ks.load(k, a.sk.t, k0 + 2 * KT, len, a.d);
-        vs.load(v, a.sv.t, k0 + 2 * KT, len, a.dv);
-      }
-    }
-    if (k0 >= wmax) continue;
+  auto use = [&](int i, const E* Ks, const E* Vs) __attribute__((always_inline)) {
+    const int k0 = i * KT;
+    if (k0 >= wmax) return;
     products_first();
     f32x4 dp[KB][NB], s[MAPS][KB][NB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       Frag vf[VS];
 #pragma unroll
-      for (int e = 0; e < VS; ++e) vf[e] = rows_frag<E>(Vs, VLD, 16 * kb, 32 * e, lane);
+      for (int e = 0; e < VS; ++e) vf[e] = VTile::rows(Vs, 16 * kb, 32 * e, lane);
 #pragma unroll
       for (int n = 0; n < NB; ++n) dp[kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -124,7 +104,7 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
       for (int kb = 0; kb < KB; ++kb) {
         Frag kf[KS];
 #pragma unroll
-        for (int e = 0; e < KS; ++e) kf[e] = rows_frag<E>(Ks, KLD, 16 * kb, m * D + 32 * e, lane);
+        for (int e = 0; e < KS; ++e) kf[e] = KTile::rows(Ks, 16 * kb, m * D + 32 * e, lane);
 #pragma unroll
         for (int n = 0; n < NB; ++n) s[m][kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -166,12 +146,49 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
         for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[m][2 * j][n], s[m][2 * j + 1][n]);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-          const Frag kt = cols_frag<E>(Ks, KLD, 32 * j, m * D + 16 * cb, lane);
+          const Frag kt = KTile::cols(Ks, 32 * j, m * D + 16 * cb, lane);
 #pragma unroll
           for (int n = 0; n < NB; ++n) dq[m][cb][n] = X::mma(kt, ds[n], dq[m][cb][n]);
         }
       }
       products_done();
+    }
+  };
+  // tiles in LDS as in the forward
+  if constexpr (kDma) {
+    const Dma<KT, MAPS, D, NW> kd(a.d, wave, lane);
+    const Dma<KT, 1, DV, NW> vd(a.dv, wave, lane);
+    E *const Kt[] = {K0, K1, K2}, *const Vt[] = {V0, V1, V2};
+    walk_tiles<SLOTS, kd.COUNT + vd.COUNT>(
+        0, last,
+        [&](int i, auto slot) __attribute__((always_inline)) {
+          kd.load(k, a.sk.t, i * KT, len, Kt[slot], wave);
+          vd.load(v, a.sv.t, i * KT, len, Vt[slot], wave);
+        },
+        [&](int i, auto slot) __attribute__((always_inline)) { use(i, Kt[slot], Vt[slot]); });
+  } else {
+    Stage<E, KT, MAPS, D, THREADS, kWhole> ks(a.d, tid);
+    Stage<E, KT, 1, DV, THREADS, kWhole> vs(a.dv, tid);
+    auto load = [&](int i) {
+      ks.load(k, a.sk.t, i * KT, len, a.d);
+      vs.load(v, a.sv.t, i * KT, len, a.dv);
+    };
+    auto store = [&](int i) {
+      ks.store(i & 1 ? K1 : K0, i * KT, len);
+      vs.store(i & 1 ? V1 : V0, i * KT, len);
+    };
+    if (last > 0) {
+      load(0);
+      store(0);
+      if (last > 1) load(1);
+    }
+    for (int i = 0; i < last; ++i) {
+      lds_barrier();
+      if (i + 1 < last) {
+        store(i + 1);
+        if (i + 2 < last) load(i + 2);
+      }
+      use(i, i & 1 ? K1 : K0, i & 1 ? V1 : V0);
     }
   }
 
@@ -201,17 +218,23 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_q_kernel(AttnBwd g, con
 }
 
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int QT>
-__global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, const float2* __restrict__ stats,
+__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) void attention_bwd_kv_kernel(AttnBwd g, const float2* __restrict__ stats,
                                                                       float* __restrict__ part, int shares) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
   constexpr int D = DK / MAPS, THREADS = 64 * NW, KT = 16 * NB * NW;
   constexpr int QB = QT / 16, KS = D / 32, VS = DV / 32, CB = D / 16, VB = DV / 16;
-  constexpr int QLD = kTileLd<E, DK>, GLD = kTileLd<E, DV>;
+  constexpr bool kDma = kWhole && sizeof(E) == 2;
+  constexpr int SLOTS = DK + DV <= 256 ? 3 : 2;
+  typedef Tile<E, DK, kDma> QTile;
+  typedef Tile<E, DV, kDma> GTile;
   constexpr bool kAhead = sizeof(E) == 2;
-  __shared__ __attribute__((aligned(16))) E Qt[2][QT * QLD];
-  __shared__ __attribute__((aligned(16))) E Gt[2][QT * GLD];
-  __shared__ __attribute__((aligned(16))) float Lt[2][MAPS][QT], Dt[2][MAPS][QT];
+  __shared__ __attribute__((aligned(16))) E Q0[QT * QTile::LD], Q1[QT * QTile::LD], Q2[kDma && SLOTS == 3 ? QT * DK : 16];
+  __shared__ __attribute__((aligned(16))) E G0[QT * GTile::LD], G1[QT * GTile::LD], G2[kDma && SLOTS == 3 ? QT * DV : 16];
+  // statistics of a tile's rows, {lse log2 e, D}; with straight loads every wave
+  // brings a map's, so that all have as many loads, and the first copies are used
+  constexpr int SC = kDma ? (NW > MAPS ? NW : MAPS) : MAPS;
+  __shared__ __attribute__((aligned(16))) float2 S0[SC * QT], S1[SC * QT], S2[kDma && SLOTS == 3 ? SC * QT : 1];
   static_assert(MAPS * QT <= THREADS, "a thread per row's statistics");
 
   const AttnFwd& a = g.f;
@@ -251,46 +274,13 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
     for (int i = 0; i < VB; ++i) dv[i][n] = f32x4{0, 0, 0, 0};
   }
 
-  Stage<E, QT, MAPS, D, THREADS, kWhole> qs(a.d, tid);
-  Stage<E, QT, 1, DV, THREADS, kWhole> gs(a.dv, tid);
-  float2 st;
-  auto load = [&](int i) {
-    const int h = hk * G + i / n_tiles, row0 = t0 + i % n_tiles * QT;
-    qs.load(static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h, a.sq.t, row0, a.T, a.d);
-    gs.load(static_cast<const E*>(g.grad_o) + b * g.sdo.b + h * g.sdo.h, g.sdo.t, row0, a.T, a.dv);
-    if (tid < MAPS * QT) {
-      const int t = row0 + tid % QT;
-      st = t < a.T ? stats[tid / QT * rows + (static_cast<long>(b) * a.H + h) * a.T + t] : make_float2(INFINITY, 0.0f);
-    }
-  };
-  auto store = [&](int i) {
-    const int row0 = t0 + i % n_tiles * QT, slot = i & 1;
-    qs.store(Qt[slot], QLD, row0, a.T);
-    gs.store(Gt[slot], GLD, row0, a.T);
-    if (tid < MAPS * QT) {
-      Lt[slot][tid / QT][tid % QT] = st.x;
-      Dt[slot][tid / QT][tid % QT] = st.y;
-    }
-  };
   // this workgroup's share of the heads' tiles
   const int n_all = G * n_tiles;
   const int first = static_cast<int>(static_cast<long>(n_all) * share / shares);
   const int last = static_cast<int>(static_cast<long>(n_all) * (share + 1) / shares);
-  if (first < last) {
-    load(first);
-    store(first);
-    if (first + 1 < last) load(first + 1);
-  }
-  for (int i = first; i < last; ++i) {
-    const int row0 = t0 + i % n_tiles * QT, slot = i & 1;
-    const E *Qs = Qt[slot], *Gs = Gt[slot];
-    const float(*Ls)[QT] = Lt[slot], (*Ds)[QT] = Dt[slot];
-    lds_barrier();
-    if (i + 1 < last) {
-      store(i + 1);
-      if (i + 2 < last) load(i + 2);
-    }
-    if (row0 + QT <= wfirst) continue;
+  auto use = [&](int i, const E* Qs, const E* Gs, const float2* Ss) __attribute__((always_inline)) {
+    const int row0 = t0 + i % n_tiles * QT;
+    if (row0 + QT <= wfirst) return;
     const float lam = MAPS > 1 ? a.lam[hk * G + i / n_tiles] : 0.0f;
     Frag ga[QB][VS], qa[MAPS][QB][KS], qc[MAPS][QT / 32][CB];
     f32x4 dp[QB][NB], s[MAPS][QB][NB], pv[QB][NB];
@@ -304,7 +294,7 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
 #pragma unroll
       for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-        for (int e = 0; e < KS; ++e) qa[m][qb][e] = rows_frag<E>(Qs, QLD, 16 * qb, m * D + 32 * e, lane);
+        for (int e = 0; e < KS; ++e) qa[m][qb][e] = QTile::rows(Qs, 16 * qb, m * D + 32 * e, lane);
     };
     auto scores = [&](int m) {
 #pragma unroll
@@ -315,19 +305,20 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
         for (int e = 0; e < KS; ++e)
 #pragma unroll
           for (int n = 0; n < NB; ++n)
-            s[m][qb][n] = X::mma(get(qa[m][qb][e], [&] { return rows_frag<E>(Qs, QLD, 16 * qb, m * D + 32 * e, lane); }),
+            s[m][qb][n] = X::mma(get(qa[m][qb][e], [&] { return QTile::rows(Qs, 16 * qb, m * D + 32 * e, lane); }),
                                  kf[n][m * KS + e], s[m][qb][n]);
       }
     };
     auto mask = [&]() {
-      if (row0 < wall) {  // some row does not see some key
+      if (row0 < wall || row0 + QT > a.T) {  // some row does not see some key, or is none
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const bool out = row0 + 16 * qb + 4 * grp + r < lim[n];
+              const int t = row0 + 16 * qb + 4 * grp + r;
+              const bool out = t < lim[n] || t >= a.T;
 #pragma unroll
               for (int m = 0; m < MAPS; ++m)
                 if (out) s[m][qb][n][r] = -INFINITY;
@@ -339,14 +330,14 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
 #pragma unroll
       for (int j = 0; j < QT / 32; ++j)
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) qc[m][j][cb] = cols_frag<E>(Qs, QLD, 32 * j, m * D + 16 * cb, lane);
+        for (int cb = 0; cb < CB; ++cb) qc[m][j][cb] = QTile::cols(Qs, 32 * j, m * D + 16 * cb, lane);
     };
     // p and ds of a map in place of its scores; pv collects p_1 - lam p_2
     auto weigh = [&](int m) {
 #pragma unroll
       for (int qb = 0; qb < QB; ++qb) {
-        const f32x4 l4 = *reinterpret_cast<const f32x4*>(&Ls[m][16 * qb + 4 * grp]);
-        const f32x4 d4 = *reinterpret_cast<const f32x4*>(&Ds[m][16 * qb + 4 * grp]);
+        const f32x4* at = reinterpret_cast<const f32x4*>(&Ss[m * QT + 16 * qb + 4 * grp]);
+        const f32x4 s01 = at[0], s23 = at[1], l4 = {s01[0], s01[2], s23[0], s23[2]}, d4 = {s01[1], s01[3], s23[1], s23[3]};
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -368,7 +359,7 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
           for (int n = 0; n < NB; ++n) 
-            dk[m][cb][n] = X::mma(get(qc[m][j][cb], [&] { return cols_frag<E>(Qs, QLD, 32 * j, m * D + 16 * cb, lane); }),
+            dk[m][cb][n] = X::mma(get(qc[m][j][cb], [&] { return QTile::cols(Qs, 32 * j, m * D + 16 * cb, lane); }),
                                   ds[n], dk[m][cb][n]);
       }
     };
@@ -376,7 +367,7 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
 #pragma unroll
       for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-        for (int e = 0; e < VS; ++e) ga[qb][e] = rows_frag<E>(Gs, GLD, 16 * qb, 32 * e, lane);
+        for (int e = 0; e < VS; ++e) ga[qb][e] = GTile::rows(Gs, 16 * qb, 32 * e, lane);
     }
     read_q(0);
     stage_border<E>();
@@ -389,7 +380,7 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
       for (int e = 0; e < VS; ++e)
 #pragma unroll
         for (int n = 0; n < NB; ++n)
-          dp[qb][n] = X::mma(get(ga[qb][e], [&] { return rows_frag<E>(Gs, GLD, 16 * qb, 32 * e, lane); }), vf[n][e], dp[qb][n]);
+          dp[qb][n] = X::mma(get(ga[qb][e], [&] { return GTile::rows(Gs, 16 * qb, 32 * e, lane); }), vf[n][e], dp[qb][n]);
     }
     stage_border<E>();
     if constexpr (MAPS > 1) read_q(1);
@@ -424,7 +415,7 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
 #pragma unroll
       for (int j = 0; j < QT / 32; ++j)
 #pragma unroll
-        for (int vb = 0; vb < VG; ++vb) gc[v0 / VG & 1][j][vb] = cols_frag<E>(Gs, GLD, 32 * j, 16 * (v0 + vb), lane);
+        for (int vb = 0; vb < VG; ++vb) gc[v0 / VG & 1][j][vb] = GTile::cols(Gs, 32 * j, 16 * (v0 + vb), lane);
     };
     read_gt(0);
     stage_border<E>();
@@ -447,10 +438,60 @@ __global__ __launch_bounds__(64 * NW) void attention_bwd_kv_kernel(AttnBwd g, co
 #pragma unroll
           for (int n = 0; n < NB; ++n)
             dv[v0 + vb][n] = X::mma(
-                get(gc[v0 / VG & 1][j][vb], [&] { return cols_frag<E>(Gs, GLD, 32 * j, 16 * (v0 + vb), lane); }), pf[j][n],
+                get(gc[v0 / VG & 1][j][vb], [&] { return GTile::cols(Gs, 32 * j, 16 * (v0 + vb), lane); }), pf[j][n],
                 dv[v0 + vb][n]);
     }
     products_done();
+  };
+  auto q_of = [&](int h) { return static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h; };
+  auto g_of = [&](int h) { return static_cast<const E*>(g.grad_o) + b * g.sdo.b + h * g.sdo.h; };
+  auto stats_of = [&](int h, int m) { return stats + m * rows + (static_cast<long>(b) * a.H + h) * a.T; };
+  // tiles in LDS as in the forward
+  if constexpr (kDma) {
+    const Dma<QT, MAPS, D, NW> qd(a.d, wave, lane);
+    const Dma<QT, 1, DV, NW> gd(a.dv, wave, lane);
+    static_assert(QT * 8 == 64 * 4, "a wave brings a map's statistics in one load");
+    E *const Qt[] = {Q0, Q1, Q2}, *const Gt[] = {G0, G1, G2};
+    float2* const St[] = {S0, S1, S2};
+    walk_tiles<SLOTS, qd.COUNT + gd.COUNT + 1>(
+        first, last,
+        [&](int i, auto slot) __attribute__((always_inline)) {
+          const int h = hk * G + i / n_tiles, row0 = t0 + i % n_tiles * QT;
+          qd.load(q_of(h), a.sq.t, row0, a.T, Qt[slot], wave);
+          gd.load(g_of(h), g.sdo.t, row0, a.T, Gt[slot], wave);
+          // rows behind the last repeat it; use() masks them
+          load_to_lds<4>(stats_of(h, wave % MAPS), 8 * min(row0 + lane / 2, a.T - 1) + 4 * (lane & 1), St[slot] + wave * QT);
+        },
+        [&](int i, auto slot) __attribute__((always_inline)) { use(i, Qt[slot], Gt[slot], St[slot]); });
+  } else {
+    Stage<E, QT, MAPS, D, THREADS, kWhole> qs(a.d, tid);
+    Stage<E, QT, 1, DV, THREADS, kWhole> gs(a.dv, tid);
+    float2 st;
+    auto load = [&](int i) {
+      const int h = hk * G + i / n_tiles, row0 = t0 + i % n_tiles * QT;
+      qs.load(q_of(h), a.sq.t, row0, a.T, a.d);
+      gs.load(g_of(h), g.sdo.t, row0, a.T, a.dv);
+      if (tid < MAPS * QT) st = stats_of(h, tid / QT)[min(row0 + tid % QT, a.T - 1)];
+    };
+    auto store = [&](int i) {
+      const int row0 = t0 + i % n_tiles * QT;
+      qs.store(i & 1 ? Q1 : Q0, row0, a.T);
+      gs.store(i & 1 ? G1 : G0, row0, a.T);
+      if (tid < MAPS * QT) (i & 1 ? S1 : S0)[tid] = st;
+    };
+    if (first < last) {
+      load(first);
+      store(first);
+      if (first + 1 < last) load(first + 1);
+    }
+    for (int i = first; i < last; ++i) {
+      lds_barrier();
+      if (i + 1 < last) {
+        store(i + 1);
+        if (i + 2 < last) load(i + 2);
+      }
+      use(i, i & 1 ? Q1 : Q0, i & 1 ? G1 : G0, i & 1 ? S1 : S0);
+    }
   }
 
 #pragma unroll

@@ -26,14 +26,17 @@ namespace attn {
 constexpr float kSlack = 8.0f;
 
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int KT>
-__global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Partial part, int tiles) {
+__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (MAPS == 1 || DV < 256) && DV <= 128 ? 2 : 1)) void attention_fwd_kernel(AttnFwd a, Partial part, int tiles) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
   constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
   constexpr int KB = KT / 16, KS = D / 32, VB = DV / 16;
-  constexpr int KLD = kTileLd<E, DK>, VLD = kTileLd<E, DV>;
-  __shared__ __attribute__((aligned(16))) E Kt[2][KT * KLD];
-  __shared__ __attribute__((aligned(16))) E Vt[2][KT * VLD];
+  constexpr bool kDma = kWhole && sizeof(E) == 2;
+  constexpr int SLOTS = DK + DV <= 256 ? 3 : 2;
+  typedef Tile<E, DK, kDma> KTile;
+  typedef Tile<E, DV, kDma> VTile;
+  __shared__ __attribute__((aligned(16))) E K0[KT * KTile::LD], K1[KT * KTile::LD], K2[kDma && SLOTS == 3 ? KT * DK : 16];
+  __shared__ __attribute__((aligned(16))) E V0[KT * VTile::LD], V1[KT * VTile::LD], V2[kDma && SLOTS == 3 ? KT * DV : 16];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), col = lane & 15, grp = lane >> 4;
   // the longest rows of all heads first, so that the last workgroups are short
@@ -76,33 +79,10 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Parti
       for (int i = 0; i < VB; ++i) o[m][i][n] = f32x4{0, 0, 0, 0};
     }
 
-  Stage<E, KT, MAPS, D, THREADS, kWhole> ks(a.d, tid);
-  Stage<E, KT, 1, DV, THREADS, kWhole> vs(a.dv, tid);
-  // Two tiles in LDS: while one is used the next is written (its loads were sent
-  // a tile earlier) and the one after is on its way; one barrier a tile.
-  if (first < last) {
-    ks.load(k, a.sk.t, first * KT, len, a.d);
-    vs.load(v, a.sv.t, first * KT, len, a.dv);
-    ks.store(Kt[0], KLD, first * KT, len);
-    vs.store(Vt[0], VLD, first * KT, len);
-    if (first + 1 < last) {
-      ks.load(k, a.sk.t, (first + 1) * KT, len, a.d);
-      vs.load(v, a.sv.t, (first + 1) * KT, len, a.dv);
-    }
-  }
-  for (int i = first; i < last; ++i) {
-    const int k0 = i * KT, slot = (i - first) & 1;
-    const E *Ks = Kt[slot], *Vs = Vt[slot];
-    lds_barrier();
-    if (i + 1 < last) {
-      ks.store(Kt[slot ^ 1], KLD, k0 + KT, len);
-      vs.store(Vt[slot ^ 1], VLD, k0 + KT, len);
-      if (i + 2 < last) {
-        ks.load(k, a.sk.t, k0 + 2 * KT, len, a.d);
-        vs.load(v, a.sv.t, k0 + 2 * KT, len, a.dv);
-      }
-    }
-    if (k0 >= wmax) continue;
+  // one tile of keys and values that lie in LDS
+  auto use = [&](int i, const E* Ks, const E* Vs) __attribute__((always_inline)) {
+    const int k0 = i * KT;
+    if (k0 >= wmax) return;
     products_first();
     f32x4 s[MAPS][KB][NB];
 #pragma unroll
@@ -111,7 +91,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Parti
       for (int kb = 0; kb < KB; ++kb) {
         Frag kf[KS];
 #pragma unroll
-        for (int e = 0; e < KS; ++e) kf[e] = rows_frag<E>(Ks, KLD, 16 * kb, m * D + 32 * e, lane);
+        for (int e = 0; e < KS; ++e) kf[e] = KTile::rows(Ks, 16 * kb, m * D + 32 * e, lane);
 #pragma unroll
         for (int n = 0; n < NB; ++n) s[m][kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -181,13 +161,52 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnFwd a, Parti
     for (int j = 0; j < KT / 32; ++j)
 #pragma unroll
       for (int vb = 0; vb < VB; ++vb) {
-        const Frag vf = cols_frag<E>(Vs, VLD, 32 * j, 16 * vb, lane);
+        const Frag vf = VTile::cols(Vs, 32 * j, 16 * vb, lane);
 #pragma unroll
         for (int m = 0; m < MAPS; ++m)
 #pragma unroll
           for (int n = 0; n < NB; ++n) o[m][vb][n] = X::mma(vf, pf[m][n][j], o[m][vb][n]);
       }
     products_done();
+  };
+  if constexpr (kDma) {
+    const Dma<KT, MAPS, D, NW> kd(a.d, wave, lane);
+    const Dma<KT, 1, DV, NW> vd(a.dv, wave, lane);
+    E *const Kt[] = {K0, K1, K2}, *const Vt[] = {V0, V1, V2};
+    walk_tiles<SLOTS, kd.COUNT + vd.COUNT>(
+        first, last,
+        [&](int i, auto slot) __attribute__((always_inline)) {
+          kd.load(k, a.sk.t, i * KT, len, Kt[slot], wave);
+          vd.load(v, a.sv.t, i * KT, len, Vt[slot], wave);
+        },
+        [&](int i, auto slot) __attribute__((always_inline)) { use(i, Kt[slot], Vt[slot]); });
+  } else {
+    // Two tiles in LDS: while one is used the next is written (its loads were sent
+    // a tile earlier) and the one after is on its way; one barrier a tile.
+    Stage<E, KT, MAPS, D, THREADS, kWhole> ks(a.d, tid);
+    Stage<E, KT, 1, DV, THREADS, kWhole> vs(a.dv, tid);
+    auto load = [&](int i) {
+      ks.load(k, a.sk.t, i * KT, len, a.d);
+      vs.load(v, a.sv.t, i * KT, len, a.dv);
+    };
+    auto store = [&](int i, int slot) {
+      ks.store(slot ? K1 : K0, i * KT, len);
+      vs.store(slot ? V1 : V0, i * KT, len);
+    };
+    if (first < last) {
+      load(first);
+      store(first, 0);
+      if (first + 1 < last) load(first + 1);
+    }
+    for (int i = first; i < last; ++i) {
+      const int slot = (i - first) & 1;
+      lds_barrier();
+      if (i + 1 < last) {
+        store(i + 1, slot ^ 1);
+        if (i + 2 < last) load(i + 2);
+      }
+      use(i, slot ? K1 : K0, slot ? V1 : V0);
+    }
   }
 
   const float lam = MAPS > 1 ? a.lam[h] : 0.0f;

@@ -207,20 +207,21 @@ int lam_rows(const AttnFwd& a) {  // tiles of the q pass
 }
 
 // The kv pass gives every tile of keys to one workgroup, or to several that share
-// the rows where the tiles are fewer than kShareTarget workgroups: two of them
-// fit on a compute unit, and twice as many even out the tiles' lengths.  A share
-// has at least kShareRows rows.
+// the rows: two fit on each of the 256 compute units, and with a causal mask,
+// whose tiles differ in length, twice as many even them out.  A share has at
+// least kShareRows rows.
 constexpr int kShareTarget = 1024, kShareRows = 256;
 
-int kv_shares(const AttnFwd& a) {
+int kv_shares(const AttnFwd& a, bool causal) {
   const int keys = a.dt ? bwd_keys<uint16_t>(a) : bwd_keys<float>(a);
   const long wgs = static_cast<long>((a.S + keys - 1) / keys) * a.B * a.Hk, rows = static_cast<long>(a.H / a.Hk) * a.T;
-  if (wgs == 0 || wgs >= kShareTarget || rows < 2 * kShareRows) return 1;
-  const long want = (kShareTarget + wgs - 1) / wgs, most = rows / kShareRows;
+  const long target = causal ? kShareTarget : kShareTarget / 2;
+  if (wgs == 0 || wgs >= target || rows < 2 * kShareRows) return 1;
+  const long want = (target + wgs - 1) / wgs, most = rows / kShareRows;
   return static_cast<int>(want < most ? want : most);
 }
 size_t kv_floats(const AttnFwd& a) {
-  const int n = kv_shares(a);
+  const int n = kv_shares(a, true);
   return n > 1 ? static_cast<size_t>(n) * a.B * a.Hk * a.S * kv_width(a) : 0;
 }
 
@@ -262,7 +263,7 @@ hipError_t launch_attention_bwd(const AttnBwd& g, void* ws, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (a.S > 0) {
-    const int n = attn::kv_shares(a);
+    const int n = attn::kv_shares(a, a.causal);
     e = a.dt ? attn::launch_bwd_kv<uint16_t>(g, stats, part, n, s) : attn::launch_bwd_kv<float>(g, stats, part, n, s);
     if (e == hipSuccess && n > 1) e = a.dt ? attn::add<uint16_t>(g, part, n, s) : attn::add<float>(g, part, n, s);
     if (e != hipSuccess) return e;

@@ -26,7 +26,8 @@ template <typename E, int MAPS, int DK, int DV, bool kWhole>
 __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a, Partial part) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
-  constexpr int D = DK / MAPS, KS = D / 32, VB = DV / 16, VLD = kTileLd<E, DV>;
+  typedef Tile<E, DV, false> VTile;
+  constexpr int D = DK / MAPS, KS = D / 32, VB = DV / 16, VLD = VTile::LD;
   constexpr int CE = 16 / static_cast<int>(sizeof(E)), CH = DV / CE;  // pieces of a value row
   constexpr int VR = 64 / CH > 0 ? 64 / CH : 1, VN = kKeys / VR;     // rows of one load of a wave, loads
   static_assert(CH <= 64, "a row per load");
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 #pragma unroll
     for (int vb = 0; vb < VB; ++vb) {
-      const Frag vf = cols_frag<E>(vs, VLD, 0, 16 * vb, lane);
+      const Frag vf = VTile::cols(vs, 0, 16 * vb, lane);
 #pragma unroll
       for (int m = 0; m < MAPS; ++m) o[m][vb] = X::mma(vf, pf[m], o[m][vb]);
     }
@@ -326,13 +327,19 @@ hipError_t append_by_width(const CacheAppend& a, hipStream_t s) {
   return append<E, 64>(a, s);
 }
 
-constexpr int kStepKeys = 256, kStepTarget = 1024;
+// Keys are split where the sequences and key heads alone give fewer than
+// kStepTarget / 2 workgroups (two fit on a compute unit), into ranges that take a
+// wave longer than the second launch: four tiles of bf16, two of fp32, whose
+// products are slower.  8 streams of 8 heads over 512 tokens bf16: one range
+// 14.6 us a call, two 18; 15 heads over 3001 tokens fp32: ranges of 256 tokens
+// 26.6 us, of 512 35, of 128 31.
+constexpr int kStepTarget = 1024;
 
 int step_splits(const AttnStep& a) {
-  const int blocks = (a.H / a.Hk + 15) / 16;
+  const int blocks = (a.H / a.Hk + 15) / 16, range = a.dt ? 512 : 256;
   const long wgs = static_cast<long>(a.B) * a.Hk * blocks, keys = static_cast<long>(a.max_pages) * a.page;
-  if (wgs >= kStepTarget / 2 || keys < 2 * kStepKeys) return 1;
-  const long want = kStepTarget / wgs, most = keys / kStepKeys;
+  if (wgs >= kStepTarget / 2 || keys < 2 * range) return 1;
+  const long want = kStepTarget / wgs, most = keys / range;
   return static_cast<int>(want < most ? want : most);
 }
 

@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.h"
 #include "gfx950.h"
 #include "vec_io.h"
@@ -43,42 +45,64 @@ struct Mma<float> {
   }
 };
 
-// Rows of DIM elements in LDS, kTileLd apart.  32 bytes (fp32: 16) more than the
-// row: with bf16 the 16-byte reads of 16 rows and the transposing reads then both
-// run at 210-220 bytes a clock and compute unit; with 16 bytes more at 120, with
-// none at 32 and 64.
-template <typename E, int DIM>
-constexpr int kTileLd = DIM + (sizeof(E) == 2 ? 16 : 4);
-
-// A[row][channels]: eight consecutive channels from c0 + 8 (lane / 16) of row lane % 16.
-template <typename E>
-__device__ __forceinline__ typename Mma<E>::Frag rows_frag(const E* tile, int ld, int row0, int c0, int lane) {
-  const E* p = tile + (row0 + (lane & 15)) * ld + c0 + 8 * (lane >> 4);
-  if constexpr (sizeof(E) == 2) {
-    return *reinterpret_cast<const bf16x8*>(p);
-  } else {
-    return Mma<float>::pack(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4));
+// A tile of rows of DIM elements in LDS, in one of two layouts.
+//   padded (kDma false): rows LD elements apart, 32 bytes (fp32: 16) more than
+//     the row.  With bf16 the 16-byte reads of 16 rows and the transposing reads
+//     then both run at 210-220 bytes a clock and compute unit; with 16 bytes more
+//     at 120, with none at 32 and 64.
+//   swizzled (kDma true, bf16): rows without a gap, as loads straight into LDS
+//     leave them, and the row's 16-byte pieces in another order: piece c of row r
+//     lies at place c ^ turn(r).  turn gives 16 rows 16 places (pairs of rows of 8
+//     pieces: 8 each), and eight neighbouring rows different pairs of places, so
+//     both kinds of reads meet every bank once, as in the padded layout.
+template <typename E, int DIM, bool kDma>
+struct Tile {
+  static constexpr int LD = DIM + (kDma ? 0 : sizeof(E) == 2 ? 16 : 4);
+  static constexpr int PIECES = DIM * static_cast<int>(sizeof(E)) / 16;
+  static_assert(!kDma || sizeof(E) == 2, "the swizzled layout is of bf16 rows");
+  static_assert(PIECES >= 8 && (PIECES & (PIECES - 1)) == 0, "a power of two of pieces");
+  __device__ __forceinline__ static int turn(int row) {
+    return PIECES >= 16 ? (row & 7) << 1 | (row >> 3 & 1) : (row >> 1 & 3) << 1 | (row >> 3 & 1);
   }
-}
 
-// A[channel][rows]: of channel c0 + lane % 16, the rows row0 + 4 (lane / 16) + 0..3 and those 16 further.
-template <typename E>
-__device__ __forceinline__ typename Mma<E>::Frag cols_frag(const E* tile, int ld, int row0, int c0, int lane) {
-  const int j = lane & 15, g = lane >> 4;
-  if constexpr (sizeof(E) == 2) {
-    const uint16_t* p = tile + (row0 + 4 * g + j / 4) * ld + c0 + 4 * (j % 4);
-    return join(lds_read_tr(p), lds_read_tr(p + 16 * ld));
-  } else {
-    const float* p = tile + (row0 + 4 * g) * ld + c0 + j;
-    f32x8 f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[e] = p[e * ld];
-      f[4 + e] = p[(16 + e) * ld];
+  // A[row][channels]: eight consecutive channels from c0 + 8 (lane / 16) of row row0 + lane % 16.
+  __device__ __forceinline__ static typename Mma<E>::Frag rows(const E* tile, int row0, int c0, int lane) {
+    const int r = lane & 15;
+    if constexpr (kDma) {
+      const int at = r * DIM + (((lane >> 4) ^ turn(r)) << 3);
+      return *reinterpret_cast<const bf16x8*>(tile + row0 * DIM + (at ^ c0));
+    } else {
+      const E* p = tile + (row0 + r) * LD + c0 + 8 * (lane >> 4);
+      if constexpr (sizeof(E) == 2) {
+        return *reinterpret_cast<const bf16x8*>(p);
+      } else {
+        return Mma<float>::pack(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4));
+      }
     }
-    return f;
   }
-}
+
+  // A[channel][rows]: of channel c0 + lane % 16, the rows row0 + 4 (lane / 16) + 0..3 and those 16 further.
+  __device__ __forceinline__ static typename Mma<E>::Frag cols(const E* tile, int row0, int c0, int lane) {
+    const int j = lane & 15, g = lane >> 4;
+    if constexpr (kDma) {
+      const int r = 4 * g + j / 4, at = r * DIM + (((j >> 1 & 1) ^ turn(r)) << 3) + 4 * (j & 1);
+      const uint16_t* p = tile + row0 * DIM + (at ^ c0);
+      return join(lds_read_tr(p), lds_read_tr(p + 16 * DIM));
+    } else if constexpr (sizeof(E) == 2) {
+      const uint16_t* p = tile + (row0 + 4 * g + j / 4) * LD + c0 + 4 * (j % 4);
+      return join(lds_read_tr(p), lds_read_tr(p + 16 * LD));
+    } else {
+      const float* p = tile + (row0 + 4 * g) * LD + c0 + j;
+      f32x8 f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[e] = p[e * LD];
+        f[4 + e] = p[(16 + e) * LD];
+      }
+      return f;
+    }
+  }
+};
 
 // A lane's 16 bytes of a row of n elements, nominally from element c on.
 // kWhole: rows end with a piece (n a multiple of CE); a piece behind the row
@@ -158,7 +182,7 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = piece.load(p, at[i] + part * static_cast<unsigned>(sizeof(E)), d);
   }
-  __device__ __forceinline__ void store(E* tile, int ld, int row0, int n) {
+  __device__ __forceinline__ void store(E* tile, int row0, int n) {
     if (row0 + ROWS > n) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -167,9 +191,107 @@ struct Stage {
     if (STEP > ROWS && row >= ROWS) return;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      *reinterpret_cast<u32x4*>(tile + (row + i * STEP) * ld + col) = piece.finish(r[i]);
+      *reinterpret_cast<u32x4*>(tile + (row + i * STEP) * Tile<E, MAPS * D, false>::LD + col) = piece.finish(r[i]);
   }
 };
+
+// Loads straight into LDS: lane l's BYTES (16 or 4) at p + off go to tile + l BYTES.
+// Written as assembly, without an output register, because the compiler would wait
+// for them to arrive in front of the next read of any tile; the wait is in
+// dma_barrier().  m0 holds the LDS address; the wait states cover m0, and the
+// pointer where it comes out of a vector register.
+template <int BYTES>
+__device__ __forceinline__ void load_to_lds(const void* p, unsigned off, const void* tile) {
+  static_assert(BYTES == 16 || BYTES == 4, "a piece or a word");
+  const unsigned at = static_cast<unsigned>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)(tile)));
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(p) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(p) : "memory", "m0");
+}
+
+// ROWS rows of MAPS parts of d elements (16-byte pieces at 16-byte addresses),
+// straight into a swizzled tile of MAPS D elements a row, by NW waves.  A wave's
+// load fills 64 places in a row; each lane picks the piece that belongs to its
+// place.  Rows from n on repeat the last, pieces behind a part the part's last:
+// they meet masked scores, or zeros in the other operand.  COUNT loads a wave.
+template <int ROWS, int MAPS, int D, int NW>
+struct Dma {
+  typedef Tile<uint16_t, MAPS * D, true> T;
+  static constexpr int COUNT = ROWS * T::PIECES / 64 / NW, STEP = NW * 64 / T::PIECES;  // rows of one round
+  static_assert(COUNT >= 1 && COUNT * NW * 64 == ROWS * T::PIECES, "every wave has as many loads");
+  int row;
+  unsigned piece[COUNT];  // bytes in front of the lane's pieces in their rows
+  __device__ __forceinline__ Dma(int d, int wave, int lane) : row((wave * 64 + lane) / T::PIECES) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      const int c = (lane % T::PIECES) ^ T::turn(row + i * STEP), map = c / (D / 8);
+      piece[i] = 2 * (map * d + min(8 * (c - map * (D / 8)), d - 8));
+    }
+  }
+  __device__ __forceinline__ void load(const uint16_t* base, long stride, int row0, int n, uint16_t* tile, int wave) const {
+    const uint16_t* p = base + row0 * stride;
+    const unsigned step = static_cast<unsigned>(stride) * 2;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+      load_to_lds<16>(p, static_cast<unsigned>(min(row + i * STEP, n - 1 - row0)) * step + piece[i],
+                      tile + (i * NW + wave) * 512);
+  }
+};
+
+// Workgroup barrier in front of a tile that was loaded straight into LDS: waits
+// until all but this wave's last LATER loads have arrived, and for its LDS reads.
+template <int LATER>
+__device__ __forceinline__ void dma_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATER) : "memory");
+}
+
+// Walks the tiles first..last-1 of a workgroup through LDS slots that loads fill
+// directly: request(i, slot) sends the loads of tile i, use(i, slot) works on it.
+// Three slots: one tile in use, one that has been on its way for a tile's time,
+// one that is requested now; two where three would keep a second workgroup off
+// the compute unit.  Every wave sends COUNT loads for every tile (behind the end
+// for the last again), so that the loads that may still be under way at a barrier
+// are a constant.  The slots are separate arrays and known in every call, which
+// lets the compiler see that reads of one do not wait for loads to another.
+template <int SLOTS, int COUNT, typename R, typename U>
+__device__ __forceinline__ void walk_tiles(int first, int last, R&& request, U&& use) {
+  typedef std::integral_constant<int, 0> C0;
+  typedef std::integral_constant<int, 1> C1;
+  typedef std::integral_constant<int, 2> C2;
+  if (first >= last) return;
+  request(first, C0());
+  if constexpr (SLOTS == 3) {
+    request(min(first + 1, last - 1), C1());
+    for (int i = first;; i += 3) {
+      dma_barrier<COUNT>();
+      request(min(i + 2, last - 1), C2());
+      use(i, C0());
+      if (i + 1 >= last) break;
+      dma_barrier<COUNT>();
+      request(min(i + 3, last - 1), C0());
+      use(i + 1, C1());
+      if (i + 2 >= last) break;
+      dma_barrier<COUNT>();
+      request(min(i + 4, last - 1), C1());
+      use(i + 2, C2());
+      if (i + 3 >= last) break;
+    }
+  } else {
+    for (int i = first;; i += 2) {
+      dma_barrier<0>();
+      request(min(i + 1, last - 1), C1());
+      use(i, C0());
+      if (i + 1 >= last) break;
+      dma_barrier<0>();
+      request(min(i + 2, last - 1), C0());
+      use(i + 1, C1());
+      if (i + 2 >= last) break;
+    }
+  }
+  dma_barrier<0>();  // nothing is on its way to LDS when the workgroup ends
+}
 
 // This wave's number in its workgroup, known to be the same in all its lanes.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6); }
