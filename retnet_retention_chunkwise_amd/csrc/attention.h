@@ -107,7 +107,7 @@ int fwd_rows(const AttnFwd& a);  // rows of a workgroup
 template <typename E>
 hipError_t launch_fwd(const AttnFwd& a, const Partial& part, hipStream_t s);
 template <typename E>
-hipError_t launch_bwd_q(const AttnBwd& a, const float* stats, float* lam_part, hipStream_t s);
+hipError_t launch_bwd_q(const AttnBwd& a, float* stats, float* lam_part, hipStream_t s);
 template <typename E>
 int bwd_rows(const AttnFwd& a);  // rows of a workgroup
 template <typename E>

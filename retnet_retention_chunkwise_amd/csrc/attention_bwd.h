@@ -15,7 +15,11 @@
 // The scores are computed twice (7 products in place of 5) so that every
 // gradient is summed by one wave in a fixed order: no atomics, the same bits
 // every time.  P and dS are rounded to the tensors' type as operands, all else
-// is fp32.
+// is fp32.  bf16 rounds o, so D from it is off by some 2^-9 of what dP - D
+// cancels from; where few keys share a row's weight that is much of what is
+// left (2 keys: up to a tenth of the gradient).  A wave whose rows all end in
+// their first tile of keys therefore takes D from the tile itself and leaves it
+// to the kv pass; with more keys the rounding of dS is as large.
 #pragma once
 
 #include "attention.h"
@@ -27,7 +31,7 @@ namespace attn {
 
 // stats: [M][B*H*T] of {lse log2 e, D}: first all of map 1.
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int KT>
-__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) void attention_bwd_q_kernel(AttnBwd g, const float2* __restrict__ stats,
+__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) void attention_bwd_q_kernel(AttnBwd g, float2* stats,
                                                                   float* __restrict__ lam_part, int tiles) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
@@ -125,6 +129,25 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
             for (int m = 0; m < MAPS; ++m)
               if (out) s[m][kb][n][r] = -INFINITY;
           }
+    }
+    if constexpr (sizeof(E) == 2) {
+      if (wmax <= KT) {  // few keys: D from this tile, the only one, for this pass and the next
+#pragma unroll
+        for (int m = 0; m < MAPS; ++m)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            float x = 0.0f;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                x = fmaf(fast_exp2(fmaf(s[m][kb][n][r], c, -st[m][n].x)), dp[kb][n][r], x);
+            x = row4_sum(x);
+            st[m][n].y = x;
+            const int t = w0 + 16 * n + col;
+            if (grp == 0 && t < a.T) stats[m * rows + static_cast<long>(bh) * a.T + t].y = x;
+          }
+      }
     }
 #pragma unroll
     for (int m = 0; m < MAPS; ++m) {
@@ -544,7 +567,7 @@ int bwd_rows(const AttnFwd& a) {
 }
 
 template <typename E>
-hipError_t launch_bwd_q(const AttnBwd& a, const float* stats, float* lam_part, hipStream_t s) {
+hipError_t launch_bwd_q(const AttnBwd& a, float* stats, float* lam_part, hipStream_t s) {
   return with_sizes(a.f, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
     constexpr bool W = decltype(whole)::value;
@@ -552,7 +575,7 @@ hipError_t launch_bwd_q(const AttnBwd& a, const float* stats, float* lam_part, h
     const int tiles = (a.f.T + C::TILE - 1) / C::TILE;
     hipLaunchKernelGGL((attention_bwd_q_kernel<E, M, DK, DV, W, C::NB, C::NW, C::STREAM>),
                        dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.H), dim3(64 * C::NW), 0, s, a,
-                       reinterpret_cast<const float2*>(stats), lam_part, tiles);
+                       reinterpret_cast<float2*>(stats), lam_part, tiles);
     return hipGetLastError();
   });
 }

@@ -24,8 +24,9 @@ def up(t):
     return None if t is None else t.detach().cpu().to(F64)
 
 
-def bounds(q, k, v, lam=None, causal=True, scale=None, offset=None, lens=None, grad_o=None):
-    """Errors allowed to o, lse, second and (with grad_o) grad_q, grad_k, grad_v, grad_lam, by name."""
+def bounds(q, k, v, lam=None, causal=True, scale=None, offset=None, lens=None, grad_o=None, few=False):
+    """Errors allowed to o, lse, second and (with grad_o) grad_q, grad_k, grad_v, grad_lam, by name.
+    few: no sequence has over 32 keys, so that D_m is sum A_m dP in fp32 and not from the rounded o and second."""
     dtype = q.dtype
     half, e = HALF[dtype], ROUND[dtype]
     q, k, v, lam, do = up(q), up(k), up(v), up(lam), up(grad_o)
@@ -82,6 +83,8 @@ def bounds(q, k, v, lam=None, causal=True, scale=None, offset=None, lens=None, g
             eD[0] = (g.abs() * (out["o"][b, h] + (dv + 8) * U * o[b, h].abs())).sum(-1, keepdim=True)
             if maps > 1:
                 eD[0] += abs(w[1]) * (eD[1] + 4 * U * D[1].abs()) + 4 * U * D[0].abs()
+            if few:
+                eD = [(A[i] * (dA[i] * dP.abs() + eP + (S + 8) * U * dP.abs())).sum(-1, keepdim=True) for i in range(maps)]
             W, eW = torch.zeros_like(dP), torch.zeros_like(dP)
             for i in range(maps):
                 p = slice(i * d, (i + 1) * d)

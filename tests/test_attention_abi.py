@@ -79,6 +79,7 @@ SIZES = [
     (dict(strides=st(Q, K, K, (512, 128, 15))), INVALID, "rows of o overlap"),
     (dict(strides=st(Q, K, K, (512, 0, 16))), INVALID, "rows of o overlap"),
     (dict(strides=st(Q, (256, -128, 16), K, Q)), INVALID, "stride"),
+    (dict(strides=st(Q, (1 << 28, 16, (1 << 24) + 1), K, Q)), UNSUPPORTED, "2^24"),
     (dict(strides=st(Q, K, (256, 1 << 47, 16), Q)), INVALID, "stride"),
     (dict(S=4096), INVALID, "workspace"),
     (dict(S=4096, ws=at(9), wsb=64), INVALID, "workspace"),
@@ -111,6 +112,7 @@ def bwd(lib, q=at(1), k=at(2), v=at(3), lam=at(4), lens=None, o=at(5), lse=at(6)
     (dict(gv=at(3)), INVALID, "overlaps"),
     (dict(gl=at(6, 16)), INVALID, "overlaps"),
     (dict(gq=at(7)), INVALID, "overlaps"),
+    (dict(strides=st((1 << 28, 16, 1 << 25), K, K, Q, Q, Q, K, K)), UNSUPPORTED, "2^24"),
     (dict(ws=None), INVALID, "workspace"),
     (dict(wsb=8), INVALID, "workspace"),
     (dict(ws=at(13, 4)), UNSUPPORTED, "aligned"),

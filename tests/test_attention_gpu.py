@@ -31,9 +31,9 @@ def dev(*ts):
     return [None if t is None else t.to(DEV) for t in ts]
 
 
-def check(name, q, k, v, lam, do, got, kept=None, grads=None, **mask):
+def check(name, q, k, v, lam, do, got, kept=None, grads=None, few=False, **mask):
     """got, kept, grads: what the calls returned, against the oracle's values."""
-    lim = bounds(q, k, v, lam, grad_o=do if grads is not None else None, **mask)
+    lim = bounds(q, k, v, lam, grad_o=do if grads is not None else None, few=few, **mask)
     o, lse, second = oracle.attention(q, k, v, lam, **mask)
     close(name + " o", got, o, lim["o"])
     if kept is not None:
@@ -107,6 +107,31 @@ def test_few_rows_over_many_keys(B, H, Hk, T, S, dk, dv, two, dtype):
     for mask in (dict(causal=True), dict(causal=False, lens=torch.tensor([S // 3] + [0] * (B - 1), dtype=torch.int32))):
         o, kept, grads = run(q, k, v, lam, do, **mask)
         check(name, q, k, v, lam, do, o, kept, grads, **mask)
+
+
+@pytest.mark.parametrize("two", [True, False])
+@pytest.mark.parametrize("T,S,d,dv,lens", [(1, 1, 64, 64, None), (2, 2, 64, 64, None), (3, 3, 96, 128, [3, 2]), (9, 9, 100, 36, None),
+                                           (32, 32, 128, 128, [32, 0]), (70, 31, 256, 256, None), (40, 100, 64, 64, [32, 7])])
+def test_gradients_over_few_keys(T, S, d, dv, lens, two):
+    """bf16 rows that see at most 32 keys: what dP - D leaves is not lost to the rounding of o."""
+    for causal in (True, False):
+        name = f"few T{T} S{S} dk{d} dv{dv} lens={lens} maps={1 + two} causal={causal}"
+        say(name)
+        q, k, v, lam, do = make(2, 4, 2, T, S, d, dv, BF16, two)
+        mask = dict(causal=causal, lens=None if lens is None else torch.tensor(lens, dtype=torch.int32))
+        o, kept, grads = run(q, k, v, lam, do, **mask)
+        check(name, q, k, v, lam, do, o, kept, grads, few=True, **mask)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,H,Hk,T,S,dk,dv,causal", [(1, 2, 1, 600, 40, 256, 256, False), (1, 3, 1, 520, 130, 60, 72, True)])
+def test_rows_shared_out(B, H, Hk, T, S, dk, dv, causal, dtype):
+    """Few keys that many rows see: the rows are shared out over workgroups and their sums added."""
+    say(f"shared out T{T} S{S} dk{dk} dv{dv} {dtype}")
+    for two in (True, False):
+        q, k, v, lam, do = make(B, H, Hk, T, S, dk, dv, dtype, two)
+        o, kept, grads = run(q, k, v, lam, do, causal=causal, offset=0)
+        check(f"shared out maps={1 + two}", q, k, v, lam, do, o, kept, grads, causal=causal, offset=0)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
