@@ -94,13 +94,16 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
     for (int kb = 0; kb < KB; ++kb) {
       Frag vf[VS];
 #pragma unroll
-      for (int e = 0; e < VS; ++e) vf[e] = VTile::rows(Vs, 16 * kb, 32 * e, lane);
+      for (int e = 0; e < VS; ++e)
+        if (!X::kSkip || 32 * e < a.dv) vf[e] = VTile::rows(Vs, 16 * kb, 32 * e, lane);
 #pragma unroll
       for (int n = 0; n < NB; ++n) dp[kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int e = 0; e < VS; ++e)
+      for (int e = 0; e < VS; ++e) {
+        if (X::kSkip && 32 * e >= a.dv) break;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) dp[kb][n] = X::mma(vf[e], gf[n][e], dp[kb][n]);
+        for (int n = 0; n < NB; ++n) dp[kb][n] = X::mma(vf[e], gf[n][e], dp[kb][n], a.dv - 32 * e);
+      }
     }
 #pragma unroll
     for (int m = 0; m < MAPS; ++m)
@@ -108,13 +111,16 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
       for (int kb = 0; kb < KB; ++kb) {
         Frag kf[KS];
 #pragma unroll
-        for (int e = 0; e < KS; ++e) kf[e] = KTile::rows(Ks, 16 * kb, m * D + 32 * e, lane);
+        for (int e = 0; e < KS; ++e)
+          if (!X::kSkip || 32 * e < a.d) kf[e] = KTile::rows(Ks, 16 * kb, m * D + 32 * e, lane);
 #pragma unroll
         for (int n = 0; n < NB; ++n) s[m][kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < KS; ++e)
+        for (int e = 0; e < KS; ++e) {
+          if (X::kSkip && 32 * e >= a.d) break;
 #pragma unroll
-          for (int n = 0; n < NB; ++n) s[m][kb][n] = X::mma(kf[e], qf[n][m * KS + e], s[m][kb][n]);
+          for (int n = 0; n < NB; ++n) s[m][kb][n] = X::mma(kf[e], qf[n][m * KS + e], s[m][kb][n], a.d - 32 * e);
+        }
       }
     products_done();
     if (k0 + KT > wall) {  // some row does not see some key
@@ -169,6 +175,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
         for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[m][2 * j][n], s[m][2 * j + 1][n]);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
+          if (X::kSkip && 16 * cb >= a.d) break;
           const Frag kt = KTile::cols(Ks, 32 * j, m * D + 16 * cb, lane);
 #pragma unroll
           for (int n = 0; n < NB; ++n) dq[m][cb][n] = X::mma(kt, ds[n], dq[m][cb][n]);
@@ -325,11 +332,13 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
 #pragma unroll
         for (int n = 0; n < NB; ++n) s[m][qb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < KS; ++e)
+        for (int e = 0; e < KS; ++e) {
+          if (X::kSkip && 32 * e >= a.d) break;
 #pragma unroll
           for (int n = 0; n < NB; ++n)
             s[m][qb][n] = X::mma(get(qa[m][qb][e], [&] { return QTile::rows(Qs, 16 * qb, m * D + 32 * e, lane); }),
-                                 kf[n][m * KS + e], s[m][qb][n]);
+                                 kf[n][m * KS + e], s[m][qb][n], a.d - 32 * e);
+        }
       }
     };
     auto mask = [&]() {
@@ -379,11 +388,13 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
 #pragma unroll
         for (int n = 0; n < NB; ++n) ds[n] = X::pack(s[m][2 * j][n], s[m][2 * j + 1][n]);
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
+        for (int cb = 0; cb < CB; ++cb) {
+          if (X::kSkip && 16 * cb >= a.d) break;
 #pragma unroll
-          for (int n = 0; n < NB; ++n) 
+          for (int n = 0; n < NB; ++n)
             dk[m][cb][n] = X::mma(get(qc[m][j][cb], [&] { return QTile::cols(Qs, 32 * j, m * D + 16 * cb, lane); }),
                                   ds[n], dk[m][cb][n]);
+        }
       }
     };
     if constexpr (kAhead) {
@@ -400,10 +411,13 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
 #pragma unroll
       for (int n = 0; n < NB; ++n) dp[qb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int e = 0; e < VS; ++e)
+      for (int e = 0; e < VS; ++e) {
+        if (X::kSkip && 32 * e >= a.dv) break;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
-          dp[qb][n] = X::mma(get(ga[qb][e], [&] { return GTile::rows(Gs, 16 * qb, 32 * e, lane); }), vf[n][e], dp[qb][n]);
+          dp[qb][n] = X::mma(get(ga[qb][e], [&] { return GTile::rows(Gs, 16 * qb, 32 * e, lane); }), vf[n][e], dp[qb][n],
+                             a.dv - 32 * e);
+      }
     }
     stage_border<E>();
     if constexpr (MAPS > 1) read_q(1);
@@ -457,12 +471,14 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
 #pragma unroll
       for (int j = 0; j < QT / 32; ++j)
 #pragma unroll
-        for (int vb = 0; vb < VG; ++vb)
+        for (int vb = 0; vb < VG; ++vb) {
+          if (X::kSkip && 16 * (v0 + vb) >= a.dv) break;
 #pragma unroll
           for (int n = 0; n < NB; ++n)
             dv[v0 + vb][n] = X::mma(
                 get(gc[v0 / VG & 1][j][vb], [&] { return GTile::cols(Gs, 32 * j, 16 * (v0 + vb), lane); }), pf[j][n],
                 dv[v0 + vb][n]);
+        }
     }
     products_done();
   };

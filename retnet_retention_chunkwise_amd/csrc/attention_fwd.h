@@ -91,13 +91,16 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (MAPS == 1 || DV < 256)
       for (int kb = 0; kb < KB; ++kb) {
         Frag kf[KS];
 #pragma unroll
-        for (int e = 0; e < KS; ++e) kf[e] = KTile::rows(Ks, 16 * kb, m * D + 32 * e, lane);
+        for (int e = 0; e < KS; ++e)
+          if (!X::kSkip || 32 * e < a.d) kf[e] = KTile::rows(Ks, 16 * kb, m * D + 32 * e, lane);
 #pragma unroll
         for (int n = 0; n < NB; ++n) s[m][kb][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < KS; ++e)
+        for (int e = 0; e < KS; ++e) {
+          if (X::kSkip && 32 * e >= a.d) break;
 #pragma unroll
-          for (int n = 0; n < NB; ++n) s[m][kb][n] = X::mma(kf[e], qf[n][m * KS + e], s[m][kb][n]);
+          for (int n = 0; n < NB; ++n) s[m][kb][n] = X::mma(kf[e], qf[n][m * KS + e], s[m][kb][n], a.d - 32 * e);
+        }
       }
     products_done();
     if (k0 + KT > wall) {  // some row does not see some key
@@ -161,6 +164,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (MAPS == 1 || DV < 256)
     for (int j = 0; j < KT / 32; ++j)
 #pragma unroll
       for (int vb = 0; vb < VB; ++vb) {
+        if (X::kSkip && 16 * vb >= a.dv) break;
         const Frag vf = VTile::cols(Vs, 32 * j, 16 * vb, lane);
 #pragma unroll
         for (int m = 0; m < MAPS; ++m)

@@ -81,7 +81,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   unsigned ok = 0;
   const int vrow = lane / CH, vchunk = (lane % CH) * CE;
   const Piece16<E, kWhole> vpiece(vchunk, a.dv);
-  auto kpiece = [&](int e, int i) { return Piece16<E, kWhole>(32 * (e % KS) + 8 * grp + i * CE, a.d); };
+  auto kpiece = [&](int e, int i) { return Piece16<E, kWhole>(32 * (e % KS) + CE * grp + 16 * i, a.d); };
   auto load = [&](int tile) {
     // lane j finds key j's rows; a key without a page (or behind the last) is
     // masked, and the new token's rows are read in its place
@@ -129,12 +129,14 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
         s[m][kb] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int e = m * KS; e < (m + 1) * KS; ++e) {
+          const int left = a.d - 32 * (e - m * KS);
+          if (X::kSkip && left <= 0) break;
           u32x4 x[KP];
 #pragma unroll
           for (int j = 0; j < KP; ++j) x[j] = kpiece(e, j).finish(kr[kb][e][j]);
           Frag kf;
           __builtin_memcpy(&kf, x, sizeof(kf));
-          s[m][kb] = X::mma(kf, qf[e], s[m][kb]);
+          s[m][kb] = X::mma(kf, qf[e], s[m][kb], left);
         }
       }
     const unsigned seen = ok;
@@ -181,6 +183,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 #pragma unroll
     for (int vb = 0; vb < VB; ++vb) {
+      if (X::kSkip && 16 * vb >= a.dv) break;
       const Frag vf = VTile::cols(vs, 0, 16 * vb, lane);
 #pragma unroll
       for (int m = 0; m < MAPS; ++m) o[m][vb] = X::mma(vf, pf[m], o[m][vb]);

@@ -28,16 +28,24 @@ struct Mma;
 template <>
 struct Mma<uint16_t> {
   typedef bf16x8 Frag;
-  __device__ __forceinline__ static f32x4 mma(Frag a, Frag b, f32x4 c) { return mfma(a, b, c); }
+  static constexpr bool kSkip = false;
+  __device__ __forceinline__ static f32x4 mma(Frag a, Frag b, f32x4 c, int = 32) { return mfma(a, b, c); }
   // Two accumulators as an operand along their rows (round to nearest even).
   __device__ __forceinline__ static Frag pack(f32x4 lo, f32x4 hi) { return pack_bf16x8(lo, hi); }
 };
 template <>
 struct Mma<float> {
   typedef f32x8 Frag;
-  __device__ __forceinline__ static f32x4 mma(Frag a, Frag b, f32x4 c) {
+  // A block of 16 channels is four instructions of 32 clocks: kernels leave out
+  // those behind the row (a uniform branch each), n of a product's 32 counting.
+  static constexpr bool kSkip = true;
+  __device__ __forceinline__ static f32x4 mma(Frag a, Frag b, f32x4 c, int n = 32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    if (n > 16) {
+#pragma unroll
+      for (int i = 4; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    }
     return c;
   }
   __device__ __forceinline__ static Frag pack(f32x4 lo, f32x4 hi) {
@@ -65,18 +73,19 @@ struct Tile {
     return PIECES >= 16 ? (row & 7) << 1 | (row >> 3 & 1) : (row >> 1 & 3) << 1 | (row >> 3 & 1);
   }
 
-  // A[row][channels]: eight consecutive channels from c0 + 8 (lane / 16) of row row0 + lane % 16.
+  // A[row][channels] of row row0 + lane % 16: bf16 the eight channels from c0 + 8 (lane / 16),
+  // fp32 the four from c0 + 4 (lane / 16) and those 16 further.
   __device__ __forceinline__ static typename Mma<E>::Frag rows(const E* tile, int row0, int c0, int lane) {
     const int r = lane & 15;
     if constexpr (kDma) {
       const int at = r * DIM + (((lane >> 4) ^ turn(r)) << 3);
       return *reinterpret_cast<const bf16x8*>(tile + row0 * DIM + (at ^ c0));
     } else {
-      const E* p = tile + (row0 + r) * LD + c0 + 8 * (lane >> 4);
+      const E* p = tile + (row0 + r) * LD + c0 + 16 / static_cast<int>(sizeof(E)) * (lane >> 4);
       if constexpr (sizeof(E) == 2) {
         return *reinterpret_cast<const bf16x8*>(p);
       } else {
-        return Mma<float>::pack(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4));
+        return Mma<float>::pack(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16));
       }
     }
   }
@@ -305,11 +314,11 @@ __device__ __forceinline__ void load_columns(const E* row, bool in, int d, int l
   constexpr int CE = 16 / static_cast<int>(sizeof(E));
 #pragma unroll
   for (int k = 0; k < MAPS * D / 32; ++k) {
-    const int map = k / (D / 32), c = (k - map * (D / 32)) * 32 + 8 * (lane >> 4);
+    const int map = k / (D / 32), c = (k - map * (D / 32)) * 32 + CE * (lane >> 4);
     u32x4 x[8 / CE];
 #pragma unroll
     for (int i = 0; i < 8 / CE; ++i) {
-      const Piece16<E, kWhole> piece(c + i * CE, d);
+      const Piece16<E, kWhole> piece(c + i * 16, d);
       x[i] = piece.zero_behind(piece.finish(piece.load(reinterpret_cast<const char*>(row + map * d), 0, d)));
       if (!in) x[i] = u32x4{0, 0, 0, 0};
     }
