@@ -106,8 +106,9 @@ template <typename E>
 int fwd_rows(const AttnFwd& a);  // rows of a workgroup
 template <typename E>
 hipError_t launch_fwd(const AttnFwd& a, const Partial& part, hipStream_t s);
+// shares > 1: every share of the keys leaves its sums in part
 template <typename E>
-hipError_t launch_bwd_q(const AttnBwd& a, float* stats, float* lam_part, hipStream_t s);
+hipError_t launch_bwd_q(const AttnBwd& a, float* stats, float* lam_part, float* part, int shares, hipStream_t s);
 template <typename E>
 int bwd_rows(const AttnFwd& a);  // rows of a workgroup
 template <typename E>

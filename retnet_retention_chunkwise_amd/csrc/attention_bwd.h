@@ -32,7 +32,8 @@ namespace attn {
 // stats: [M][B*H*T] of {lse log2 e, D}: first all of map 1.
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int KT>
 __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) void attention_bwd_q_kernel(AttnBwd g, float2* stats,
-                                                                  float* __restrict__ lam_part, int tiles) {
+                                                                  float* __restrict__ lam_part, float* __restrict__ part,
+                                                                  int tiles, int shares) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
   constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
@@ -53,7 +54,10 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
   const int len = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
   auto seen = [&](int t) { return a.causal ? min(max(t + a.offset + 1, 0), len) : len; };
   const int q0 = tile * QT, w0 = q0 + wave * 16 * NB;
-  const int last = (seen(min(q0 + QT, a.T) - 1) + KT - 1) / KT;
+  // this workgroup's share of the rows' tiles of keys
+  const int share = blockIdx.y, all = (seen(min(q0 + QT, a.T) - 1) + KT - 1) / KT;
+  const int first = static_cast<int>(static_cast<long>(all) * share / shares);
+  const int last = static_cast<int>(static_cast<long>(all) * (share + 1) / shares);
   const int wmax = w0 < a.T ? seen(min(w0 + 16 * NB, a.T) - 1) : 0, wall = seen(w0);
 
   const E* q = static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h;
@@ -190,7 +194,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
     const Dma<KT, 1, DV, NW> vd(a.dv, wave, lane);
     E *const Kt[] = {K0, K1, K2}, *const Vt[] = {V0, V1, V2};
     walk_tiles<SLOTS, kd.COUNT + vd.COUNT>(
-        0, last,
+        first, last,
         [&](int i, auto slot) __attribute__((always_inline)) {
           kd.load(k, a.sk.t, i * KT, len, Kt[slot], wave);
           vd.load(v, a.sv.t, i * KT, len, Vt[slot], wave);
@@ -207,12 +211,12 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
       ks.store(i & 1 ? K1 : K0, i * KT, len);
       vs.store(i & 1 ? V1 : V0, i * KT, len);
     };
-    if (last > 0) {
-      load(0);
-      store(0);
-      if (last > 1) load(1);
+    if (first < last) {
+      load(first);
+      store(first);
+      if (first + 1 < last) load(first + 1);
     }
-    for (int i = 0; i < last; ++i) {
+    for (int i = first; i < last; ++i) {
       lds_barrier();
       if (i + 1 < last) {
         store(i + 1);
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
       float x = 0.0f;
 #pragma unroll
       for (int i = 0; i < NW; ++i) x += wave_lam[i];
-      lam_part[(static_cast<long>(b) * tiles + tile) * a.H + h] = -x;
+      lam_part[((static_cast<long>(b) * tiles + tile) * shares + share) * a.H + h] = -x;
     }
   }
 #pragma unroll
@@ -238,9 +242,16 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
     const int t = w0 + 16 * n + col;
     if (t >= a.T) continue;
     E* out = static_cast<E*>(g.grad_q) + b * g.sdq.b + h * g.sdq.h + t * g.sdq.t;
+    const int d4 = (a.d + 3) & ~3;
+    float* to = part + (share * rows + static_cast<long>(bh) * a.T + t) * (MAPS * d4);
 #pragma unroll
     for (int m = 0; m < MAPS; ++m) {
       const float f = m == 0 ? a.scale : -a.lam[h] * a.scale;
+      if (shares > 1) {  // fp32 sums of the share, [share][b, h, row][MAPS d4]
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) store4<float, true>(to + m * d4, 16 * cb + 4 * grp, d4, dq[m][cb][n] * f);
+        continue;
+      }
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) store4<E, kWhole>(out + m * a.d, 16 * cb + 4 * grp, a.d, dq[m][cb][n] * f);
     }
@@ -583,15 +594,15 @@ int bwd_rows(const AttnFwd& a) {
 }
 
 template <typename E>
-hipError_t launch_bwd_q(const AttnBwd& a, float* stats, float* lam_part, hipStream_t s) {
+hipError_t launch_bwd_q(const AttnBwd& a, float* stats, float* lam_part, float* part, int shares, hipStream_t s) {
   return with_sizes(a.f, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
     constexpr bool W = decltype(whole)::value;
     typedef BwdShape<E, DK> C;
     const int tiles = (a.f.T + C::TILE - 1) / C::TILE;
     hipLaunchKernelGGL((attention_bwd_q_kernel<E, M, DK, DV, W, C::NB, C::NW, C::STREAM>),
-                       dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.H), dim3(64 * C::NW), 0, s, a,
-                       reinterpret_cast<float2*>(stats), lam_part, tiles);
+                       dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.H, shares), dim3(64 * C::NW), 0, s, a,
+                       reinterpret_cast<float2*>(stats), lam_part, part, tiles, shares);
     return hipGetLastError();
   });
 }

@@ -2,6 +2,8 @@
 // keys and the backward's row statistics.  Both are bound by memory.
 #include "attention.h"
 
+#include <algorithm>
+
 #include "attention_tiles.h"
 #include "row_sum.h"
 
@@ -36,60 +38,77 @@ __device__ __forceinline__ void put4(E* row, int c, int n, f32x4 x) {
     store4<E, false>(row, c, n, x);
 }
 
-// A workgroup per row; lanes along the channels, four each, and waves along the
-// shares.  The shares' outputs o_i with maxima m_i and sums l_i join as
+// WPR waves per row, along the shares; lanes along the channels, four each.  The
+// shares' outputs o_i with maxima m_i and sums l_i join as
 // sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i, the waves' sums in wave order.
-template <typename E, int MAPS>
+template <typename E, int MAPS, int WPR>
 __global__ __launch_bounds__(64 * kWaves) void attention_join_kernel(AttnFwd a, Partial p, long rows) {
-  __shared__ float tops[kWaves][MAPS], sums[kWaves][MAPS];
-  __shared__ f32x4 outs[kWaves][MAPS][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = 4 * lane;
-  const long row = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = wave_id() % WPR, ch = 4 * lane;
+  const long row = static_cast<long>(blockIdx.x) * (kWaves / WPR) + wave_id() / WPR;
+  if (row >= rows) return;  // with a wave per row, which meets no barrier
   const int t = static_cast<int>(row % a.T), dv4 = (a.dv + 3) & ~3;
   const long bh = row / a.T;
   const int h = static_cast<int>(bh % a.H), b = static_cast<int>(bh / a.H);
   const float2* ml = reinterpret_cast<const float2*>(p.ml);
-  // this wave's shares: wave, wave + kWaves, ..., one maximum a lane to begin with
+  f32x4 y[MAPS];
+  float tops[MAPS], sums[MAPS];
+  // this wave's shares: wave, wave + WPR, ..., one maximum a lane to begin with
 #pragma unroll
   for (int m = 0; m < MAPS; ++m) {
     float top = -INFINITY;
-    for (int i = wave + kWaves * lane; i < p.nsplit; i += kWaves * 64) top = fmaxf(top, ml[(i * rows + row) * MAPS + m].x);
+    for (int i = wave + WPR * lane; i < p.nsplit; i += WPR * 64) top = fmaxf(top, ml[(i * rows + row) * MAPS + m].x);
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
     const float at = top == -INFINITY ? 0.0f : top;
     float l = 0.0f;
     f32x4 x = {0, 0, 0, 0};
 #pragma unroll 4
-    for (int i = wave; i < p.nsplit; i += kWaves) {
+    for (int i = wave; i < p.nsplit; i += WPR) {
       const long j = (i * rows + row) * MAPS + m;
       const float2 s = ml[j];
-      f32x4 y = {0, 0, 0, 0};
-      if (ch < dv4) y = *reinterpret_cast<const f32x4*>(p.out + j * dv4 + ch);
+      f32x4 z = {0, 0, 0, 0};
+      if (ch < dv4) z = *reinterpret_cast<const f32x4*>(p.out + j * dv4 + ch);
       const float f = fast_exp2(s.x - at);
       l = fmaf(s.y, f, l);
-      x += y * f;
+      x += z * f;
     }
-    if (lane == 0) {
-      tops[wave][m] = top;
-      sums[wave][m] = l;
-    }
-    outs[wave][m][lane] = x;
+    tops[m] = top;
+    sums[m] = l;
+    y[m] = x;
   }
-  __syncthreads();
-  if (wave != 0) return;
-  f32x4 y[MAPS];
+  if constexpr (WPR > 1) {
+    __shared__ float wave_top[WPR][MAPS], wave_sum[WPR][MAPS];
+    __shared__ f32x4 wave_out[WPR][MAPS][64];
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+      if (lane == 0) {
+        wave_top[wave][m] = tops[m];
+        wave_sum[wave][m] = sums[m];
+      }
+      wave_out[wave][m][lane] = y[m];
+    }
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int m = 0; m < MAPS; ++m) {
+      float top = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) top = fmaxf(top, wave_top[w][m]);
+      f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) {
+        const float f = wave_top[w][m] == -INFINITY ? 0.0f : fast_exp2(wave_top[w][m] - top);
+        l = fmaf(wave_sum[w][m], f, l);
+        x += wave_out[w][m][lane] * f;
+      }
+      tops[m] = top;
+      sums[m] = l;
+      y[m] = x;
+    }
+  }
 #pragma unroll
   for (int m = 0; m < MAPS; ++m) {
-    float top = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][m]);
-    y[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = tops[w][m] == -INFINITY ? 0.0f : fast_exp2(tops[w][m] - top);
-      l = fmaf(sums[w][m], f, l);
-      y[m] += outs[w][m][lane] * f;
-    }
+    const float top = tops[m], l = sums[m];
     y[m] *= l == 0.0f ? 0.0f : 1.0f / l;
     if (a.lse != nullptr && lane == 0)
       a.lse[(bh * MAPS + m) * a.T + t] = l == 0.0f ? -INFINITY : top * kLn2 + logf(l);
@@ -153,12 +172,40 @@ __global__ __launch_bounds__(64 * kWaves) void attention_add_kernel(AttnBwd g, c
   }
 }
 
+// grad_q from the shares' sums [share][row][MAPS d4], likewise: a thread per four
+// channels of a row (b, h, t).
+template <typename E, int MAPS>
+__global__ __launch_bounds__(64 * kWaves) void attention_add_q_kernel(AttnBwd g, const float* __restrict__ part, int shares,
+                                                                      long rows) {
+  const AttnFwd& a = g.f;
+  const int d4 = (a.d + 3) & ~3, width = MAPS * d4, per = width / 4;
+  const long at = static_cast<long>(blockIdx.x) * (64 * kWaves) + threadIdx.x, row = at / per;
+  if (row >= rows) return;
+  const int c = 4 * static_cast<int>(at % per), m = MAPS > 1 && c >= d4;
+  f32x4 x = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int i = 0; i < shares; ++i) x += *reinterpret_cast<const f32x4*>(part + (i * rows + row) * width + c);
+  const int t = static_cast<int>(row % a.T);
+  const long bh = row / a.T;
+  const int h = static_cast<int>(bh % a.H), b = static_cast<int>(bh / a.H);
+  put4<E>(static_cast<E*>(g.grad_q) + b * g.sdq.b + h * g.sdq.h + t * g.sdq.t + m * a.d, c - m * d4, a.d, x);
+}
+
 int kv_width(const AttnFwd& a) { return a.maps() * ((a.d + 3) & ~3) + ((a.dv + 3) & ~3); }
 
 template <typename E>
 hipError_t add(const AttnBwd& g, const float* part, int shares, hipStream_t s) {
   const long rows = static_cast<long>(g.f.B) * g.f.Hk * g.f.S, n = rows * (kv_width(g.f) / 4);
   auto* kern = g.f.maps() > 1 ? attention_add_kernel<E, 2> : attention_add_kernel<E, 1>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((n + 64 * kWaves - 1) / (64 * kWaves))), dim3(64 * kWaves), 0, s, g,
+                     part, shares, rows);
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t add_q(const AttnBwd& g, const float* part, int shares, hipStream_t s) {
+  const long rows = static_cast<long>(g.f.B) * g.f.H * g.f.T, n = rows * g.f.maps() * ((g.f.d + 3) / 4);
+  auto* kern = g.f.maps() > 1 ? attention_add_q_kernel<E, 2> : attention_add_q_kernel<E, 1>;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((n + 64 * kWaves - 1) / (64 * kWaves))), dim3(64 * kWaves), 0, s, g,
                      part, shares, rows);
   return hipGetLastError();
@@ -179,38 +226,54 @@ hipError_t stats(const AttnBwd& g, float* to, hipStream_t s) {
   return stats_by_width<E, 64>(g, to, s);
 }
 
+template <typename E, int WPR>
+hipError_t join_by(const AttnFwd& a, const Partial& p, hipStream_t s) {
+  const long rows = static_cast<long>(a.B) * a.H * a.T, per = kWaves / WPR;
+  auto* kern = a.maps() > 1 ? attention_join_kernel<E, 2, WPR> : attention_join_kernel<E, 1, WPR>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(64 * kWaves), 0, s, a, p, rows);
+  return hipGetLastError();
+}
 template <typename E>
 hipError_t join(const AttnFwd& a, const Partial& p, hipStream_t s) {
-  const long rows = static_cast<long>(a.B) * a.H * a.T;
-  auto* kern = a.maps() > 1 ? attention_join_kernel<E, 2> : attention_join_kernel<E, 1>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(rows)), dim3(64 * kWaves), 0, s, a, p, rows);
-  return hipGetLastError();
+  // one wave reads a row's few shares as fast as four, which then wait for each other
+  return p.nsplit > 8 ? join_by<E, kWaves>(a, p, s) : join_by<E, 1>(a, p, s);
 }
 
 long rows_of(const AttnFwd& a) { return static_cast<long>(a.B) * a.H * a.T; }
 
 // Keys are split where the tiles of rows alone are too few to fill the device's
-// 256 compute units, into ranges of at least kSplitKeys keys.
-constexpr int kSplitKeys = 256, kSplitTarget = 512;
+// 256 compute units, into ranges of at least kRange keys, so that about
+// kSplitTarget workgroups share them.  A tile of 32 keys takes a workgroup 1 us
+// (fp32 2.6), a second kernel about 4: sequences of fewer than 512 keys (fp32
+// 256) are left whole.  Measured, whole against split: B1 H4 T1000 d128 bf16
+// training pass 109 and 75 us, B1 H4/2 T1000 d64 fp32 144 and 87, but B1 H4 T300
+// d128 bf16 forward 13 and 17.
+constexpr int kRange = 128, kSplitTarget = 512;
 
-int fwd_splits(const AttnFwd& a) {
-  const int rows = a.dt ? fwd_rows<uint16_t>(a) : fwd_rows<float>(a);
+int key_ranges(const AttnFwd& a, int rows) {  // for tiles of so many rows
   const long wgs = static_cast<long>((a.T + rows - 1) / rows) * a.B * a.H;
-  if (wgs == 0 || wgs >= kSplitTarget / 2 || a.S < 2 * kSplitKeys) return 1;
-  const long want = kSplitTarget / wgs, most = a.S / kSplitKeys;
+  if (wgs == 0 || wgs >= kSplitTarget / 2 || a.S < kRange * (a.dt ? 4 : 2)) return 1;
+  const long want = kSplitTarget / wgs, most = a.S / kRange;
   return static_cast<int>(want < most ? want : most);
 }
+int fwd_splits(const AttnFwd& a) { return key_ranges(a, a.dt ? fwd_rows<uint16_t>(a) : fwd_rows<float>(a)); }
+int q_shares(const AttnFwd& a) { return key_ranges(a, a.dt ? bwd_rows<uint16_t>(a) : bwd_rows<float>(a)); }
+size_t q_floats(const AttnFwd& a) {
+  const int n = q_shares(a);
+  return n > 1 ? static_cast<size_t>(n) * rows_of(a) * a.maps() * ((a.d + 3) & ~3) : 0;
+}
 
-int lam_rows(const AttnFwd& a) {  // tiles of the q pass
+int lam_rows(const AttnFwd& a) {  // workgroups of the q pass, of a head
   const int rows = a.dt ? bwd_rows<uint16_t>(a) : bwd_rows<float>(a);
-  return a.B * ((a.T + rows - 1) / rows);
+  return a.B * ((a.T + rows - 1) / rows) * q_shares(a);
 }
 
 // The kv pass gives every tile of keys to one workgroup, or to several that share
 // the rows: two fit on each of the 256 compute units, and with a causal mask,
 // whose tiles differ in length, twice as many even them out.  A share has at
-// least kShareRows rows.
-constexpr int kShareTarget = 1024, kShareRows = 256;
+// least kShareRows rows (256 in place of 128: B3 H6/2 T501 fp32 training pass 153
+// us and 136, B2 H8/2 T500 d128 bf16 84 and 80).
+constexpr int kShareTarget = 1024, kShareRows = 128;
 
 int kv_shares(const AttnFwd& a, bool causal) {
   const int keys = a.dt ? bwd_keys<uint16_t>(a) : bwd_keys<float>(a);
@@ -224,6 +287,9 @@ size_t kv_floats(const AttnFwd& a) {
   const int n = kv_shares(a, true);
   return n > 1 ? static_cast<size_t>(n) * a.B * a.Hk * a.S * kv_width(a) : 0;
 }
+
+// the shares' sums, of the q pass and then of the kv pass
+size_t part_floats(const AttnFwd& a) { return std::max(q_floats(a), kv_floats(a)); }
 
 size_t stats_floats(const AttnFwd& a) { return (static_cast<size_t>(rows_of(a)) * a.maps() * 2 + 3) & ~static_cast<size_t>(3); }
 
@@ -240,7 +306,7 @@ size_t attention_fwd_workspace(const AttnFwd& a) {
 }
 
 size_t attention_bwd_workspace(const AttnFwd& a) {
-  return 4 * (attn::stats_floats(a) + attn::kv_floats(a) + (a.maps() > 1 ? static_cast<size_t>(attn::lam_rows(a)) * a.H : 0));
+  return 4 * (attn::stats_floats(a) + attn::part_floats(a) + (a.maps() > 1 ? static_cast<size_t>(attn::lam_rows(a)) * a.H : 0));
 }
 
 hipError_t launch_attention_fwd(const AttnFwd& a, void* ws, hipStream_t s) {
@@ -254,12 +320,14 @@ hipError_t launch_attention_bwd(const AttnBwd& g, void* ws, hipStream_t s) {
   const AttnFwd& a = g.f;
   float* stats = static_cast<float*>(ws);
   float* part = stats + attn::stats_floats(a);
-  float* lam_part = part + attn::kv_floats(a);
+  float* lam_part = part + attn::part_floats(a);
   hipError_t e = hipSuccess;
   if (a.T > 0) {
     e = a.dt ? attn::stats<uint16_t>(g, stats, s) : attn::stats<float>(g, stats, s);
     if (e != hipSuccess) return e;
-    e = a.dt ? attn::launch_bwd_q<uint16_t>(g, stats, lam_part, s) : attn::launch_bwd_q<float>(g, stats, lam_part, s);
+    const int n = attn::q_shares(a);
+    e = a.dt ? attn::launch_bwd_q<uint16_t>(g, stats, lam_part, part, n, s) : attn::launch_bwd_q<float>(g, stats, lam_part, part, n, s);
+    if (e == hipSuccess && n > 1) e = a.dt ? attn::add_q<uint16_t>(g, part, n, s) : attn::add_q<float>(g, part, n, s);
     if (e != hipSuccess) return e;
   }
   if (a.S > 0) {

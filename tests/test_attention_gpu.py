@@ -97,7 +97,7 @@ def test_matches_oracle(B, H, Hk, T, S, dk, dv, dtype, two, causal):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("two", [True, False])
 @pytest.mark.parametrize("B,H,Hk,T,S,dk,dv", [(1, 2, 1, 1, 700, 64, 64), (2, 4, 2, 16, 2049, 32, 40), (1, 1, 1, 3, 1024, 128, 128),
-                                              (1, 2, 2, 70, 1500, 128, 256)])
+                                              (1, 2, 2, 70, 1500, 128, 256), (2, 2, 1, 300, 530, 100, 72)])
 def test_few_rows_over_many_keys(B, H, Hk, T, S, dk, dv, two, dtype):
     """The keys are split over workgroups and joined."""
     name = f"split B{B} H{H}/{Hk} T{T} S{S} dk{dk} dv{dv} {dtype} maps={1 + two}"
