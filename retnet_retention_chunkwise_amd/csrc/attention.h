@@ -134,6 +134,8 @@ auto with_sizes(const A& a, F&& f) {
     }
     if (dk <= 64 && a.dv <= 64) return f(maps, N64(), N64(), std::true_type());
     if (dk <= 128 && a.dv <= 128) return f(maps, N128(), N128(), std::true_type());
+    if (a.dv <= 128) return f(maps, N256(), N128(), std::true_type());
+    if (dk <= 128) return f(maps, N128(), N256(), std::true_type());
     return f(maps, N256(), N256(), std::true_type());
   };
   return a.maps() > 1 ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 1>());

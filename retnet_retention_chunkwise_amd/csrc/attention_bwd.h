@@ -31,7 +31,7 @@ namespace attn {
 
 // stats: [M][B*H*T] of {lse log2 e, D}: first all of map 1.
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int KT>
-__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) void attention_bwd_q_kernel(AttnBwd g, float2* stats,
+__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)) void attention_bwd_q_kernel(AttnBwd g, float2* stats,
                                                                   float* __restrict__ lam_part, float* __restrict__ part,
                                                                   int tiles, int shares) {
   typedef Mma<E> X;
@@ -39,7 +39,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
   constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
   constexpr int KB = KT / 16, KS = D / 32, VS = DV / 32, CB = D / 16;
   constexpr bool kDma = kWhole && sizeof(E) == 2;
-  constexpr int SLOTS = DK + DV <= 256 ? 3 : 2;
+  constexpr int SLOTS = DK + DV <= 384 ? 3 : 2;
   typedef Tile<E, DK, kDma> KTile;
   typedef Tile<E, DV, kDma> VTile;
   __shared__ __attribute__((aligned(16))) E K0[KT * KTile::LD], K1[KT * KTile::LD], K2[kDma && SLOTS == 3 ? KT * DK : 16];
@@ -259,14 +259,14 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) voi
 }
 
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int QT>
-__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK <= 128 ? 2 : 1)) void attention_bwd_kv_kernel(AttnBwd g, const float2* __restrict__ stats,
+__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)) void attention_bwd_kv_kernel(AttnBwd g, const float2* __restrict__ stats,
                                                                       float* __restrict__ part, int shares) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
   constexpr int D = DK / MAPS, THREADS = 64 * NW, KT = 16 * NB * NW;
   constexpr int QB = QT / 16, KS = D / 32, VS = DV / 32, CB = D / 16, VB = DV / 16;
   constexpr bool kDma = kWhole && sizeof(E) == 2;
-  constexpr int SLOTS = DK + DV <= 256 ? 3 : 2;
+  constexpr int SLOTS = DK + DV <= 384 ? 3 : 2;
   typedef Tile<E, DK, kDma> QTile;
   typedef Tile<E, DV, kDma> GTile;
   constexpr bool kAhead = sizeof(E) == 2;
@@ -578,9 +578,9 @@ template <typename E, int DK>
 struct KvShape {
   static constexpr int NB = 1, NW = 4, TILE = 16 * NB * NW, STREAM = 32;
 };
-template <typename E, int DK>
+template <typename E, int DK, int DV>
 struct BwdShape {
-  static constexpr int NB = sizeof(E) == 2 && DK <= 128 ? 2 : 1;
+  static constexpr int NB = sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1;
   static constexpr int NW = 4, TILE = 16 * NB * NW, STREAM = 32;
 };
 
@@ -590,7 +590,7 @@ int bwd_keys(const AttnFwd& a) {
 }
 template <typename E>
 int bwd_rows(const AttnFwd& a) {
-  return with_sizes(a, [](auto, auto dk, auto, auto) { return BwdShape<E, decltype(dk)::value>::TILE; });
+  return with_sizes(a, [](auto, auto dk, auto dv, auto) { return BwdShape<E, decltype(dk)::value, decltype(dv)::value>::TILE; });
 }
 
 template <typename E>
@@ -598,7 +598,7 @@ hipError_t launch_bwd_q(const AttnBwd& a, float* stats, float* lam_part, float* 
   return with_sizes(a.f, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
     constexpr bool W = decltype(whole)::value;
-    typedef BwdShape<E, DK> C;
+    typedef BwdShape<E, DK, DV> C;
     const int tiles = (a.f.T + C::TILE - 1) / C::TILE;
     hipLaunchKernelGGL((attention_bwd_q_kernel<E, M, DK, DV, W, C::NB, C::NW, C::STREAM>),
                        dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.H, shares), dim3(64 * C::NW), 0, s, a,

@@ -32,7 +32,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (MAPS == 1 || DV < 256)
   constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
   constexpr int KB = KT / 16, KS = D / 32, VB = DV / 16;
   constexpr bool kDma = kWhole && sizeof(E) == 2;
-  constexpr int SLOTS = DK + DV <= 256 ? 3 : 2;
+  constexpr int SLOTS = DK + DV <= 384 ? 3 : 2;
   typedef Tile<E, DK, kDma> KTile;
   typedef Tile<E, DV, kDma> VTile;
   __shared__ __attribute__((aligned(16))) E K0[KT * KTile::LD], K1[KT * KTile::LD], K2[kDma && SLOTS == 3 ? KT * DK : 16];
@@ -262,19 +262,9 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (MAPS == 1 || DV < 256)
   }
 }
 
-// Keys are split where the rows alone give fewer workgroups than the device has
-// compute units, into ranges of at least kSplitKeys keys.
-constexpr int kSplitKeys = 256, kSplitTarget = 512;
-
-inline int splits(long workgroups, int keys) {
-  if (workgroups >= kSplitTarget / 2 || keys < 2 * kSplitKeys) return 1;
-  const long want = kSplitTarget / workgroups, most = keys / kSplitKeys;
-  return static_cast<int>(want < most ? want : most);
-}
-
 template <typename E, int MAPS, int DK, int DV>
 struct FwdShape {
-  static constexpr int NB = sizeof(E) == 2 && DV * MAPS <= 256 ? 2 : 1;
+  static constexpr int NB = sizeof(E) == 2 && DV * MAPS <= 256 && (MAPS == 1 || DK <= 128) ? 2 : 1;
   static constexpr int NW = 4, KT = 32, QT = 16 * NB * NW;
 };
 

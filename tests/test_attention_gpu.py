@@ -78,6 +78,11 @@ CASES = [
     (1, 2, 1, 70, 90, 256, 256, F32, True, False),
     (1, 1, 1, 40, 40, 255, 255, F32, False, True),
     (3, 8, 8, 16, 16, 48, 24, BF16, True, True),
+    (1, 2, 1, 190, 190, 192, 96, BF16, True, True),   # one side wider than the other
+    (1, 2, 2, 175, 175, 64, 160, BF16, True, False),
+    (1, 2, 2, 140, 140, 192, 128, BF16, False, True),
+    (1, 2, 1, 70, 70, 160, 64, F32, True, True),
+    (1, 2, 1, 70, 70, 96, 256, F32, False, True),
     (1, 2, 2, 300, 20, 64, 64, BF16, True, True),   # more rows than keys: the first see none
     (1, 2, 1, 20, 300, 64, 64, BF16, True, True),   # the last rows of a longer sequence
 ]

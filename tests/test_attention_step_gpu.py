@@ -81,6 +81,9 @@ def run(name, q, k, v, kc, vc, table, lens, lam):
     ([1, 700], 34, 2, 18, 130, 1, BF16),
     ([2000, 1023, 1024], 4, 2, 128, 100, 64, F32),
     ([511, 1200], 3, 3, 40, 256, 256, BF16),
+    ([33, 700], 4, 1, 192, 96, 64, BF16),
+    ([20, 333], 2, 2, 160, 68, 16, F32),
+    ([65, 130], 4, 2, 64, 136, 64, F32),
 ])
 def test_step_matches_oracle(lens, H, Hk, dk, dv, page, dtype, two):
     name = f"step {lens} H{H}/{Hk} dk{dk} dv{dv} page{page} {dtype} maps={1 + two}"
