@@ -32,8 +32,8 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   constexpr int VR = 64 / CH > 0 ? 64 / CH : 1, VN = kKeys / VR;     // rows of one load of a wave, loads
   static_assert(CH <= 64, "a row per load");
   struct Join {
-    float out[MAPS][16][DV + 4];
-    float top[kWaves][MAPS][16], sum[kWaves][MAPS][16];
+    float out[kWaves][MAPS][16][DV + 4];
+    float2 ml[kWaves][MAPS][16];  // maximum and sum
   };
   union Lds {
     E v[kWaves][kKeys * VLD];
@@ -61,8 +61,6 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   E* vc = static_cast<E*>(a.v_cache) + hk * a.svc.h;
   const int* table = a.table + static_cast<long>(b) * a.max_pages;
 
-  Frag qf[MAPS * KS];
-  load_columns<E, MAPS, D, kWhole>(static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h, live, a.d, lane, qf);
   const float c = a.scale * kLog2e, slack = kSlack / c;
   f32x4 o[MAPS][VB];
   float mx[MAPS], sum[MAPS];
@@ -82,16 +80,22 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   const int vrow = lane / CH, vchunk = (lane % CH) * CE;
   const Piece16<E, kWhole> vpiece(vchunk, a.dv);
   auto kpiece = [&](int e, int i) { return Piece16<E, kWhole>(32 * (e % KS) + CE * grp + 16 * i, a.d); };
-  auto load = [&](int tile) {
-    // lane j finds key j's rows; a key without a page (or behind the last) is
-    // masked, and the new token's rows are read in its place
+  // Lane j finds key j's rows.  Its page is looked up a tile ahead of the rows,
+  // which are a memory latency behind it already.
+  auto page_of = [&](int tile) {
+    const int key = tile * kKeys + (lane & (kKeys - 1));
+    return key < keys - 1 ? table[key / a.page] : -1;
+  };
+  auto load = [&](int tile, int page) {
+    // a key without a page (or behind the last) is masked, and the new token's
+    // rows are read in its place
     const int key = tile * kKeys + (lane & (kKeys - 1));
     const E *kp = knew, *vp = vnew;
     bool in = key < keys;
     if (key < keys - 1) {
-      const int page = table[key / a.page], r = key % a.page;
       in = page >= 0 && page < a.pages;
       if (in) {
+        const int r = key % a.page;
         kp = kc + page * a.skc.b + r * a.skc.t;
         vp = vc + page * a.svc.b + r * a.svc.t;
       }
@@ -115,8 +119,24 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   };
 
   E* vs = lds.v[wave];
-  int i = first + wave;
-  if (i < last) load(i);
+  int i = first + wave, next_page = -1;
+  if (i < last) {
+    const int page = page_of(i);
+    next_page = page_of(i + kWaves);
+    load(i, page);
+  }
+  Frag qf[MAPS * KS];
+  load_columns<E, MAPS, D, kWhole>(static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h, live, a.d, lane, qf);
+  // the new token's elements, a thread each, and their page, to be stored below
+  const bool stores = len >= 0 && len < a.max_pages * static_cast<long>(a.page) && split == part.nsplit - 1 && gb == 0;
+  static_assert(DK <= 64 * kWaves && DV <= 64 * kWaves, "a thread per element");
+  int new_page = -1;
+  E new_k, new_v;
+  if (stores) {
+    new_page = table[len / a.page];
+    if (tid < MAPS * a.d) new_k = knew[tid];
+    if (tid < a.dv) new_v = vnew[tid];
+  }
   for (; i < last; i += kWaves) {
 #pragma unroll
     for (int j = 0; j < VN; ++j)
@@ -140,7 +160,10 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
         }
       }
     const unsigned seen = ok;
-    if (i + kWaves < last) load(i + kWaves);
+    if (i + kWaves < last) {
+      load(i + kWaves, next_page);
+      next_page = page_of(i + 2 * kWaves);
+    }
     if (seen != 0xffffffffu) {
 #pragma unroll
       for (int m = 0; m < MAPS; ++m)
@@ -192,64 +215,50 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
     __builtin_amdgcn_wave_barrier();
   }
 
-  // the new token's rows into their place
-  if (len >= 0 && len < a.max_pages * static_cast<long>(a.page) && split == part.nsplit - 1 && gb == 0) {
-    const int page = table[len / a.page], r = len % a.page;
-    if (page >= 0 && page < a.pages) {
-      E* kp = kc + page * a.skc.b + r * a.skc.t;
-      E* vp = vc + page * a.svc.b + r * a.svc.t;
-      for (int x = tid; x < MAPS * a.d; x += 64 * kWaves) kp[x] = knew[x];
-      for (int x = tid; x < a.dv; x += 64 * kWaves) vp[x] = vnew[x];
-    }
+  if (stores && new_page >= 0 && new_page < a.pages) {
+    const int r = len % a.page;
+    if (tid < MAPS * a.d) kc[new_page * a.skc.b + r * a.skc.t + tid] = new_k;
+    if (tid < a.dv) vc[new_page * a.svc.b + r * a.svc.t + tid] = new_v;
   }
 
-  // the waves' shares onto one maximum, added in wave order
+  // the waves' shares side by side; every thread adds its part of them onto one
+  // maximum, in wave order
   __syncthreads();
 #pragma unroll
   for (int m = 0; m < MAPS; ++m) {
     sum[m] = row4_sum(sum[m]);
-    if (grp == 0) {
-      lds.j.top[wave][m][col] = mx[m];
-      lds.j.sum[wave][m][col] = sum[m];
-    }
+    if (grp == 0) lds.j.ml[wave][m][col] = make_float2(mx[m], sum[m]);
+#pragma unroll
+    for (int j = 0; j < VB; ++j) *reinterpret_cast<f32x4*>(&lds.j.out[wave][m][col][16 * j + 4 * grp]) = o[m][j];
   }
   __syncthreads();
+  if (!live) return;
+  float f[MAPS][kWaves];
 #pragma unroll
   for (int m = 0; m < MAPS; ++m) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds.j.top[w][m][col]);
-    const float f = mx[m] == -INFINITY ? 0.0f : fast_exp2((mx[m] - top) * c);
-    float l = 0.0f;
+    float2 ml[kWaves];
+    float top = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const float t = lds.j.top[w][m][col];
-      if (t != -INFINITY) l = fmaf(lds.j.sum[w][m][col], fast_exp2((t - top) * c), l);
+      ml[w] = lds.j.ml[w][m][col];
+      top = fmaxf(top, ml[w].x);
+    }
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      f[m][w] = ml[w].x == -INFINITY ? 0.0f : fast_exp2((ml[w].x - top) * c);
+      l = fmaf(ml[w].y, f[m][w], l);
     }
     mx[m] = top;
     sum[m] = l;
-#pragma unroll
-    for (int j = 0; j < VB; ++j) o[m][j] *= f;
   }
-  for (int w = 0; w < kWaves; ++w) {
-    if (wave == w) {
+  auto joined = [&](int m, int ch) {
+    f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-      for (int m = 0; m < MAPS; ++m)
-#pragma unroll
-        for (int j = 0; j < VB; ++j) {
-          f32x4* p = reinterpret_cast<f32x4*>(&lds.j.out[m][col][16 * j + 4 * grp]);
-          *p = w == 0 ? o[m][j] : *p + o[m][j];
-        }
-    }
-    __syncthreads();
-  }
+    for (int w = 0; w < kWaves; ++w) x += *reinterpret_cast<const f32x4*>(&lds.j.out[w][m][col][ch]) * f[m][w];
+    return x;
+  };
   // wave w writes channels 4 grp.. of the blocks w, w + 4, ...
-  if (!live) return;
   const int dv4 = (a.dv + 3) & ~3;
-  const float lam = MAPS > 1 ? a.lam[h] : 0.0f;
-  float inv[MAPS];
-#pragma unroll
-  for (int m = 0; m < MAPS; ++m) inv[m] = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
   if (part.nsplit > 1) {
 #pragma unroll
     for (int m = 0; m < MAPS; ++m) {
@@ -257,17 +266,20 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
       if (tid < 16) reinterpret_cast<float2*>(part.ml)[at] = make_float2(mx[m] * c, sum[m]);
       for (int vb = wave; vb < VB; vb += kWaves) {
         const int ch = 16 * vb + 4 * grp;
-        if (ch < dv4)
-          *reinterpret_cast<f32x4*>(part.out + at * dv4 + ch) = *reinterpret_cast<const f32x4*>(&lds.j.out[m][col][ch]);
+        if (ch < dv4) *reinterpret_cast<f32x4*>(part.out + at * dv4 + ch) = joined(m, ch);
       }
     }
     return;
   }
+  const float lam = MAPS > 1 ? a.lam[h] : 0.0f;
+  float inv[MAPS];
+#pragma unroll
+  for (int m = 0; m < MAPS; ++m) inv[m] = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
   E* out = static_cast<E*>(a.o) + b * a.so.b + h * a.so.h;
   for (int vb = wave; vb < VB; vb += kWaves) {
     const int ch = 16 * vb + 4 * grp;
-    f32x4 y = *reinterpret_cast<const f32x4*>(&lds.j.out[0][col][ch]) * inv[0];
-    if constexpr (MAPS > 1) y -= *reinterpret_cast<const f32x4*>(&lds.j.out[1][col][ch]) * (inv[1] * lam);
+    f32x4 y = joined(0, ch) * inv[0];
+    if constexpr (MAPS > 1) y -= joined(1, ch) * (inv[1] * lam);
     store4<E, kWhole>(out, ch, a.dv, y);
   }
 }
