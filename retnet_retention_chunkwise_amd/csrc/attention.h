@@ -58,6 +58,19 @@ struct AttnStep {
   int dt;
   bool whole;        // rows of whole 16-byte pieces
   int maps() const { return lam != nullptr ? 2 : 1; }
+  // key / page by a product, for 0 <= key < 2^30: mul exceeds 2^(30 + s) / page,
+  // 2^s >= page, by less than one, which moves no quotient's floor.
+  unsigned page_mul;
+  int page_shift;
+  __host__ __device__ int page_of(int key) const {
+    return static_cast<int>(static_cast<unsigned long long>(key) * page_mul >> page_shift);
+  }
+  void set_page(int n) {
+    page = n;
+    page_shift = 30;
+    while (1LL << (page_shift - 30) < n) ++page_shift;
+    page_mul = static_cast<unsigned>(((1ULL << page_shift) + n - 1) / n);
+  }
 };
 // T tokens of every sequence into the cache.
 struct CacheAppend {

@@ -259,7 +259,7 @@ size_t retention_attention_step_workspace_bytes(int B, int H, int Hk, int dk, in
   a.Hk = Hk;
   a.d = dk / maps;
   a.dv = dv;
-  a.page = page;
+  a.set_page(page);
   a.max_pages = max_pages;
   a.dt = dt == RET_BF16 ? 1 : 0;
   return ret::attention_step_workspace(a);
@@ -310,7 +310,7 @@ ret_status retention_attention_step(const void* q, const void* k, const void* v,
   a.d = dk / maps;
   a.dv = dv;
   a.pages = pages;
-  a.page = page;
+  a.set_page(page);
   a.max_pages = max_pages;
   a.scale = scale;
   a.dt = dt == RET_BF16 ? 1 : 0;

@@ -19,10 +19,10 @@ namespace ret {
 namespace attn {
 namespace {
 
-constexpr int kWaves = 4, kKeys = 32;
+constexpr int kKeys = 32;
 constexpr float kSlack = 8.0f;  // see attention_fwd.h
 
-template <typename E, int MAPS, int DK, int DV, bool kWhole>
+template <typename E, int MAPS, int DK, int DV, bool kWhole, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a, Partial part) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   // which are a memory latency behind it already.
   auto page_of = [&](int tile) {
     const int key = tile * kKeys + (lane & (kKeys - 1));
-    return key < keys - 1 ? table[key / a.page] : -1;
+    return key < keys - 1 ? table[a.page_of(key)] : -1;
   };
   auto load = [&](int tile, int page) {
     // a key without a page (or behind the last) is masked, and the new token's
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
     if (key < keys - 1) {
       in = page >= 0 && page < a.pages;
       if (in) {
-        const int r = key % a.page;
+        const int r = key - a.page_of(key) * a.page;
         kp = kc + page * a.skc.b + r * a.skc.t;
         vp = vc + page * a.svc.b + r * a.svc.t;
       }
@@ -127,13 +127,14 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   }
   Frag qf[MAPS * KS];
   load_columns<E, MAPS, D, kWhole>(static_cast<const E*>(a.q) + b * a.sq.b + h * a.sq.h, live, a.d, lane, qf);
+  const float lam = MAPS > 1 ? a.lam[h] : 0.0f;
   // the new token's elements, a thread each, and their page, to be stored below
   const bool stores = len >= 0 && len < a.max_pages * static_cast<long>(a.page) && split == part.nsplit - 1 && gb == 0;
   static_assert(DK <= 64 * kWaves && DV <= 64 * kWaves, "a thread per element");
   int new_page = -1;
   E new_k, new_v;
   if (stores) {
-    new_page = table[len / a.page];
+    new_page = table[a.page_of(len)];
     if (tid < MAPS * a.d) new_k = knew[tid];
     if (tid < a.dv) new_v = vnew[tid];
   }
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
   }
 
   if (stores && new_page >= 0 && new_page < a.pages) {
-    const int r = len % a.page;
+    const int r = len - a.page_of(len) * a.page;
     if (tid < MAPS * a.d) kc[new_page * a.skc.b + r * a.skc.t + tid] = new_k;
     if (tid < a.dv) vc[new_page * a.svc.b + r * a.svc.t + tid] = new_v;
   }
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
     for (int w = 0; w < kWaves; ++w) x += *reinterpret_cast<const f32x4*>(&lds.j.out[w][m][col][ch]) * f[m][w];
     return x;
   };
-  // wave w writes channels 4 grp.. of the blocks w, w + 4, ...
+  // wave w writes channels 4 grp.. of the blocks w, w + kWaves, ...
   const int dv4 = (a.dv + 3) & ~3;
   if (part.nsplit > 1) {
 #pragma unroll
@@ -271,7 +272,6 @@ __global__ __launch_bounds__(64 * kWaves) void attention_step_kernel(AttnStep a,
     }
     return;
   }
-  const float lam = MAPS > 1 ? a.lam[h] : 0.0f;
   float inv[MAPS];
 #pragma unroll
   for (int m = 0; m < MAPS; ++m) inv[m] = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
@@ -362,9 +362,15 @@ template <typename E>
 hipError_t step(const AttnStep& a, const Partial& p, hipStream_t s) {
   return with_sizes(a, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
-    const int blocks = (a.H / a.Hk + 15) / 16;
-    hipLaunchKernelGGL((attention_step_kernel<E, M, DK, DV, decltype(whole)::value>),
-                       dim3(static_cast<unsigned>(a.B) * a.Hk * blocks, p.nsplit), dim3(64 * kWaves), 0, s, a, p);
+    constexpr bool W = decltype(whole)::value;
+    const unsigned wgs = static_cast<unsigned>(a.B) * a.Hk * ((a.H / a.Hk + 15) / 16);
+    if constexpr (sizeof(E) == 2 && DK + DV <= 256) {
+      if (static_cast<long>(wgs) * p.nsplit <= 256) {
+        hipLaunchKernelGGL((attention_step_kernel<E, M, DK, DV, W, 8>), dim3(wgs, p.nsplit), dim3(64 * 8), 0, s, a, p);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((attention_step_kernel<E, M, DK, DV, W, 4>), dim3(wgs, p.nsplit), dim3(64 * 4), 0, s, a, p);
     return hipGetLastError();
   });
 }
