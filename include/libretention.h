@@ -463,7 +463,10 @@ size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D);
  * outputs are rounded once.  lam and its gradient are fp32 [H]; lam, lse and
  * int arrays need the alignment of their elements only.
  * Limits: dk, dv <= 256; every tensor (a cache aside) below 2^31 elements,
- * B*H*T <= 2^25, T and S <= 2^30, B*H*ceil(T/64) and B*Hk*ceil(S/64) <= 2^23.
+ * B*H*T <= 2^25, T and S <= 2^30, B*H*ceil(T/64) and B*Hk*ceil(S/64) <= 2^23;
+ * in whole sequences, tokens of k and v (backward: of q and grad_o too) at most
+ * 2^24 elements apart.  Any alignment of rows; bf16 rows that start at multiples
+ * of 16 bytes, with d (dk / maps) and dv multiples of 8, are read the fastest way.
  * No sum depends on timing: the same call gives the same bits.
  */
 
@@ -484,8 +487,9 @@ size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D);
  *             that is 0), 16-byte aligned, owned by the caller, overlapping no
  *             other argument; contents ignored on entry.  Calls that overlap in
  *             time need workspaces of their own.
- * Inputs that are not finite reach the rows that see them as the formula says;
- * a value row that is not finite may also reach rows before it.
+ * An element that is not finite makes the results of the rows that see it NaN
+ * or what the formula says; a value row that is not finite may also reach rows
+ * before it.
  */
 ret_status retention_attention_fwd(const void* q, const void* k, const void* v, const float* lam, const int* lens,
                                    void* o, float* lse, void* second, const ret_strides* strides, int B, int H, int Hk,
@@ -505,6 +509,9 @@ size_t retention_attention_workspace_bytes(int B, int H, int Hk, int T, int S, i
  *   grad_lam : written, fp32 [H]; NULL exactly when lam is NULL.
  *   strides : q, k, v, o, grad_o, grad_q, grad_k, grad_v.
  *   workspace : retention_attention_bwd_workspace_bytes() bytes, as above.
+ * A row's mean of d L / d A under its weights, which the softmax's gradient
+ * subtracts, comes from o and second as they were rounded, and for rows of at
+ * most 32 keys (where it matters most) from the weights themselves.
  */
 ret_status retention_attention_bwd(const void* q, const void* k, const void* v, const float* lam, const int* lens,
                                    const void* o, const float* lse, const void* second, const void* grad_o,

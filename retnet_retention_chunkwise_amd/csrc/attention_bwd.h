@@ -154,6 +154,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)
                 x = fmaf(fast_exp2(fmaf(s[m][kb][n][r], c, -st[m][n].x)), dp[kb][n][r], x);
             x = row4_sum(x);
             st[m][n].y = x;
+            // another share may read either value: it has no keys for these rows
             const int t = w0 + 16 * n + col;
             if (grp == 0 && t < a.T) stats[m * rows + static_cast<long>(bh) * a.T + t].y = x;
           }
