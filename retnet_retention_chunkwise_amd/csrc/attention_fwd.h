@@ -14,7 +14,15 @@
 // fp32 value notices: p is then at most 2^kSlack instead of 1.  Both maps read
 // the same value tile once and keep an output each, because they are divided by
 // different sums.  Products are bf16 MFMA (fp32: fp32 MFMA); scores, maxima,
-// sums and outputs are fp32; p is rounded to bf16 as an operand.
+// sums and outputs are fp32; p is rounded to bf16 as an operand, which costs as
+// much as the output's own rounding and halves the product's time.
+//
+// 32 rows a wave (bf16, where the outputs' registers allow): a tile's operands are
+// read from LDS once for twice the products.  Bound by matrix and vector
+// instructions, which do not overlap between a SIMD's two waves: about 24 clocks of
+// products and 31 of softmax a score at 128 channels and two maps, 91% of the time.
+// B1 H16/4 T8192 d128 two maps causal: 414 us (1.0 PFLOP/s of visible pairs); B4 H8
+// T2048 d256: 123 us (0.84).
 #pragma once
 
 #include "attention.h"

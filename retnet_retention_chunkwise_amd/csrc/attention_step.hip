@@ -11,6 +11,9 @@
 // workgroups and their shares joined by a second launch.  The new token's key
 // and value are read from the arguments and stored beside; nobody reads their
 // place in the cache during the call.
+// Bound by memory: 128 streams of 16/4 heads over up to 2048 tokens, d128 bf16,
+// 270 MB in 58 us (4.6 TB/s); 2 of 32/8 over 65536, 537 MB in 97 us and 6 for the
+// join.  Few short streams are bound by latency: 8 of 8 over 512, 11 us.
 #include "attention.h"
 
 #include "attention_tiles.h"
@@ -301,6 +304,8 @@ __device__ __forceinline__ void copy_row(const E* from, E* to, int n, int lane) 
                               reinterpret_cast<typename R::at*>(to + c));
 }
 
+// Bound by memory, and read and written once: past the caches.  4 x 2048 tokens of
+// 8 heads, 256 + 256 channels bf16: 134 MB in 27 us (5.0 TB/s).
 constexpr int kAppendThreads = 256, kAppendRounds = 4;
 
 template <typename E, int LPR>
@@ -345,8 +350,8 @@ hipError_t append_by_width(const CacheAppend& a, hipStream_t s) {
 // Keys are split where the sequences and key heads alone give fewer than
 // kStepTarget / 2 workgroups (two fit on a compute unit), into ranges that take a
 // wave longer than the second launch: four tiles of bf16, two of fp32, whose
-// products are slower.  8 streams of 8 heads over 512 tokens bf16: one range
-// 14.6 us a call, two 18; 15 heads over 3001 tokens fp32: ranges of 256 tokens
+// products are slower.  With four waves a workgroup, 8 streams of 8 heads over 512
+// tokens bf16: one range 14.6 us a call, two 18; 15 heads over 3001 tokens fp32: ranges of 256 tokens
 // 26.6 us, of 512 35, of 128 31.
 constexpr int kStepTarget = 1024;
 
@@ -364,6 +369,10 @@ hipError_t step(const AttnStep& a, const Partial& p, hipStream_t s) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
     constexpr bool W = decltype(whole)::value;
     const unsigned wgs = static_cast<unsigned>(a.B) * a.Hk * ((a.H / a.Hk + 15) / 16);
+    // Workgroups that have a compute unit each to themselves take eight waves, whose
+    // chains of tiles are half as long: 8 streams of 8 heads over 512 tokens 11.2 us,
+    // with four 12.4; where all units are taken they only make the join longer (128
+    // streams 63.7 us, with four 61).  Wider heads and fp32 have no registers for it.
     if constexpr (sizeof(E) == 2 && DK + DV <= 256) {
       if (static_cast<long>(wgs) * p.nsplit <= 256) {
         hipLaunchKernelGGL((attention_step_kernel<E, M, DK, DV, W, 8>), dim3(wgs, p.nsplit), dim3(64 * 8), 0, s, a, p);
