@@ -17,12 +17,13 @@
 // sums and outputs are fp32; p is rounded to bf16 as an operand, which costs as
 // much as the output's own rounding and halves the product's time.
 //
-// 32 rows a wave (bf16, where the outputs' registers allow): a tile's operands are
-// read from LDS once for twice the products.  Bound by matrix and vector
-// instructions, which do not overlap between a SIMD's two waves: about 24 clocks of
-// products and 31 of softmax a score at 128 channels and two maps, 91% of the time.
-// B1 H16/4 T8192 d128 two maps causal: 414 us (1.0 PFLOP/s of visible pairs); B4 H8
-// T2048 d256: 123 us (0.84).
+// 32 rows a wave (bf16, up to 128 channels): a tile's operands are read from LDS
+// once for twice the products.  Wider rows leave room for one such wave a SIMD; 16
+// rows and two waves are faster (B4 H8 T2048 one map d256: 101 us, with 32 rows 126).
+// Bound by matrix and vector instructions, which do not overlap between a SIMD's
+// two waves: about 24 clocks of products and 31 of softmax a score at 128 channels
+// and two maps, 91% of the time.  B1 H16/4 T8192 d128 two maps causal: 414 us (1.0
+// PFLOP/s of visible pairs); B4 H8 T2048 d256: 123 us (0.84).
 #pragma once
 
 #include "attention.h"
@@ -34,7 +35,7 @@ namespace attn {
 constexpr float kSlack = 8.0f;
 
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int KT>
-__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (MAPS == 1 || DV < 256) && DV <= 128 ? 2 : 1)) void attention_fwd_kernel(AttnFwd a, Partial part, int tiles) {
+__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DV <= 128 ? 2 : 1)) void attention_fwd_kernel(AttnFwd a, Partial part, int tiles) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
   constexpr int D = DK / MAPS, THREADS = 64 * NW, QT = 16 * NB * NW;
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (MAPS == 1 || DV < 256)
 
 template <typename E, int MAPS, int DK, int DV>
 struct FwdShape {
-  static constexpr int NB = sizeof(E) == 2 && DV * MAPS <= 256 && (MAPS == 1 || DK <= 128) ? 2 : 1;
+  static constexpr int NB = sizeof(E) == 2 && DK <= 128 && DV <= 128 ? 2 : 1;
   static constexpr int NW = 4, KT = 32, QT = 16 * NB * NW;
 };
 
