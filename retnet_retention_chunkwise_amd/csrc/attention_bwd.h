@@ -266,7 +266,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)
 }
 
 template <typename E, int MAPS, int DK, int DV, bool kWhole, int NB, int NW, int QT>
-__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)) void attention_bwd_kv_kernel(AttnBwd g, const float2* __restrict__ stats,
+__global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (kWhole || DK + DV <= 256) ? 2 : 1)) void attention_bwd_kv_kernel(AttnBwd g, const float2* __restrict__ stats,
                                                                       float* __restrict__ part, int shares) {
   typedef Mma<E> X;
   typedef typename X::Frag Frag;
@@ -276,7 +276,11 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)
   constexpr int SLOTS = DK + DV <= 384 ? 3 : 2;
   typedef Tile<E, DK, kDma> QTile;
   typedef Tile<E, DV, kDma> GTile;
-  constexpr bool kAhead = sizeof(E) == 2;
+  // Operands are read a stage ahead, except beside the sums of wide rows, which
+  // leave registers for that or for a second wave on the SIMD: the wave gains more
+  // (B2 H8 T2000 one map d256: training pass 308 us, reading ahead 370).  Rows that
+  // are not whole spill then (T1500 250 and 201 channels: 424 us, reading ahead 401).
+  constexpr bool kAhead = sizeof(E) == 2 && (!kWhole || DK + DV <= 256);
   __shared__ __attribute__((aligned(16))) E Q0[QT * QTile::LD], Q1[QT * QTile::LD], Q2[kDma && SLOTS == 3 ? QT * DK : 16];
   __shared__ __attribute__((aligned(16))) E G0[QT * GTile::LD], G1[QT * GTile::LD], G2[kDma && SLOTS == 3 ? QT * DV : 16];
   // statistics of a tile's rows, {lse log2 e, D}; with straight loads every wave
