@@ -341,3 +341,48 @@ def test_graph_and_streams(T, S):
             assert all(torch.equal(a, b) for a, b in zip(held, want))
         both()
         torch.cuda.synchronize()
+
+
+def test_two_streams_at_once():
+    """Training passes of different inputs that overlap in time, each with workspaces of its own: the bits of each alone."""
+    sets = [dev(*make(1, 4, 2, 700, 700, d, 64, dtype, True, seed=d)) for d, dtype in ((64, BF16), (96, F32))]
+
+    def both(q, k, v, lam, do):
+        o, kept = ret.attention_fwd(q, k, v, lam, keep=True)
+        return (o, *kept, *ret.attention_bwd(q, k, v, o, do, kept, lam))
+
+    want = [both(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(both(*sets[i]))
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        assert all(torch.equal(a, b) for run in got[i] for a, b in zip(run, w))
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_shapes(seed):
+    """Any widths, lengths, masks and types, against the bounds."""
+    g = torch.Generator().manual_seed(seed)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))  # noqa: E731
+    two, dtype = bool(seed & 1), BF16 if seed & 2 else F32
+    Hk, B = pick(1, 3), pick(1, 2)
+    H, T, S = Hk * pick(1, 4), pick(1, 200), pick(1, 600)
+    dk, dv = (2 * pick(1, 128) if two else pick(1, 256)), pick(1, 256)
+    if seed & 4:
+        dk, dv = -(-dk // 16) * 16, -(-dv // 8) * 8
+    mask = dict(causal=bool(seed & 8))
+    if mask["causal"]:
+        mask["offset"] = pick(-T, S)
+    if pick(0, 1):
+        mask["lens"] = torch.tensor([pick(0, S) for _ in range(B)], dtype=torch.int32)
+    name = f"random {seed}: B{B} H{H}/{Hk} T{T} S{S} dk{dk} dv{dv} {dtype} maps={1 + two} {mask}"
+    say(name)
+    q, k, v, lam, do = make(B, H, Hk, T, S, dk, dv, dtype, two, seed=seed)
+    o, kept, grads = run(q, k, v, lam, do, **mask)
+    check(name, q, k, v, lam, do, o, kept, grads, **mask)
