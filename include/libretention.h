@@ -456,8 +456,8 @@ size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D);
  *   o[t] = sum_s A_1[t,s] v[s]                        (lam NULL: one map)
  *   o[t] = sum_s (A_1[t,s] - lam_h A_2[t,s]) v[s]     (differential attention)
  * The two maps take the two halves of the dk channels of a row of q and k.
- * Strides are those of ret_strides.  scale is finite and > 0 (1 / sqrt of a
- * map's channels is usual).  Products are of the tensors' type (bf16 or fp32
+ * Strides are those of ret_strides.  scale lies within 2^-100..2^100 (1 / sqrt of
+ * a map's channels is usual).  Products are of the tensors' type (bf16 or fp32
  * MFMA) with fp32 accumulators; scores, softmax statistics and sums are fp32;
  * probabilities are rounded to the tensors' type before they meet the values;
  * outputs are rounded once.  lam and its gradient are fp32 [H]; lam, lse and

@@ -23,7 +23,7 @@ struct AttnFwd {
   Strides3 sq, sk, sv, so;
   int B, H, Hk, T, S;
   int d, dv;         // channels of one map; of a value
-  float scale;       // of the scores, > 0
+  float scale;       // of the scores, within 2^-100..2^100
   bool causal;
   int offset;        // causal: row t sees the keys up to t + offset
   int dt;

@@ -10,6 +10,9 @@ constexpr int kMaxLen = 1 << 30;               // tokens, and the offset's magni
 constexpr long long kMaxAttnRows = 1LL << 25;  // rows of q: a wave each, below 2^32 threads in all
 constexpr long kMaxTokenStride = 1L << 24;
 constexpr long long kMaxTiles = 1LL << 23;     // workgroups of 256 threads
+// Scales: the kernels form scale log2 e and 8 / (scale log2 e), which leave fp32 below
+// 1.6e-38 and above 2.3e38 (the running maximum then never moves, or every score is NaN).
+constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p+100f;
 
 struct Sizes {
   int B, H, Hk, T, S, dk, dv, maps;
@@ -52,6 +55,8 @@ ret_status check_attn(const char* fn, const Sizes& z, ret_dtype dt) {
 ret_status check_scores(const char* fn, float scale, int offset) {
   if (!std::isfinite(scale) || scale <= 0.0f)
     return fail(RET_ERR_INVALID_ARG, "%s: scale=%g must be finite and > 0", fn, static_cast<double>(scale));
+  if (scale < kMinScale || scale > kMaxScale)
+    return fail(RET_ERR_UNSUPPORTED, "%s: scale=%g is not within 2^-100..2^100", fn, static_cast<double>(scale));
   if (offset < -kMaxLen || offset > kMaxLen)
     return fail(RET_ERR_INVALID_ARG, "%s: offset=%d is beyond 2^30", fn, offset);
   return RET_OK;
