@@ -17,9 +17,12 @@
 // every time.  P and dS are rounded to the tensors' type as operands, all else
 // is fp32.  bf16 rounds o, so D from it is off by some 2^-9 of what dP - D
 // cancels from; where few keys share a row's weight that is much of what is
-// left (2 keys: up to a tenth of the gradient).  A wave whose rows all end in
-// their first tile of keys therefore takes D from the tile itself and leaves it
-// to the kv pass; with more keys the rounding of dS is as large.
+// left.  A row that ends in its first tile of keys therefore takes D from the
+// tile itself and leaves it to the kv pass.  A longer row keeps the D of the
+// rounded o, however few of its keys carry its weight: for unit inputs of 64
+// channels dq is off by 0.0024 of itself with the exact D, and by 0.0027, 0.0032
+// and 0.0038 where 9, 3 and 2 keys carry the row; where one key does and the
+// others weigh e^-12 of it, what little is left is off by a quarter and more.
 //
 // Bound as the forward is; B2 H16/4 T4096 d128 two maps causal: q pass 240 us,
 // kv pass 350 (0.28 TFLOP executed), rows 26.  The kv pass holds 16 keys a wave:
@@ -147,7 +150,9 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)
           }
     }
     if constexpr (sizeof(E) == 2) {
-      if (wmax <= KT) {  // few keys: D from this tile, the only one, for this pass and the next
+      // Rows that end in their first tile of keys (a wave's first row is its shortest)
+      // take D from it, for this pass and the next.
+      if (k0 == 0 && wall <= KT) {
 #pragma unroll
         for (int m = 0; m < MAPS; ++m)
 #pragma unroll
@@ -159,10 +164,11 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)
               for (int r = 0; r < 4; ++r)
                 x = fmaf(fast_exp2(fmaf(s[m][kb][n][r], c, -st[m][n].x)), dp[kb][n][r], x);
             x = row4_sum(x);
-            st[m][n].y = x;
+            const bool few = lim[n] <= KT;
+            if (few) st[m][n].y = x;
             // another share may read either value: it has no keys for these rows
             const int t = w0 + 16 * n + col;
-            if (grp == 0 && t < a.T) stats[m * rows + static_cast<long>(bh) * a.T + t].y = x;
+            if (few && grp == 0 && t < a.T) stats[m * rows + static_cast<long>(bh) * a.T + t].y = x;
           }
       }
     }
