@@ -473,8 +473,9 @@ size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D);
 /*
  * A whole sequence.  Row t sees the keys s < lens[b] (lens NULL: S) and, when
  * causal, s <= t + offset (offset S - T aligns the last row with the last key).
- * A row that sees no key is 0, and its lse -inf.  Keys and values from lens[b]
- * on are not used, whatever they hold.
+ * A row that sees no key is 0, and its lse -inf.  Keys and values that no row
+ * sees (from lens[b] on, or behind the last row's limit) are not used, whatever
+ * they hold.
  *   q [B,H,T,dk], k [B,Hk,S,dk], v [B,Hk,S,dv] in dt.
  *   lam     : nullable; device fp32 [H].    lens : nullable; device int [B], taken into 0..S.
  *   o       : written, [B,H,T,dv] in dt.
@@ -505,7 +506,7 @@ size_t retention_attention_workspace_bytes(int B, int H, int Hk, int T, int S, i
  *   grad_o  : [B,H,T,dv] in dt.
  *   grad_q [B,H,T,dk], grad_k [B,Hk,S,dk], grad_v [B,Hk,S,dv] : written in dt,
  *             summed over the query heads that share a key head; 0 for rows that
- *             see no key and for keys and values from lens[b] on.
+ *             see no key and for keys and values that no row sees.
  *   grad_lam : written, fp32 [H]; NULL exactly when lam is NULL.
  *   strides : q, k, v, o, grad_o, grad_q, grad_k, grad_v.
  *   workspace : retention_attention_bwd_workspace_bytes() bytes, as above.

@@ -64,7 +64,8 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)
   auto seen = [&](int t) { return a.causal ? min(max(t + a.offset + 1, 0), len) : len; };
   const int q0 = tile * QT, w0 = q0 + wave * 16 * NB;
   // this workgroup's share of the rows' tiles of keys
-  const int share = blockIdx.y, all = (seen(min(q0 + QT, a.T) - 1) + KT - 1) / KT;
+  const int kmax = seen(min(q0 + QT, a.T) - 1);  // what lies behind is not read: it may hold anything
+  const int share = blockIdx.y, all = (kmax + KT - 1) / KT;
   const int first = static_cast<int>(static_cast<long>(all) * share / shares);
   const int last = static_cast<int>(static_cast<long>(all) * (share + 1) / shares);
   const int wmax = w0 < a.T ? seen(min(w0 + 16 * NB, a.T) - 1) : 0, wall = seen(w0);
@@ -209,20 +210,20 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DK + DV <= 256 ? 2 : 1)
     walk_tiles<SLOTS, kd.COUNT + vd.COUNT>(
         first, last,
         [&](int i, auto slot) __attribute__((always_inline)) {
-          kd.load(k, a.sk.t, i * KT, len, Kt[slot], wave);
-          vd.load(v, a.sv.t, i * KT, len, Vt[slot], wave);
+          kd.load(k, a.sk.t, i * KT, kmax, Kt[slot], wave);
+          vd.load(v, a.sv.t, i * KT, kmax, Vt[slot], wave);
         },
         [&](int i, auto slot) __attribute__((always_inline)) { use(i, Kt[slot], Vt[slot]); });
   } else {
     Stage<E, KT, MAPS, D, THREADS, kWhole> ks(a.d, tid);
     Stage<E, KT, 1, DV, THREADS, kWhole> vs(a.dv, tid);
     auto load = [&](int i) {
-      ks.load(k, a.sk.t, i * KT, len, a.d);
-      vs.load(v, a.sv.t, i * KT, len, a.dv);
+      ks.load(k, a.sk.t, i * KT, kmax, a.d);
+      vs.load(v, a.sv.t, i * KT, kmax, a.dv);
     };
     auto store = [&](int i) {
-      ks.store(i & 1 ? K1 : K0, i * KT, len);
-      vs.store(i & 1 ? V1 : V0, i * KT, len);
+      ks.store(i & 1 ? K1 : K0, i * KT, kmax);
+      vs.store(i & 1 ? V1 : V0, i * KT, kmax);
     };
     if (first < last) {
       load(first);
@@ -300,7 +301,9 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (kWhole || DK + DV <= 2
   // the keys that most rows see first, of all heads and shares
   const int heads = a.B * a.Hk, bh = blockIdx.x % heads, share = blockIdx.x / heads % shares, tile = blockIdx.x / heads / shares;
   const int b = bh / a.Hk, hk = bh % a.Hk, G = a.H / a.Hk;
-  const int len = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
+  // keys that some row sees; the others count as zeros, whatever they hold, and have no gradient
+  const int all = a.lens != nullptr ? min(max(a.lens[b], 0), a.S) : a.S;
+  const int len = a.causal ? min(max(a.T + a.offset, 0), all) : all;
   const int k0 = tile * KT, w0 = k0 + wave * 16 * NB;
   // the first row that sees a key
   auto from = [&](int key) { return a.causal ? min(max(key - a.offset, 0), a.T) : 0; };
@@ -565,7 +568,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (kWhole || DK + DV <= 2
   for (int n = 0; n < NB; ++n) {
     const int key = w0 + 16 * n + col;
     if (key >= a.S) continue;
-    const bool in = key < len;  // keys behind the sequence have no gradient
+    const bool in = key < len;
     const f32x4 zero = {0, 0, 0, 0};
     if (shares > 1) {  // fp32 sums of the share, [share][b, hk, key][dk4 + dv4]
       const int d4 = (a.d + 3) & ~3, dv4 = (a.dv + 3) & ~3;

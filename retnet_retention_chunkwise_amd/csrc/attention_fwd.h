@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DV <= 128 ? 2 : 1)) voi
   // keys that a row t sees
   auto seen = [&](int t) { return a.causal ? min(max(t + a.offset + 1, 0), len) : len; };
   const int q0 = tile * QT, w0 = q0 + wave * 16 * NB;
-  const int kmax = seen(min(q0 + QT, a.T) - 1);
+  const int kmax = seen(min(q0 + QT, a.T) - 1);  // what lies behind is not read: it may hold anything
   const int all = (kmax + KT - 1) / KT;
   const int first = static_cast<int>(static_cast<long>(all) * split / part.nsplit);
   const int last = static_cast<int>(static_cast<long>(all) * (split + 1) / part.nsplit);
@@ -189,8 +189,8 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DV <= 128 ? 2 : 1)) voi
     walk_tiles<SLOTS, kd.COUNT + vd.COUNT>(
         first, last,
         [&](int i, auto slot) __attribute__((always_inline)) {
-          kd.load(k, a.sk.t, i * KT, len, Kt[slot], wave);
-          vd.load(v, a.sv.t, i * KT, len, Vt[slot], wave);
+          kd.load(k, a.sk.t, i * KT, kmax, Kt[slot], wave);
+          vd.load(v, a.sv.t, i * KT, kmax, Vt[slot], wave);
         },
         [&](int i, auto slot) __attribute__((always_inline)) { use(i, Kt[slot], Vt[slot]); });
   } else {
@@ -199,12 +199,12 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DV <= 128 ? 2 : 1)) voi
     Stage<E, KT, MAPS, D, THREADS, kWhole> ks(a.d, tid);
     Stage<E, KT, 1, DV, THREADS, kWhole> vs(a.dv, tid);
     auto load = [&](int i) {
-      ks.load(k, a.sk.t, i * KT, len, a.d);
-      vs.load(v, a.sv.t, i * KT, len, a.dv);
+      ks.load(k, a.sk.t, i * KT, kmax, a.d);
+      vs.load(v, a.sv.t, i * KT, kmax, a.dv);
     };
     auto store = [&](int i, int slot) {
-      ks.store(slot ? K1 : K0, i * KT, len);
-      vs.store(slot ? V1 : V0, i * KT, len);
+      ks.store(slot ? K1 : K0, i * KT, kmax);
+      vs.store(slot ? V1 : V0, i * KT, kmax);
     };
     if (first < last) {
       load(first);
