@@ -57,7 +57,7 @@ ARCH = "gfx950"
 # around the VALU work on accumulators (decay masks, state scaling).
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang",
           "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form=true", f"-I{INCLUDE}", f"-I{CSRC}", "-Wall",
-          "-Wno-unused-function", "-Wno-inline-asm"]
+          "-Wno-unused-function"]
 
 
 def _hipcc() -> str:

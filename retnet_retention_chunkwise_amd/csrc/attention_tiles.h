@@ -209,6 +209,8 @@ struct Stage {
 // for them to arrive in front of the next read of any tile; the wait is in
 // dma_barrier().  m0 holds the LDS address; the wait states cover m0, and the
 // pointer where it comes out of a vector register.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0, named as clobbered, is reserved
 template <int BYTES>
 __device__ __forceinline__ void load_to_lds(const void* p, unsigned off, const void* tile) {
   static_assert(BYTES == 16 || BYTES == 4, "a piece or a word");
@@ -219,6 +221,7 @@ __device__ __forceinline__ void load_to_lds(const void* p, unsigned off, const v
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(p) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // ROWS rows of MAPS parts of d elements (16-byte pieces at 16-byte addresses),
 // straight into a swizzled tile of MAPS D elements a row, by NW waves.  A wave's
