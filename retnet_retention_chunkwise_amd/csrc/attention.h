@@ -10,6 +10,9 @@ namespace ret {
 
 constexpr int kAttnMaxDk = 256;  // channels of q and k, all maps together
 constexpr int kAttnMaxDv = 256;
+// Elements between tokens of a whole sequence's tensors that are read in tiles: a
+// tile's rows are addressed in 32 bits from its first.
+constexpr long kMaxTokenStride = 1L << 24;
 
 struct AttnFwd {
   const void* q;
@@ -124,8 +127,7 @@ template <typename E>
 hipError_t launch_bwd_q(const AttnBwd& a, float* stats, float* lam_part, float* part, int shares, hipStream_t s);
 template <typename E>
 int bwd_rows(const AttnFwd& a);  // rows of a workgroup
-template <typename E>
-int bwd_keys(const AttnFwd& a);  // keys of a workgroup
+constexpr int kBwdKeys = 64;     // keys of a workgroup, of any size and type
 // shares > 1: every share of the rows leaves its sums in part
 template <typename E>
 hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, float* part, int shares, hipStream_t s);

@@ -8,7 +8,6 @@ namespace {
 
 constexpr int kMaxLen = 1 << 30;               // tokens, and the offset's magnitude
 constexpr long long kMaxAttnRows = 1LL << 25;  // rows of q: a wave each, below 2^32 threads in all
-constexpr long kMaxTokenStride = 1L << 24;
 constexpr long long kMaxTiles = 1LL << 23;     // workgroups of 256 threads
 // Scales: the kernels form scale log2 e and 8 / (scale log2 e), which leave fp32 below
 // 1.6e-38 and above 2.3e38 (the running maximum then never moves, or every score is NaN).
@@ -62,10 +61,10 @@ ret_status check_scores(const char* fn, float scale, int offset) {
   return RET_OK;
 }
 
-// Distances between tokens: a tile of 64 rows is addressed in 32 bits.
+// Distances between tokens of tensors that are read in tiles.
 ret_status check_token_strides(const char* fn, std::initializer_list<std::pair<const Strides3*, int>> all) {
   for (const auto& x : all)
-    if (x.second > 1 && x.first->t > kMaxTokenStride)
+    if (x.second > 1 && x.first->t > ret::kMaxTokenStride)
       return fail(RET_ERR_UNSUPPORTED, "%s: a distance of %ld elements between tokens exceeds 2^24", fn, x.first->t);
   return RET_OK;
 }

@@ -594,9 +594,9 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (kWhole || DK + DV <= 2
   }
 }
 
-template <typename E, int DK>
 struct KvShape {
   static constexpr int NB = 1, NW = 4, TILE = 16 * NB * NW, STREAM = 32;
+  static_assert(TILE == kBwdKeys, "keys of a workgroup");
 };
 template <typename E, int DK, int DV>
 struct BwdShape {
@@ -604,10 +604,6 @@ struct BwdShape {
   static constexpr int NW = 4, TILE = 16 * NB * NW, STREAM = 32;
 };
 
-template <typename E>
-int bwd_keys(const AttnFwd& a) {
-  return with_sizes(a, [](auto, auto dk, auto, auto) { return KvShape<E, decltype(dk)::value>::TILE; });
-}
 template <typename E>
 int bwd_rows(const AttnFwd& a) {
   return with_sizes(a, [](auto, auto dk, auto dv, auto) { return BwdShape<E, decltype(dk)::value, decltype(dv)::value>::TILE; });
@@ -632,7 +628,7 @@ hipError_t launch_bwd_kv(const AttnBwd& a, const float* stats, float* part, int 
   return with_sizes(a.f, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
     constexpr bool W = decltype(whole)::value;
-    typedef KvShape<E, DK> C;
+    typedef KvShape C;
     const int tiles = (a.f.S + C::TILE - 1) / C::TILE;
     hipLaunchKernelGGL((attention_bwd_kv_kernel<E, M, DK, DV, W, C::NB, C::NW, C::STREAM>),
                        dim3(static_cast<unsigned>(tiles) * a.f.B * a.f.Hk * shares), dim3(64 * C::NW), 0, s, a,

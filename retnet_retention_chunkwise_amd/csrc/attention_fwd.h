@@ -271,7 +271,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && DV <= 128 ? 2 : 1)) voi
   }
 }
 
-template <typename E, int MAPS, int DK, int DV>
+template <typename E, int DK, int DV>
 struct FwdShape {
   static constexpr int NB = sizeof(E) == 2 && DK <= 128 && DV <= 128 ? 2 : 1;
   static constexpr int NW = 4, KT = 32, QT = 16 * NB * NW;
@@ -280,9 +280,7 @@ struct FwdShape {
 // Rows of a tile, for the sizes that hold the call's.
 template <typename E>
 int fwd_rows(const AttnFwd& a) {
-  return with_sizes(a, [](auto m, auto dk, auto dv, auto) {
-    return FwdShape<E, decltype(m)::value, decltype(dk)::value, decltype(dv)::value>::QT;
-  });
+  return with_sizes(a, [](auto, auto dk, auto dv, auto) { return FwdShape<E, decltype(dk)::value, decltype(dv)::value>::QT; });
 }
 
 template <typename E>
@@ -290,7 +288,7 @@ hipError_t launch_fwd(const AttnFwd& a, const Partial& part, hipStream_t s) {
   return with_sizes(a, [&](auto m, auto dk, auto dv, auto whole) {
     constexpr int M = decltype(m)::value, DK = decltype(dk)::value, DV = decltype(dv)::value;
     constexpr bool W = decltype(whole)::value;
-    typedef FwdShape<E, M, DK, DV> C;
+    typedef FwdShape<E, DK, DV> C;
     const int tiles = (a.T + C::QT - 1) / C::QT;
     hipLaunchKernelGGL((attention_fwd_kernel<E, M, DK, DV, W, C::NB, C::NW, C::KT>),
                        dim3(static_cast<unsigned>(tiles) * a.B * a.H, part.nsplit), dim3(64 * C::NW), 0, s, a, part,

@@ -279,8 +279,7 @@ int lam_rows(const AttnFwd& a) {  // workgroups of the q pass, of a head
 constexpr int kShareTarget = 1024, kShareRows = 128;
 
 int kv_shares(const AttnFwd& a, bool causal) {
-  const int keys = a.dt ? bwd_keys<uint16_t>(a) : bwd_keys<float>(a);
-  const long wgs = static_cast<long>((a.S + keys - 1) / keys) * a.B * a.Hk, rows = static_cast<long>(a.H / a.Hk) * a.T;
+  const long wgs = static_cast<long>((a.S + kBwdKeys - 1) / kBwdKeys) * a.B * a.Hk, rows = static_cast<long>(a.H / a.Hk) * a.T;
   const long target = causal ? kShareTarget : kShareTarget / 2;
   if (wgs == 0 || wgs >= target || rows < 2 * kShareRows) return 1;
   const long want = (target + wgs - 1) / wgs, most = rows / kShareRows;

@@ -17,6 +17,7 @@
 
 #include <type_traits>
 
+#include "attention.h"
 #include "common.h"
 #include "gfx950.h"
 #include "vec_io.h"
@@ -163,9 +164,9 @@ struct Stage {
   static constexpr int CE = 16 / static_cast<int>(sizeof(E));
   static constexpr int CH = MAPS * D / CE;               // pieces of a row
   static constexpr int STEP = THREADS / CH;              // rows of one round
-  static constexpr int N = STEP > ROWS ? 1 : ROWS / STEP;  // rounds
-  static_assert(THREADS % CH == 0 && (STEP > ROWS || ROWS % STEP == 0),
-                "a thread stays in its columns, rounds are full or one round has threads to spare");
+  static constexpr int N = ROWS / STEP;                  // rounds
+  static_assert(THREADS % CH == 0 && ROWS % STEP == 0, "a thread stays in its columns, rounds are full");
+  static_assert(ROWS * kMaxTokenStride * sizeof(E) <= 1UL << 32, "a place in the tile has 32 bits");
   u32x4 r[N];
   Piece16<E, kWhole> piece;
   int row, col;  // of the thread's first piece in the tile
@@ -176,14 +177,14 @@ struct Stage {
         col(tid % CH * CE),
         part(MAPS > 1 ? tid % CH / (D / CE) * d : 0) {}
 
-  // Rows row0.. of base, stride (below 2^24 elements) apart; n > 0 rows are
+  // Rows row0.. of base, stride (at most kMaxTokenStride) apart; n > row0 rows are
   // readable.  A tile's address is uniform, a thread's place in it 32 bits.
   __device__ __forceinline__ void load(const E* base, long stride, int row0, int n, int d) {
     const char* p = reinterpret_cast<const char*>(base + row0 * stride);
     const unsigned step = static_cast<unsigned>(stride) * sizeof(E);
     unsigned at[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) at[i] = (STEP > ROWS ? min(row, ROWS - 1) : row + i * STEP) * step;
+    for (int i = 0; i < N; ++i) at[i] = (row + i * STEP) * step;
     if (row0 + ROWS > n) {
 #pragma unroll
       for (int i = 0; i < N; ++i) at[i] = min(row + i * STEP, n - 1 - row0) * step;
@@ -197,7 +198,6 @@ struct Stage {
       for (int i = 0; i < N; ++i)
         if (row0 + row + i * STEP >= n) r[i] = u32x4{0, 0, 0, 0};
     }
-    if (STEP > ROWS && row >= ROWS) return;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       *reinterpret_cast<u32x4*>(tile + (row + i * STEP) * Tile<E, MAPS * D, false>::LD + col) = piece.finish(r[i]);
@@ -233,6 +233,7 @@ struct Dma {
   typedef Tile<uint16_t, MAPS * D, true> T;
   static constexpr int COUNT = ROWS * T::PIECES / 64 / NW, STEP = NW * 64 / T::PIECES;  // rows of one round
   static_assert(COUNT >= 1 && COUNT * NW * 64 == ROWS * T::PIECES, "every wave has as many loads");
+  static_assert(ROWS * kMaxTokenStride * 2 <= 1L << 32, "a place in the tile has 32 bits");
   int row;
   unsigned piece[COUNT];  // bytes in front of the lane's pieces in their rows
   __device__ __forceinline__ Dma(int d, int wave, int lane) : row((wave * 64 + lane) / T::PIECES) {
