@@ -107,6 +107,10 @@ struct Partial {
   float* ml;
   int nsplit;
 };
+// Shares that so many keys need at least: a sum of weights grows by one key at a
+// time in each of four lanes (the step: 16), and stands still at 2^24 equal ones.
+constexpr int kMaxRange = 1 << 24;
+inline int least_ranges(long keys) { return keys > kMaxRange ? static_cast<int>((keys + kMaxRange - 1) / kMaxRange) : 1; }
 inline size_t partial_floats(long rows, int maps, int dv, int nsplit) {
   return nsplit > 1 ? static_cast<size_t>(nsplit) * rows * maps * (((dv + 3) & ~3) + 4) : 0;  // ml in 16 bytes
 }

@@ -229,6 +229,8 @@ hipError_t stats(const AttnBwd& g, float* to, hipStream_t s) {
   return stats_by_width<E, 64>(g, to, s);
 }
 
+long rows_of(const AttnFwd& a) { return static_cast<long>(a.B) * a.H * a.T; }
+
 template <typename E, int WPR>
 hipError_t join_by(const AttnFwd& a, const Partial& p, hipStream_t s) {
   const long rows = static_cast<long>(a.B) * a.H * a.T, per = kWaves / WPR;
@@ -239,10 +241,9 @@ hipError_t join_by(const AttnFwd& a, const Partial& p, hipStream_t s) {
 template <typename E>
 hipError_t join(const AttnFwd& a, const Partial& p, hipStream_t s) {
   // one wave reads a row's few shares as fast as four, which then wait for each other
-  return p.nsplit > 8 ? join_by<E, kWaves>(a, p, s) : join_by<E, 1>(a, p, s);
+  // (and a workgroup for each of very many rows would be more than a launch takes)
+  return p.nsplit > 8 && rows_of(a) < 1 << 23 ? join_by<E, kWaves>(a, p, s) : join_by<E, 1>(a, p, s);
 }
-
-long rows_of(const AttnFwd& a) { return static_cast<long>(a.B) * a.H * a.T; }
 
 // Keys are split where the tiles of rows alone are too few to fill the device's
 // 256 compute units, into ranges of at least kRange keys, so that about
@@ -259,7 +260,9 @@ int key_ranges(const AttnFwd& a, int rows) {  // for tiles of so many rows
   const long want = kSplitTarget / wgs, most = a.S / kRange;
   return static_cast<int>(want < most ? want : most);
 }
-int fwd_splits(const AttnFwd& a) { return key_ranges(a, a.dt ? fwd_rows<uint16_t>(a) : fwd_rows<float>(a)); }
+int fwd_splits(const AttnFwd& a) {
+  return std::max(key_ranges(a, a.dt ? fwd_rows<uint16_t>(a) : fwd_rows<float>(a)), least_ranges(a.S));
+}
 int q_shares(const AttnFwd& a) { return key_ranges(a, a.dt ? bwd_rows<uint16_t>(a) : bwd_rows<float>(a)); }
 size_t q_floats(const AttnFwd& a) {
   const int n = q_shares(a);

@@ -16,6 +16,8 @@
 // join.  Few short streams are bound by latency: 8 of 8 over 512, 11 us.
 #include "attention.h"
 
+#include <algorithm>
+
 #include "attention_tiles.h"
 
 namespace ret {
@@ -358,9 +360,10 @@ constexpr int kStepTarget = 1024;
 int step_splits(const AttnStep& a) {
   const int blocks = (a.H / a.Hk + 15) / 16, range = a.dt ? 512 : 256;
   const long wgs = static_cast<long>(a.B) * a.Hk * blocks, keys = static_cast<long>(a.max_pages) * a.page;
-  if (wgs >= kStepTarget / 2 || keys < 2 * range) return 1;
+  const int least = least_ranges(keys);
+  if (wgs >= kStepTarget / 2 || keys < 2 * range) return least;
   const long want = kStepTarget / wgs, most = keys / range;
-  return static_cast<int>(want < most ? want : most);
+  return std::max(least, static_cast<int>(want < most ? want : most));
 }
 
 template <typename E>
