@@ -61,9 +61,13 @@ struct Mma<float> {
 //     at 120, with none at 32 and 64.
 //   swizzled (kDma true, bf16): rows without a gap, as loads straight into LDS
 //     leave them, and the row's 16-byte pieces in another order: piece c of row r
-//     lies at place c ^ turn(r).  turn gives 16 rows 16 places (pairs of rows of 8
-//     pieces: 8 each), and eight neighbouring rows different pairs of places, so
-//     both kinds of reads meet every bank once, as in the padded layout.
+//     lies at place c ^ turn(r), turn even.  Transposing reads take two pieces of
+//     eight neighbouring rows at a time, which turn puts into different pairs of
+//     places.  16-byte reads take one piece of rows 0-3 and 12-15 and the next of
+//     rows 4-11 (then the other way round): rows that share a turn are of different
+//     sets, and meet different places of their pair.  So both meet every bank once
+//     (no conflicts counted; rows at 247 bytes a clock and compute unit, columns at
+//     204; with turns that differ in all 16 rows the rows ran at 127).
 template <typename E, int DIM, bool kDma>
 struct Tile {
   static constexpr int LD = DIM + (kDma ? 0 : sizeof(E) == 2 ? 16 : 4);
@@ -71,7 +75,7 @@ struct Tile {
   static_assert(!kDma || sizeof(E) == 2, "the swizzled layout is of bf16 rows");
   static_assert(PIECES >= 8 && (PIECES & (PIECES - 1)) == 0, "a power of two of pieces");
   __device__ __forceinline__ static int turn(int row) {
-    return PIECES >= 16 ? (row & 7) << 1 | (row >> 3 & 1) : (row >> 1 & 3) << 1 | (row >> 3 & 1);
+    return PIECES >= 16 ? (row & 7) << 1 : (row >> 1 & 3) << 1;
   }
 
   // A[row][channels] of row row0 + lane % 16: bf16 the eight channels from c0 + 8 (lane / 16),
