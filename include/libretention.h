@@ -467,6 +467,8 @@ size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D);
  * in whole sequences, tokens of k and v (backward: of q and grad_o too) at most
  * 2^24 elements apart.  Any alignment of rows; bf16 rows that start at multiples
  * of 16 bytes, with d (dk / maps) and dv multiples of 8, are read the fastest way.
+ * Scores have to stay below 2^30 in magnitude, and a value times 2^8 times the number
+ * of keys within fp32's range: sums are divided at the end, and weights up to 2^8 there.
  * No sum depends on timing: the same call gives the same bits.
  */
 
@@ -489,8 +491,9 @@ size_t retention_residual_norm_bwd_workspace_bytes(int rows, int D);
  *             other argument; contents ignored on entry.  Calls that overlap in
  *             time need workspaces of their own.
  * An element that is not finite makes the results of the rows that see it NaN
- * or what the formula says; a value row that is not finite may also reach rows
- * before it.
+ * or what the formula says (a row whose scores are all -inf counts as one that
+ * sees no key); a value row that is not finite, and in the backward any row, may
+ * also reach results fewer than 64 tokens away that do not meet it.
  */
 ret_status retention_attention_fwd(const void* q, const void* k, const void* v, const float* lam, const int* lens,
                                    void* o, float* lse, void* second, const ret_strides* strides, int B, int H, int Hk,
@@ -511,8 +514,12 @@ size_t retention_attention_workspace_bytes(int B, int H, int Hk, int T, int S, i
  *   strides : q, k, v, o, grad_o, grad_q, grad_k, grad_v.
  *   workspace : retention_attention_bwd_workspace_bytes() bytes, as above.
  * A row's mean of d L / d A under its weights, which the softmax's gradient
- * subtracts, comes from o and second as they were rounded, and for rows of at
- * most 32 keys (where it matters most) from the weights themselves.
+ * subtracts, comes from o and second as they were rounded; for bf16 rows of at
+ * most 32 keys it comes from the weights themselves.  Longer bf16 rows lose by it
+ * where few keys carry them (64 channels of unit inputs: grad_q is off by 0.0024
+ * of itself with the exact mean, by 0.0027, 0.0032 and 0.0038 where 9, 3 and 2
+ * keys carry the row), and rows that one key carries alone have little of their
+ * (small) gradient left.
  */
 ret_status retention_attention_bwd(const void* q, const void* k, const void* v, const float* lam, const int* lens,
                                    const void* o, const float* lse, const void* second, const void* grad_o,
@@ -559,7 +566,8 @@ size_t retention_attention_step_workspace_bytes(int B, int H, int Hk, int dk, in
  *   counts  : nullable (T); device int [B], tokens to store.
  *   strides : k, v, k_cache, v_cache.
  * Tokens whose page is not there, and those behind max_pages * page, are left
- * out; all else in the cache stays as it was.  Limits as above with T for S.
+ * out; all else in the cache stays as it was.  No two tokens may have the same
+ * place.  Limits as above with T for S.
  */
 ret_status retention_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, const int* table,
                                   const int* start, const int* counts, const ret_strides* strides, int B, int Hk,

@@ -24,11 +24,14 @@
 // and 0.0038 where 9, 3 and 2 keys carry the row; where one key does and the
 // others weigh e^-12 of it, what little is left is off by a quarter and more.
 //
-// Bound as the forward is; B2 H16/4 T4096 d128 two maps causal: q pass 240 us,
-// kv pass 350 (0.28 TFLOP executed), rows 26.  The kv pass holds 16 keys a wave:
+// Bound as the forward is; B2 H16/4 T4096 d128 two maps causal: q pass 257 us,
+// kv pass 373 (0.28 TFLOP executed), rows 28.  The kv pass holds 16 keys a wave:
 // with 32 the accumulators spill, with a third wave a SIMD they do too (1440 us for
-// the whole pass in place of 924).  Its operands are read a stage ahead, which
-// the compiler would undo without barriers (918 us, 831 with).
+// the whole training pass in place of 924, when measured).  Its operands are read a
+// stage ahead, which the compiler would undo without barriers (918 us, 831 with).
+// With two maps it reads its head's weight once a tile, behind that tile's loads,
+// and waits for all of them with it: a tile is on its way for less than the tile's
+// time before it that three slots would allow.
 #pragma once
 
 #include "attention.h"
@@ -285,8 +288,10 @@ __global__ __launch_bounds__(64 * NW, (sizeof(E) == 2 && (kWhole || DK + DV <= 2
   typedef Tile<E, DV, kDma> GTile;
   // Operands are read a stage ahead, except beside the sums of wide rows, which
   // leave registers for that or for a second wave on the SIMD: the wave gains more
-  // (B2 H8 T2000 one map d256: training pass 308 us, reading ahead 370).  Rows that
-  // are not whole spill then (T1500 250 and 201 channels: 424 us, reading ahead 401).
+  // (B2 H8 T2000 one map d256: training pass 308 us, reading ahead 370), though most
+  // of these kernels then spill 2 to 11 registers, and what is read back in the loop
+  // waits for the loads under way.  Rows that are not whole spill more, and lose by it
+  // (T1500 250 and 201 channels: 424 us, reading ahead 401).
   constexpr bool kAhead = sizeof(E) == 2 && (!kWhole || DK + DV <= 256);
   __shared__ __attribute__((aligned(16))) E Q0[QT * QTile::LD], Q1[QT * QTile::LD], Q2[kDma && SLOTS == 3 ? QT * DK : 16];
   __shared__ __attribute__((aligned(16))) E G0[QT * GTile::LD], G1[QT * GTile::LD], G2[kDma && SLOTS == 3 ? QT * DV : 16];

@@ -10,8 +10,9 @@
 //                              registers, rounded to the tensors' type)
 // so a row's scores lie in one lane group's registers and its maximum takes
 // two lane swaps.  One pass with a running maximum and sum; the maximum is only
-// moved (and O scaled) when a score exceeds it by 2^kSlack, which no bf16 or
-// fp32 value notices: p is then at most 2^kSlack instead of 1.  Both maps read
+// moved (and O scaled) when a score exceeds it by 2^kSlack: p is then at most
+// 2^kSlack instead of 1, which takes as much from the range of the sums and
+// nothing from their precision.  Both maps read
 // the same value tile once and keep an output each, because they are divided by
 // different sums.  Products are bf16 MFMA (fp32: fp32 MFMA); scores, maxima,
 // sums and outputs are fp32; p is rounded to bf16 as an operand, which costs as
@@ -19,11 +20,15 @@
 //
 // 32 rows a wave (bf16, up to 128 channels): a tile's operands are read from LDS
 // once for twice the products.  Wider rows leave room for one such wave a SIMD; 16
-// rows and two waves are faster (B4 H8 T2048 one map d256: 101 us, with 32 rows 126).
-// Bound by matrix and vector instructions, which do not overlap between a SIMD's
-// two waves: about 24 clocks of products and 31 of softmax a score at 128 channels
-// and two maps, 91% of the time.  B1 H16/4 T8192 d128 two maps causal: 414 us (1.0
-// PFLOP/s of visible pairs); B4 H8 T2048 d256: 123 us (0.84).
+// rows and two waves are faster (B4 H8 T2048 one map d256: 126 us to 101 when that
+// was chosen, 96 now).
+// Bound by matrix and vector instructions: a wave does a tile's scores, softmax and
+// sums one after the other, and two waves of a SIMD make up for little of that (16
+// products of one, 349 clocks, and 32 exponentials of the other, 413, take 617
+// together; 16 products with 48 vector instructions in between 453).  About 24 clocks
+// of products and 31 of softmax a score at 128 channels and two maps.  B1 H16/4 T8192
+// d128 two maps causal: 411 us (1.0 PFLOP/s of visible pairs); B4 H8 T2048 d256: 117
+// us (0.88).
 #pragma once
 
 #include "attention.h"

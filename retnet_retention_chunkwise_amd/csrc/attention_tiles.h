@@ -122,8 +122,11 @@ struct Tile {
 // kWhole: rows end with a piece (n a multiple of CE); a piece behind the row
 // reads the row's last.  Otherwise a piece that the row ends in is read so far
 // back that it ends with the row, and shifted when it is used, with zeros behind
-// the row.  No lane leaves the others.  What a whole row's padding holds is
-// left: it meets zeros in the other operand or fills outputs that are not stored.
+// the row.  No lane leaves the others: with a branch for the lanes of a row's end,
+// masks were spilled and the compiler placed a copy of an address in front of the
+// instruction that gave the lanes back, which sent stores anywhere.  What a whole
+// row's padding holds is left: it meets zeros in the other operand or fills outputs
+// that are not stored.
 template <typename E, bool kWhole>
 struct Piece16 {
   static constexpr int CE = 16 / static_cast<int>(sizeof(E));
